@@ -228,6 +228,143 @@ enum topk_reduce_op { TOPK_REDUCE_SUM = 0, TOPK_REDUCE_MAX = 1, TOPK_REDUCE_MIN 
 int topk_reduce_i32(const int32_t* in, size_t n, int op, int64_t* out, struct CUstream_st* stream);
 int topk_reduce_f32(const float* in, size_t n, int op, double* out, struct CUstream_st* stream);
 
+/*
+ * A paged key-value cache with TopK eviction: topk_kv_append, topk_kv_attend
+ * and topk_kv_evict.  The TopK page (section 6) keys a selection by a score
+ * that carries an item; here the items are a decoder's cached keys and
+ * values, and the score is the attention each one has received.
+ *
+ * A pool holds `pages` pages of `page_size` slots; every slot holds, for each
+ * of `heads` heads, a key and a value of `dim` 16-bit elements.  Row b of
+ * `table` names the pages of sequence b in order: its slot s is slot
+ * s % page_size of page table[b][s / page_size].  lens[b] is the number of
+ * slots that sequence b holds (the same for every head; which tokens they
+ * hold may differ by head after an eviction).  Two sequences may name the
+ * same page only while neither is appended to or evicted from there.
+ *
+ *   k, v      the pools: element (page, slot, head, i) lies at
+ *             page * stride[0] + slot * stride[1] + head * stride[2] + i.
+ *             16-byte aligned; strides are positive multiples of 8.
+ *   dtype     TOPK_KV_F16 or TOPK_KV_BF16, of the pools and of every query,
+ *             output, and new key or value.
+ *   page_size a multiple of 8, at most 65536; dim a multiple of 8, at most 256.
+ *   table     int32, rows of table_width entries table_stride apart;
+ *             table_width * page_size (a sequence's capacity) is below 2^30.
+ *             Entries past a sequence's slots are not read.  An entry
+ *             outside [0, pages) is never followed: appends and moves to or
+ *             from it are dropped, and its slots are attended to as zeros.
+ *   lens      int32[seqs]; a length below 0 counts as 0, one above the
+ *             capacity as the capacity.
+ *
+ * topk_kv_rows is a per-slot side array [seqs, heads, slots]: element
+ * (b, h, s) lies at b * seq_stride + h * head_stride + s.
+ *
+ * All pointers are device memory (TOPK_ERR_INVALID_ARG for host memory) and
+ * the calls only enqueue.  Nothing here uses atomics on results: equal inputs
+ * give equal outputs, bit for bit, on the same device.
+ */
+enum topk_kv_dtype { TOPK_KV_F16 = 0, TOPK_KV_BF16 = 1 };
+
+/* Largest dim of a cache. */
+#define TOPK_KV_MAX_DIM 256
+
+struct topk_kv_cache {
+    void* k;
+    void* v;
+    int dtype;
+    int pages, page_size, heads, dim;
+    int64_t k_stride[3], v_stride[3]; /* page, slot, head */
+    const int32_t* table;
+    int64_t table_stride;
+    int table_width;
+    int seqs;
+    const int32_t* lens;
+};
+
+struct topk_kv_rows {
+    void* data; /* null: absent */
+    int64_t seq_stride, head_stride;
+    int slots;
+};
+
+/*
+ * topk_kv_append -- write new keys and values behind what each sequence
+ * holds.  Token i of sequence b (i counts from 0) goes to slot lens[b] + i of
+ * every head; lens is not changed.
+ *
+ *   k_new, v_new  token t, head h at t * stride[0] + h * stride[1]; 16-byte
+ *                 aligned, strides multiples of 8.
+ *   tokens        number of tokens in k_new; 0 does nothing.
+ *   starts        int32[seqs + 1]: sequence b's tokens are [starts[b],
+ *                 starts[b + 1]), ascending from 0; null: one token each
+ *                 (tokens == seqs).  Tokens from starts[seqs] on are ignored.
+ *   weight        float32 rows or absent: the new slots get 0.
+ *   pos, next_pos int32 rows and int32[seqs], both or neither: the new slots
+ *                 get next_pos[b] + i.
+ *
+ * Tokens beyond the sequence's capacity are dropped.  One launch.
+ */
+int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const int64_t* k_new_stride,
+                   const void* v_new, const int64_t* v_new_stride, int tokens, const int32_t* starts,
+                   const struct topk_kv_rows* weight, const struct topk_kv_rows* pos, const int32_t* next_pos,
+                   struct CUstream_st* stream);
+
+/*
+ * topk_kv_attend -- attention of one new token per sequence over its slots,
+ * and the attention each slot gets.  Query head j reads key-value head
+ * j / (q_heads / heads).  With s_t = scale * q . k_t over t < lens[b] and
+ * p = softmax(s):
+ *   out[b][j] = sum_t p_t v_t,  lse[b][j] = log sum_t exp(s_t),
+ *   weight_out[b][h][t] = weight[b][h][t] + the sum of p_t over the query
+ *   heads of h, for t < lens[b] (other entries are not touched).
+ * A sequence without slots, or whose every score is -inf, gives out = 0,
+ * lse = -inf and leaves its weights' values as they are.  A NaN or +inf
+ * score makes its head's out, lse and shares NaN; a value that is not finite
+ * makes its element of out not finite.
+ *
+ *   q           (sequence, query head) at b * stride[0] + j * stride[1];
+ *               16-byte aligned, strides multiples of 8.
+ *   q_heads     a multiple of heads.
+ *   scale       finite.
+ *   out         contiguous [seqs, q_heads, dim], 16-byte aligned.
+ *   lse         contiguous float32 [seqs, q_heads], natural logarithm, or null.
+ *   weight, weight_out
+ *               float32 rows with at least a sequence's capacity of slots,
+ *               both or neither; the same array, or not overlapping.
+ *
+ * Products, sums and softmax statistics are float32.
+ */
+int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64_t* q_stride, int q_heads, float scale,
+                   void* out, float* lse, const struct topk_kv_rows* weight, const struct topk_kv_rows* weight_out,
+                   struct CUstream_st* stream);
+
+/*
+ * topk_kv_evict -- keep, per sequence and head, the `budget` slots with the
+ * largest weight, and move them below slot `budget`.  Sequences with at most
+ * `budget` slots keep everything.
+ *
+ * Order: protected slots first, then by weight descending (topk_rows_f32's
+ * order: NaN above +inf, -0 equal to +0), the lower slot among equals.  A
+ * slot is protected when pos < sink or pos >= next_pos[b] - recent.
+ * A kept slot below `budget` stays where it is; the kept slots at or above
+ * it, in ascending order, fill the slots below it that were not kept, in
+ * ascending order.  Keys, values, weights and positions move alike; slots at
+ * or above `budget` are left as they are in the pools (their pages can be
+ * reused).  Attention does not depend on the order of slots, so only the kept
+ * tail is moved, in place.
+ *
+ *   weight, pos          rows with at least a sequence's capacity of slots.
+ *   next_pos             int32[seqs]: the position after the newest token.
+ *   budget >= 1; sink, recent >= 0; sink + recent <= budget.
+ *   weight_out, pos_out  rows of at least min(budget, capacity) slots: the
+ *                        same arrays as weight and pos, or not overlapping.
+ *   lens_out             int32[seqs]: min(lens, budget); may be lens itself.
+ */
+int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* weight,
+                  const struct topk_kv_rows* pos, const int32_t* next_pos, int budget, int sink, int recent,
+                  const struct topk_kv_rows* weight_out, const struct topk_kv_rows* pos_out, int32_t* lens_out,
+                  struct CUstream_st* stream);
+
 /* Bytes of the device array that topk_i32_noalloc uses as scratch. */
 #define TOPK_NOALLOC_SCRATCH_BYTES (1u << 20)
 

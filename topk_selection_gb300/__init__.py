@@ -8,8 +8,11 @@ not been built, importing the binding raises.
     topk_i32(x, k)          -> int32 tensor [k], the k largest values, descending
     topk_rows_f32(x, k)     -> (float32 [rows, k], int32 [rows, k]) per-row best
                                values and their columns; lower column wins ties
+    kv_append, kv_attend, kv_evict
+                            -> a decoder's paged key-value cache: append, attend
+                               with accumulated weights, keep the best slots
 
-Both accept CUDA tensors (asynchronous on the current stream) or CPU tensors
+The first two accept CUDA tensors (asynchronous on the current stream) or CPU tensors
 (the library stages them through device memory and returns when done).
 """
 from __future__ import annotations
@@ -25,11 +28,12 @@ __all__ = ["topk_i32", "topk_rows_f32", "topk_i32_ptr", "topk_rows_f32_ptr", "To
            "status_string", "release_workspace", "launch_count", "last_cuda_error", "library_path",
            "check_stream", "set_option", "OPT_STAGE2_CAP", "OPT_RADIX_CAP", "OPT_RADIX_SAMPLE_RANK",
            "reduce", "reduce_ptr", "REDUCE_OPS", "topk_items_f32", "topk_items_f32_ptr", "sort_u32",
-           "sort_u32_ptr"]
+           "sort_u32_ptr", "kv_append", "kv_attend", "kv_evict", "KV_MAX_DIM"]
 
 MAX_K = 131072      # topk_i32, topk_u32, topk_f32
 NOALLOC_MAX_K = 32768  # topk_i32_noalloc
 MAX_K_ROWS = 1024   # topk_rows_f32
+KV_MAX_DIM = 256    # kv_append, kv_attend, kv_evict
 (TOPK_OK, TOPK_ERR_INVALID_ARG, TOPK_ERR_UNSUPPORTED, TOPK_ERR_NO_MEMORY, TOPK_ERR_CUDA,
  TOPK_ERR_DEVICE_TIMEOUT) = range(6)
 
@@ -42,6 +46,21 @@ class TopKError(RuntimeError):
 
 def library_path() -> str:
     return _build.LIB_PATH
+
+
+class _KvCache(ctypes.Structure):
+    """struct topk_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int), ("seqs", ctypes.c_int),
+                ("lens", ctypes.c_void_p)]
+
+
+class _KvRows(ctypes.Structure):
+    """struct topk_kv_rows."""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slots", ctypes.c_int)]
 
 
 def _load():
@@ -78,6 +97,12 @@ def _load():
     lib.topk_u32.restype = ci
     lib.topk_f32.argtypes = [vp, sz, ci, vp, vp]
     lib.topk_f32.restype = ci
+    lib.topk_kv_append.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, vp, vp, vp]
+    lib.topk_kv_append.restype = ci
+    lib.topk_kv_attend.argtypes = [vp, vp, vp, ci, ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.topk_kv_attend.restype = ci
+    lib.topk_kv_evict.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, vp]
+    lib.topk_kv_evict.restype = ci
     lib.topk_last_launch_early.argtypes = []
     lib.topk_last_launch_early.restype = ci
     return lib
@@ -348,6 +373,171 @@ def reduce(x: torch.Tensor, op: str, out: torch.Tensor | None = None, stream=Non
     if rc != TOPK_OK:
         raise TopKError(rc, "topk_reduce_f32" if is_float else "topk_reduce_i32")
     return out
+
+
+_KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _kv_check(t, name, dtype, device, shape):
+    """A tensor of this dtype and device whose sizes are `shape` (None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
+                         f"got {tuple(t.shape)}")
+
+
+def _kv_strides(t, name, n):
+    """The strides of t's first n dimensions; its last must lie densely.  A
+    dimension of one element may have any stride in torch: the library gets
+    one that it accepts, which nothing is multiplied by."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return (ctypes.c_int64 * n)(*(8 if t.shape[i] == 1 else t.stride(i) for i in range(n)))
+
+
+def _kv_cache(k_pages, v_pages, table, lens):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _KV_DTYPES:
+        raise TypeError("k_pages must be a float16 or bfloat16 tensor")
+    if not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
+    dev = k_pages.device
+    _kv_check(k_pages, "k_pages", k_pages.dtype, dev, (None,) * 4)
+    _kv_check(v_pages, "v_pages", k_pages.dtype, dev, tuple(k_pages.shape))
+    _kv_check(table, "table", torch.int32, dev, (None, None))
+    _kv_check(lens, "lens", torch.int32, dev, (table.shape[0],))
+    if not lens.is_contiguous() or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("lens and the rows of table must be contiguous")
+    pages, page_size, heads, dim = k_pages.shape
+    seqs, width = table.shape
+    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _KV_DTYPES[k_pages.dtype], pages, page_size, heads, dim,
+                    _kv_strides(k_pages, "k_pages", 3), _kv_strides(v_pages, "v_pages", 3), table.data_ptr(),
+                    table.stride(0) if seqs > 1 else width, width, seqs, lens.data_ptr())
+
+
+def _kv_rows(t, name, dtype, k_pages, seqs):
+    if t is None:
+        return None
+    _kv_check(t, name, dtype, k_pages.device, (seqs, k_pages.shape[2], None))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return ctypes.byref(_KvRows(t.data_ptr(), t.stride(0), t.stride(1), t.shape[2]))
+
+
+def _kv_call(fn, name, device, stream, *args):
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream_handle(stream, device))
+    if rc != TOPK_OK:
+        raise TopKError(rc, name)
+
+
+def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+              k_new: torch.Tensor, v_new: torch.Tensor, starts: torch.Tensor | None = None,
+              weight: torch.Tensor | None = None, pos: torch.Tensor | None = None,
+              next_pos: torch.Tensor | None = None, stream=None) -> None:
+    """Write new tokens' keys and values into a paged cache, behind the lens[b]
+    slots that each sequence holds (topk_kv_append in include/topk.h).
+
+    k_pages, v_pages  [pages, page_size, heads, dim] float16 or bfloat16, any
+                      strides (head-major pools are transposed views)
+    table, lens       int32 [seqs, pages of a sequence], int32 [seqs]
+    k_new, v_new      [tokens, heads, dim]; sequence b's are rows starts[b] to
+                      starts[b + 1] (int32 [seqs + 1]), or row b without starts
+    weight            float32 [seqs, heads, slots]: 0 is written at the new slots
+    pos, next_pos     int32 [seqs, heads, slots] and [seqs]: next_pos[b] + i is
+                      written at the new slots
+
+    lens is not changed: add the tokens' numbers to it afterwards."""
+    cache = _kv_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    _kv_check(k_new, "k_new", k_pages.dtype, dev, (None, cache.heads, cache.dim))
+    _kv_check(v_new, "v_new", k_pages.dtype, dev, tuple(k_new.shape))
+    if (pos is None) != (next_pos is None):
+        raise ValueError("pos and next_pos come together")
+    for t, name, n in ((starts, "starts", cache.seqs + 1), (next_pos, "next_pos", cache.seqs)):
+        if t is not None:
+            _kv_check(t, name, torch.int32, dev, (n,))
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    if k_new.shape[0] == 0:
+        return
+    _kv_call(_lib.topk_kv_append, "topk_kv_append", dev, stream, ctypes.byref(cache), k_new.data_ptr(),
+             _kv_strides(k_new, "k_new", 2), v_new.data_ptr(), _kv_strides(v_new, "v_new", 2), k_new.shape[0],
+             None if starts is None else starts.data_ptr(),
+             _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
+             _kv_rows(pos, "pos", torch.int32, k_pages, cache.seqs),
+             None if next_pos is None else next_pos.data_ptr())
+
+
+def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+              scale: float | None = None, weight: torch.Tensor | None = None,
+              weight_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              lse: torch.Tensor | None = None, stream=None):
+    """Attention of one new token per sequence over a paged cache: (out [seqs,
+    q_heads, dim], lse float32 [seqs, q_heads]) -- topk_kv_attend in
+    include/topk.h.
+
+    q is [seqs, q_heads, dim], q_heads a multiple of the cache's heads; scale
+    defaults to dim ** -0.5.  With weight (float32 [seqs, heads, slots]), the
+    attention that each slot gets, summed over its query heads, is added to it
+    and written to weight_out (default: weight itself)."""
+    cache = _kv_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    _kv_check(q, "q", k_pages.dtype, dev, (cache.seqs, None, cache.dim))
+    q_heads = q.shape[1]
+    if out is None:
+        out = torch.empty((cache.seqs, q_heads, cache.dim), dtype=q.dtype, device=dev)
+    else:
+        _kv_check(out, "out", q.dtype, dev, tuple(q.shape))
+    if lse is None:
+        lse = torch.empty((cache.seqs, q_heads), dtype=torch.float32, device=dev)
+    else:
+        _kv_check(lse, "lse", torch.float32, dev, (cache.seqs, q_heads))
+    if not out.is_contiguous() or not lse.is_contiguous():
+        raise ValueError("out and lse must be contiguous")
+    if weight_out is None:
+        weight_out = weight
+    elif weight is None:
+        raise ValueError("weight_out needs weight")
+    _kv_call(_lib.topk_kv_attend, "topk_kv_attend", dev, stream, ctypes.byref(cache), q.data_ptr(),
+             _kv_strides(q, "q", 2), q_heads, cache.dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+             lse.data_ptr(), _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
+             _kv_rows(weight_out, "weight_out", torch.float32, k_pages, cache.seqs))
+    return out, lse
+
+
+def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+             weight: torch.Tensor, pos: torch.Tensor, next_pos: torch.Tensor, budget: int, sink: int = 0,
+             recent: int = 0, weight_out: torch.Tensor | None = None, pos_out: torch.Tensor | None = None,
+             lens_out: torch.Tensor | None = None, stream=None):
+    """Keep, per sequence and head, the `budget` slots with the largest weight
+    (and those with pos < sink or pos >= next_pos - recent), moving the kept
+    ones from above the budget into the places freed below it: (weight_out,
+    pos_out, lens_out), by default weight, pos and lens themselves, changed in
+    place -- topk_kv_evict in include/topk.h.  Pages past the first
+    ceil(budget / page_size) of a sequence can be reused afterwards."""
+    cache = _kv_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    weight_out = weight if weight_out is None else weight_out
+    pos_out = pos if pos_out is None else pos_out
+    lens_out = lens if lens_out is None else lens_out
+    for t, name in ((next_pos, "next_pos"), (lens_out, "lens_out")):
+        _kv_check(t, name, torch.int32, dev, (cache.seqs,))
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _kv_call(_lib.topk_kv_evict, "topk_kv_evict", dev, stream, ctypes.byref(cache),
+             _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
+             _kv_rows(pos, "pos", torch.int32, k_pages, cache.seqs), next_pos.data_ptr(), int(budget), int(sink),
+             int(recent), _kv_rows(weight_out, "weight_out", torch.float32, k_pages, cache.seqs),
+             _kv_rows(pos_out, "pos_out", torch.int32, k_pages, cache.seqs), lens_out.data_ptr())
+    return weight_out, pos_out, lens_out
 
 
 class _null:

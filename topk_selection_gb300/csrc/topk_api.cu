@@ -72,6 +72,8 @@ struct Workspace {
     void* sort = nullptr;       // topk_sort_u32 scratch (its header zero between calls)
     size_t sort_bytes = 0;
     unsigned sort_epoch = 0;    // tags the sort's look-back words, one per call
+    void* kv = nullptr;         // key-value cache operators' scratch
+    size_t kv_bytes = 0;
 };
 
 std::mutex g_ws_mutex;
@@ -187,6 +189,26 @@ int sort_spins_option() { return g_sort_spins.load(std::memory_order_relaxed); }
 int sort_withhold_option() { return g_sort_withhold.load(std::memory_order_relaxed); }
 void note_cuda_error(int err) { t_last_cuda_error = err; }
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
+int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status) {
+    Workspace* w = nullptr;
+    int rc = workspace(s, device, kI32CandOffset, 0, 0, &w);
+    if (rc != TOPK_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(g_ws_mutex);
+        rc = grow(&w->kv, &w->kv_bytes, bytes);
+    }
+    if (rc != TOPK_OK) return rc;
+    mark_not_released(w);
+    *scratch = w->kv;
+    *status = reinterpret_cast<unsigned*>(static_cast<char*>(w->ctrl_cand) + kI32StatusOffset);
+    return TOPK_OK;
+}
+int device_pointer(const void* p) {
+    bool host = false;
+    const int rc = is_host_pointer(p, &host);
+    return rc != TOPK_OK ? rc : host ? TOPK_ERR_INVALID_ARG : TOPK_OK;
+}
 void note_unreleased_launch(int device, cudaStream_t s) {
     Workspace* w = nullptr;
     {
@@ -625,7 +647,7 @@ int topk_release_workspace(void) {
     for (auto& kv : g_ws) {
         Workspace& w = kv.second;
         cudaSetDevice(kv.first.first);
-        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk})
+        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk, w.kv})
             if (p && cudaFree(p) != cudaSuccess) rc = TOPK_ERR_CUDA;
     }
     g_ws.clear();

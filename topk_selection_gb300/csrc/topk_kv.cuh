@@ -1,0 +1,78 @@
+// Shared by the key-value cache operators' files: the cache as the kernels
+// see it, and the launch functions behind the C ABI (include/topk.h holds the
+// contract).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "topk_internal.h"
+
+namespace topk {
+
+struct KvCache {
+    uint16_t* k;  // 16-bit elements, f16 or bf16 alike where they are only moved
+    uint16_t* v;
+    long long ks[3], vs[3];  // elements between pages, slots, heads
+    const int* table;
+    long long table_stride;
+    const int* lens;
+    int pages, page_size, heads, dim;
+    int seqs, width;  // width: table entries of a sequence
+    int bf16;
+
+    __host__ __device__ int capacity() const { return width * page_size; }
+    // Slots that sequence b holds.
+    __device__ int len(int b) const {
+        const int n = lens[b];
+        return n < 0 ? 0 : n > capacity() ? capacity() : n;
+    }
+    // Page of sequence b's slot, or -1 when the table names none.
+    __device__ int page_of(int b, int slot) const {
+        const int p = table[b * table_stride + slot / page_size];
+        return (unsigned)p < (unsigned)pages ? p : -1;
+    }
+};
+
+// A per-slot side array, [seqs, heads, slots].
+template <typename T>
+struct KvRows {
+    T* data;
+    long long seq, head;
+    __device__ T* row(int b, int h) const { return data + b * seq + h * head; }
+};
+
+cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k_new, const long long* k_stride,
+                             const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
+                             KvRows<float> weight, KvRows<int> pos, const int* next_pos);
+
+// scratch: kv_attend_scratch(...) bytes, 256-byte aligned, no contents needed.
+struct KvAttend {
+    const uint16_t* q;
+    long long qs[2];  // elements between sequences, query heads
+    int q_heads;
+    float scale;
+    uint16_t* out;
+    float* lse;
+    KvRows<const float> weight;
+    KvRows<float> weight_out;
+};
+size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a);
+cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, void* scratch,
+                             unsigned* status, int* launches);
+
+struct KvEvict {
+    KvRows<const float> weight;
+    KvRows<const int> pos;
+    const int* next_pos;
+    int budget, sink, recent;
+    KvRows<float> weight_out;
+    KvRows<int> pos_out;
+    int* lens_out;
+};
+size_t kv_evict_scratch(const KvCache& c, const KvEvict& e);
+cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
+                            unsigned* status, int* launches);
+
+}  // namespace topk

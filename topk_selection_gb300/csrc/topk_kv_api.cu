@@ -1,0 +1,222 @@
+// C ABI of the key-value cache operators: argument checks, scratch and
+// dispatch.  The contract is in include/topk.h.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/topk.h"
+#include "topk_internal.h"
+#include "topk_kv.cuh"
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+int cuda_fail(cudaError_t e) {
+    topk::note_cuda_error((int)e);
+    return TOPK_ERR_CUDA;
+}
+
+// Strides of 16-byte granularity, as the kernels' wide loads and tensor maps need.
+bool strides_ok(const int64_t* s, int n) {
+    for (int i = 0; i < n; ++i)
+        if (s[i] <= 0 || (s[i] & 7) || s[i] >= (int64_t(1) << 38)) return false;
+    return true;
+}
+
+int check_cache(const topk_kv_cache* c, topk::KvCache* out) {
+    if (!c || !c->k || !c->v || !c->table || !c->lens) return TOPK_ERR_INVALID_ARG;
+    if (c->dtype != TOPK_KV_F16 && c->dtype != TOPK_KV_BF16) return TOPK_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->page_size < 1 || c->heads < 1 || c->dim < 1 || c->table_width < 1 || c->seqs < 1 ||
+        c->table_stride < c->table_width)
+        return TOPK_ERR_INVALID_ARG;
+    if (misaligned(c->k, 16) || misaligned(c->v, 16) || misaligned(c->table, 4) || misaligned(c->lens, 4))
+        return TOPK_ERR_INVALID_ARG;
+    if (!strides_ok(c->k_stride, 3) || !strides_ok(c->v_stride, 3)) return TOPK_ERR_INVALID_ARG;
+    if ((c->page_size & 7) || c->page_size > 65536 || (c->dim & 7) || c->dim > TOPK_KV_MAX_DIM ||
+        c->seqs > 65535 || c->heads > 4096 || (int64_t)c->table_width * c->page_size >= (int64_t(1) << 30) ||
+        (int64_t)c->seqs * c->heads > (1 << 24))
+        return TOPK_ERR_UNSUPPORTED;
+    topk::KvCache& o = *out;
+    o.k = static_cast<uint16_t*>(c->k);
+    o.v = static_cast<uint16_t*>(c->v);
+    for (int i = 0; i < 3; ++i) {
+        o.ks[i] = c->k_stride[i];
+        o.vs[i] = c->v_stride[i];
+    }
+    o.table = c->table;
+    o.table_stride = c->table_stride;
+    o.lens = c->lens;
+    o.pages = c->pages;
+    o.page_size = c->page_size;
+    o.heads = c->heads;
+    o.dim = c->dim;
+    o.seqs = c->seqs;
+    o.width = c->table_width;
+    o.bf16 = c->dtype == TOPK_KV_BF16;
+    return TOPK_OK;
+}
+
+// A side array with at least `slots` slots whose rows do not lie in one another.
+int check_rows(const topk_kv_rows* r, const topk::KvCache& c, int slots) {
+    if (misaligned(r->data, 4) || r->slots < slots) return TOPK_ERR_INVALID_ARG;
+    if ((c.heads > 1 && r->head_stride < r->slots) || (c.seqs > 1 && r->seq_stride < r->slots))
+        return TOPK_ERR_INVALID_ARG;
+    if (r->head_stride < 0 || r->seq_stride < 0) return TOPK_ERR_INVALID_ARG;
+    return TOPK_OK;
+}
+
+template <typename T>
+topk::KvRows<T> rows_of(const topk_kv_rows* r) {
+    if (!r) return {nullptr, 0, 0};
+    return {static_cast<T*>(r->data), r->seq_stride, r->head_stride};
+}
+
+bool present(const topk_kv_rows* r) { return r && r->data; }
+
+// The bytes that a side array spans.
+size_t span(const topk_kv_rows* r, const topk::KvCache& c) {
+    return 4 * ((size_t)(c.seqs - 1) * r->seq_stride + (size_t)(c.heads - 1) * r->head_stride + r->slots);
+}
+
+// Whether `out` is the same array as `in`, or overlaps none of it.
+bool same_or_apart(const topk_kv_rows* in, const topk_kv_rows* out, const topk::KvCache& c) {
+    if (in->data == out->data) return in->seq_stride == out->seq_stride && in->head_stride == out->head_stride;
+    const char *a = static_cast<const char*>(in->data), *b = static_cast<const char*>(out->data);
+    return a + span(in, c) <= b || b + span(out, c) <= a;
+}
+
+int on_device(std::initializer_list<const void*> ps) {
+    for (const void* p : ps) {
+        if (!p) continue;
+        const int rc = topk::device_pointer(p);
+        if (rc != TOPK_OK) return rc;
+    }
+    return TOPK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const int64_t* k_new_stride,
+                   const void* v_new, const int64_t* v_new_stride, int tokens, const int32_t* starts,
+                   const struct topk_kv_rows* weight, const struct topk_kv_rows* pos, const int32_t* next_pos,
+                   struct CUstream_st* stream) {
+    topk::KvCache c;
+    int rc = check_cache(cache, &c);
+    if (rc != TOPK_OK) return rc;
+    if (tokens < 0 || !k_new_stride || !v_new_stride || (!starts && tokens != c.seqs)) return TOPK_ERR_INVALID_ARG;
+    if (present(pos) != (next_pos != nullptr)) return TOPK_ERR_INVALID_ARG;
+    if (present(weight) && (rc = check_rows(weight, c, c.capacity())) != TOPK_OK) return rc;
+    if (present(pos) && (rc = check_rows(pos, c, c.capacity())) != TOPK_OK) return rc;
+    if (tokens == 0) return TOPK_OK;
+    if (!k_new || !v_new || misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(starts, 4) ||
+        misaligned(next_pos, 4) || !strides_ok(k_new_stride, 2) || !strides_ok(v_new_stride, 2))
+        return TOPK_ERR_INVALID_ARG;
+    rc = on_device({c.k, c.v, c.table, c.lens, k_new, v_new, starts, present(weight) ? weight->data : nullptr,
+                    present(pos) ? pos->data : nullptr, next_pos});
+    if (rc != TOPK_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return cuda_fail(e);
+    topk::note_unreleased_launch(device, s);
+    const long long ks[2] = {k_new_stride[0], k_new_stride[1]}, vs[2] = {v_new_stride[0], v_new_stride[1]};
+    e = topk::kv_append_launch(s, c, static_cast<const uint16_t*>(k_new), ks, static_cast<const uint16_t*>(v_new), vs,
+                               tokens, starts, rows_of<float>(weight), rows_of<int>(pos), next_pos);
+    if (e != cudaSuccess) return cuda_fail(e);
+    topk::note_launch();
+    return TOPK_OK;
+}
+
+int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64_t* q_stride, int q_heads, float scale,
+                   void* out, float* lse, const struct topk_kv_rows* weight, const struct topk_kv_rows* weight_out,
+                   struct CUstream_st* stream) {
+    topk::KvCache c;
+    int rc = check_cache(cache, &c);
+    if (rc != TOPK_OK) return rc;
+    if (!q || !q_stride || !out || q_heads < 1 || q_heads % c.heads || !std::isfinite(scale) || misaligned(q, 16) ||
+        misaligned(out, 16) || misaligned(lse, 4) || !strides_ok(q_stride, 2))
+        return TOPK_ERR_INVALID_ARG;
+    if (present(weight) != present(weight_out)) return TOPK_ERR_INVALID_ARG;
+    if (present(weight)) {
+        if ((rc = check_rows(weight, c, c.capacity())) != TOPK_OK) return rc;
+        if ((rc = check_rows(weight_out, c, c.capacity())) != TOPK_OK) return rc;
+        if (!same_or_apart(weight, weight_out, c)) return TOPK_ERR_INVALID_ARG;
+    }
+    if ((int64_t)c.seqs * q_heads > (1 << 24)) return TOPK_ERR_UNSUPPORTED;
+    rc = on_device({c.k, c.v, c.table, c.lens, q, out, lse, present(weight) ? weight->data : nullptr,
+                    present(weight_out) ? weight_out->data : nullptr});
+    if (rc != TOPK_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return cuda_fail(e);
+    topk::KvAttend a = {};
+    a.q = static_cast<const uint16_t*>(q);
+    a.qs[0] = q_stride[0];
+    a.qs[1] = q_stride[1];
+    a.q_heads = q_heads;
+    a.scale = scale;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.weight = rows_of<const float>(weight);
+    a.weight_out = rows_of<float>(weight_out);
+    void* scratch = nullptr;
+    unsigned* status = nullptr;
+    rc = topk::kv_scratch(device, s, topk::kv_attend_scratch(device, c, a), &scratch, &status);
+    if (rc != TOPK_OK) return rc;
+    int launches = 0;
+    e = topk::kv_attend_launch(device, s, c, a, scratch, status, &launches);
+    topk::note_launches(launches);
+    return e == cudaSuccess ? TOPK_OK : cuda_fail(e);
+}
+
+int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* weight,
+                  const struct topk_kv_rows* pos, const int32_t* next_pos, int budget, int sink, int recent,
+                  const struct topk_kv_rows* weight_out, const struct topk_kv_rows* pos_out, int32_t* lens_out,
+                  struct CUstream_st* stream) {
+    topk::KvCache c;
+    int rc = check_cache(cache, &c);
+    if (rc != TOPK_OK) return rc;
+    if (!present(weight) || !present(pos) || !next_pos || !present(weight_out) || !present(pos_out) || !lens_out)
+        return TOPK_ERR_INVALID_ARG;
+    if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget || misaligned(next_pos, 4) ||
+        misaligned(lens_out, 4))
+        return TOPK_ERR_INVALID_ARG;
+    const int keep = budget < c.capacity() ? budget : c.capacity();
+    if ((rc = check_rows(weight, c, c.capacity())) != TOPK_OK || (rc = check_rows(pos, c, c.capacity())) != TOPK_OK ||
+        (rc = check_rows(weight_out, c, keep)) != TOPK_OK || (rc = check_rows(pos_out, c, keep)) != TOPK_OK)
+        return rc;
+    if (!same_or_apart(weight, weight_out, c) || !same_or_apart(pos, pos_out, c)) return TOPK_ERR_INVALID_ARG;
+    if (lens_out != c.lens && lens_out < c.lens + c.seqs && c.lens < lens_out + c.seqs) return TOPK_ERR_INVALID_ARG;
+    rc = on_device({c.k, c.v, c.table, c.lens, weight->data, pos->data, next_pos, weight_out->data, pos_out->data,
+                    lens_out});
+    if (rc != TOPK_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return cuda_fail(err);
+    topk::KvEvict e = {};
+    e.weight = rows_of<const float>(weight);
+    e.pos = rows_of<const int>(pos);
+    e.next_pos = next_pos;
+    e.budget = budget;
+    e.sink = sink;
+    e.recent = recent;
+    e.weight_out = rows_of<float>(weight_out);
+    e.pos_out = rows_of<int>(pos_out);
+    e.lens_out = lens_out;
+    void* scratch = nullptr;
+    unsigned* status = nullptr;
+    rc = topk::kv_scratch(device, s, topk::kv_evict_scratch(c, e), &scratch, &status);
+    if (rc != TOPK_OK) return rc;
+    int launches = 0;
+    err = topk::kv_evict_launch(device, s, c, e, scratch, status, &launches);
+    topk::note_launches(launches);
+    return err == cudaSuccess ? TOPK_OK : cuda_fail(err);
+}
+
+}  // extern "C"
