@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -377,63 +378,102 @@ def reduce(x: torch.Tensor, op: str, out: torch.Tensor | None = None, stream=Non
 
 _KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
+# The C structures as packed bytes: a decoding step makes several of these
+# calls per token and layer, and packing costs a tenth of what filling
+# ctypes structures does.  _KvCache and _KvRows above spell out the fields.
+_kv_pack_cache = struct.Struct("@PPiiiii4xqqqqqqPqiiP").pack
+_kv_pack_rows = struct.Struct("@Pqqi4x").pack
+_kv_pack_strides = struct.Struct("@qq").pack
 
-def _kv_check(t, name, dtype, device, shape):
-    """A tensor of this dtype and device whose sizes are `shape` (None: any)."""
+
+def _kv_refuse(t, name, dtype, device, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
-                         f"got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
 
 
-def _kv_strides(t, name, n):
-    """The strides of t's first n dimensions; its last must lie densely.  A
-    dimension of one element may have any stride in torch: the library gets
-    one that it accepts, which nothing is multiplied by."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _kv_ints(t, name, device, n):
+    """The address of a contiguous int32 vector of n elements; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.shape != (n,):
+        _kv_refuse(t, name, torch.int32, device, (n,))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _kv_strides(t, name, shape):
+    """t's strides but the last, which has to be 1.  A dimension of one
+    element may have any stride in torch: the library gets one that it
+    accepts, which nothing is multiplied by."""
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return (ctypes.c_int64 * n)(*(8 if t.shape[i] == 1 else t.stride(i) for i in range(n)))
+    if 1 in shape:
+        return [8 if n == 1 else x for n, x in zip(shape[:-1], strides)]
+    return strides[:-1]
 
 
 def _kv_cache(k_pages, v_pages, table, lens):
+    """(struct topk_kv_cache, device, dtype, sequences, heads, dim)."""
     if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _KV_DTYPES:
         raise TypeError("k_pages must be a float16 or bfloat16 tensor")
     if not k_pages.is_cuda:
         raise ValueError("k_pages must be a CUDA tensor")
-    dev = k_pages.device
-    _kv_check(k_pages, "k_pages", k_pages.dtype, dev, (None,) * 4)
-    _kv_check(v_pages, "v_pages", k_pages.dtype, dev, tuple(k_pages.shape))
-    _kv_check(table, "table", torch.int32, dev, (None, None))
-    _kv_check(lens, "lens", torch.int32, dev, (table.shape[0],))
-    if not lens.is_contiguous() or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("lens and the rows of table must be contiguous")
-    pages, page_size, heads, dim = k_pages.shape
+    dev, dtype, shape = k_pages.device, k_pages.dtype, k_pages.shape
+    if len(shape) != 4:
+        _kv_refuse(k_pages, "k_pages", dtype, dev, (None,) * 4)
+    if not isinstance(v_pages, torch.Tensor) or v_pages.dtype != dtype or v_pages.device != dev or \
+            v_pages.shape != shape:
+        _kv_refuse(v_pages, "v_pages", dtype, dev, tuple(shape))
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.device != dev or table.dim() != 2:
+        _kv_refuse(table, "table", torch.int32, dev, (None, None))
     seqs, width = table.shape
-    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _KV_DTYPES[k_pages.dtype], pages, page_size, heads, dim,
-                    _kv_strides(k_pages, "k_pages", 3), _kv_strides(v_pages, "v_pages", 3), table.data_ptr(),
-                    table.stride(0) if seqs > 1 else width, width, seqs, lens.data_ptr())
+    stride = table.stride()
+    if stride[1] != 1 and width > 1:
+        raise ValueError("the rows of table must be contiguous")
+    cache = _kv_pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _KV_DTYPES[dtype], *shape,
+                           *_kv_strides(k_pages, "k_pages", shape), *_kv_strides(v_pages, "v_pages", shape),
+                           table.data_ptr(), stride[0] if seqs > 1 else width, width, seqs,
+                           _kv_ints(lens, "lens", dev, seqs))
+    return cache, dev, dtype, seqs, shape[2], shape[3]
 
 
-def _kv_rows(t, name, dtype, k_pages, seqs):
+def _kv_rows(t, name, dtype, device, seqs, heads):
+    """struct topk_kv_rows of a tensor [seqs, heads, slots], or None."""
     if t is None:
         return None
-    _kv_check(t, name, dtype, k_pages.device, (seqs, k_pages.shape[2], None))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.dim() != 3 or \
+            t.shape[:2] != (seqs, heads):
+        _kv_refuse(t, name, dtype, device, (seqs, heads, None))
+    a, b, c = t.stride()
+    slots = t.shape[2]
+    if c != 1 and slots > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return ctypes.byref(_KvRows(t.data_ptr(), t.stride(0), t.stride(1), t.shape[2]))
+    return _kv_pack_rows(t.data_ptr(), a, b, slots)
+
+
+# The current stream's handle by device index; torch.cuda.current_stream
+# builds a Stream object, which takes as long as a launch.
+_kv_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _kv_call(fn, name, device, stream, *args):
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream, device))
+    index = device.index
+    if stream is None and _kv_raw_stream is not None:
+        handle = _kv_raw_stream(index)
+    else:
+        handle = _stream_handle(stream, device)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(stream, device))
+            rc = fn(*args, handle)
     if rc != TOPK_OK:
         raise TopKError(rc, name)
 
@@ -455,25 +495,24 @@ def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                       written at the new slots
 
     lens is not changed: add the tokens' numbers to it afterwards."""
-    cache = _kv_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
-    _kv_check(k_new, "k_new", k_pages.dtype, dev, (None, cache.heads, cache.dim))
-    _kv_check(v_new, "v_new", k_pages.dtype, dev, tuple(k_new.shape))
+    cache, dev, dtype, seqs, heads, dim = _kv_cache(k_pages, v_pages, table, lens)
+    if not isinstance(k_new, torch.Tensor) or k_new.dtype != dtype or k_new.device != dev or k_new.dim() != 3 or \
+            k_new.shape[1:] != (heads, dim):
+        _kv_refuse(k_new, "k_new", dtype, dev, (None, heads, dim))
+    shape = k_new.shape
+    if not isinstance(v_new, torch.Tensor) or v_new.dtype != dtype or v_new.device != dev or v_new.shape != shape:
+        _kv_refuse(v_new, "v_new", dtype, dev, tuple(shape))
     if (pos is None) != (next_pos is None):
         raise ValueError("pos and next_pos come together")
-    for t, name, n in ((starts, "starts", cache.seqs + 1), (next_pos, "next_pos", cache.seqs)):
-        if t is not None:
-            _kv_check(t, name, torch.int32, dev, (n,))
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    if k_new.shape[0] == 0:
+    starts = _kv_ints(starts, "starts", dev, seqs + 1)
+    next_pos = _kv_ints(next_pos, "next_pos", dev, seqs)
+    weight = _kv_rows(weight, "weight", torch.float32, dev, seqs, heads)
+    pos = _kv_rows(pos, "pos", torch.int32, dev, seqs, heads)
+    if shape[0] == 0:
         return
-    _kv_call(_lib.topk_kv_append, "topk_kv_append", dev, stream, ctypes.byref(cache), k_new.data_ptr(),
-             _kv_strides(k_new, "k_new", 2), v_new.data_ptr(), _kv_strides(v_new, "v_new", 2), k_new.shape[0],
-             None if starts is None else starts.data_ptr(),
-             _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
-             _kv_rows(pos, "pos", torch.int32, k_pages, cache.seqs),
-             None if next_pos is None else next_pos.data_ptr())
+    _kv_call(_lib.topk_kv_append, "topk_kv_append", dev, stream, cache, k_new.data_ptr(),
+             _kv_pack_strides(*_kv_strides(k_new, "k_new", shape)), v_new.data_ptr(),
+             _kv_pack_strides(*_kv_strides(v_new, "v_new", shape)), shape[0], starts, weight, pos, next_pos)
 
 
 def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -488,28 +527,29 @@ def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, tab
     defaults to dim ** -0.5.  With weight (float32 [seqs, heads, slots]), the
     attention that each slot gets, summed over its query heads, is added to it
     and written to weight_out (default: weight itself)."""
-    cache = _kv_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
-    _kv_check(q, "q", k_pages.dtype, dev, (cache.seqs, None, cache.dim))
-    q_heads = q.shape[1]
+    cache, dev, dtype, seqs, heads, dim = _kv_cache(k_pages, v_pages, table, lens)
+    if not isinstance(q, torch.Tensor) or q.dtype != dtype or q.device != dev or q.dim() != 3 or \
+            q.shape[0] != seqs or q.shape[2] != dim:
+        _kv_refuse(q, "q", dtype, dev, (seqs, None, dim))
+    shape = q.shape
     if out is None:
-        out = torch.empty((cache.seqs, q_heads, cache.dim), dtype=q.dtype, device=dev)
-    else:
-        _kv_check(out, "out", q.dtype, dev, tuple(q.shape))
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif not isinstance(out, torch.Tensor) or out.dtype != dtype or out.device != dev or out.shape != shape:
+        _kv_refuse(out, "out", dtype, dev, tuple(shape))
     if lse is None:
-        lse = torch.empty((cache.seqs, q_heads), dtype=torch.float32, device=dev)
-    else:
-        _kv_check(lse, "lse", torch.float32, dev, (cache.seqs, q_heads))
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    elif not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or \
+            lse.shape != shape[:2]:
+        _kv_refuse(lse, "lse", torch.float32, dev, tuple(shape[:2]))
     if not out.is_contiguous() or not lse.is_contiguous():
         raise ValueError("out and lse must be contiguous")
-    if weight_out is None:
-        weight_out = weight
-    elif weight is None:
+    if weight is None and weight_out is not None:
         raise ValueError("weight_out needs weight")
-    _kv_call(_lib.topk_kv_attend, "topk_kv_attend", dev, stream, ctypes.byref(cache), q.data_ptr(),
-             _kv_strides(q, "q", 2), q_heads, cache.dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
-             lse.data_ptr(), _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
-             _kv_rows(weight_out, "weight_out", torch.float32, k_pages, cache.seqs))
+    weight = _kv_rows(weight, "weight", torch.float32, dev, seqs, heads)
+    weight_out = weight if weight_out is None else _kv_rows(weight_out, "weight_out", torch.float32, dev, seqs, heads)
+    _kv_call(_lib.topk_kv_attend, "topk_kv_attend", dev, stream, cache, q.data_ptr(),
+             _kv_pack_strides(*_kv_strides(q, "q", shape)), shape[1], dim ** -0.5 if scale is None else float(scale),
+             out.data_ptr(), lse.data_ptr(), weight, weight_out)
     return out, lse
 
 
@@ -523,20 +563,16 @@ def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, 
     pos_out, lens_out), by default weight, pos and lens themselves, changed in
     place -- topk_kv_evict in include/topk.h.  Pages past the first
     ceil(budget / page_size) of a sequence can be reused afterwards."""
-    cache = _kv_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
+    cache, dev, _, seqs, heads, _ = _kv_cache(k_pages, v_pages, table, lens)
     weight_out = weight if weight_out is None else weight_out
     pos_out = pos if pos_out is None else pos_out
     lens_out = lens if lens_out is None else lens_out
-    for t, name in ((next_pos, "next_pos"), (lens_out, "lens_out")):
-        _kv_check(t, name, torch.int32, dev, (cache.seqs,))
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _kv_call(_lib.topk_kv_evict, "topk_kv_evict", dev, stream, ctypes.byref(cache),
-             _kv_rows(weight, "weight", torch.float32, k_pages, cache.seqs),
-             _kv_rows(pos, "pos", torch.int32, k_pages, cache.seqs), next_pos.data_ptr(), int(budget), int(sink),
-             int(recent), _kv_rows(weight_out, "weight_out", torch.float32, k_pages, cache.seqs),
-             _kv_rows(pos_out, "pos_out", torch.int32, k_pages, cache.seqs), lens_out.data_ptr())
+    _kv_call(_lib.topk_kv_evict, "topk_kv_evict", dev, stream, cache,
+             _kv_rows(weight, "weight", torch.float32, dev, seqs, heads),
+             _kv_rows(pos, "pos", torch.int32, dev, seqs, heads), _kv_ints(next_pos, "next_pos", dev, seqs),
+             int(budget), int(sink), int(recent),
+             _kv_rows(weight_out, "weight_out", torch.float32, dev, seqs, heads),
+             _kv_rows(pos_out, "pos_out", torch.int32, dev, seqs, heads), _kv_ints(lens_out, "lens_out", dev, seqs))
     return weight_out, pos_out, lens_out
 
 

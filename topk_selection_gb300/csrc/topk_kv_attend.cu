@@ -217,45 +217,59 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         // Copies, in the order in which the products use them:
         // K(0), K(1), V(0), K(2), V(1), ..., V(count - 1).
         const uint64_t policy = l2_evict_first_policy();
-        Walk wk = w, wv = w;
-        int item = 0, piece = -1, q_loads = 0;
-        bool ok = true;
-        auto wait_warp = [&](uint64_t* b, uint32_t parity) { return __all_sync(kFullMask, wait(b, parity)); };
-        auto load = [&](Walk& x, const CUtensorMap* map, int y0) {
-            const int slot0 = x.t * kTile, valid = min(kTile, x.n - slot0);
-            const int boxes = (valid + p.box - 1) / p.box, copies = boxes * S::kSub;
-            int page[(16 * S::kSub + 31) / 32];
-            // The table's entries are fetched before the wait for the ring.
+        constexpr int kPer = (16 * S::kSub + 31) / 32;  // copies of a lane, at most
+        struct Tile {
+            int row, b, slot0, copies;
+            int page[kPer];
+        };
+        // The pages of a tile, fetched a tile ahead of their use: the load
+        // takes as long as a third of a tile's copy.
+        auto fetch = [&](const Walk& x, Tile& t) {
+            t.row = x.r;
+            t.b = x.b;
+            t.slot0 = x.t * kTile;
+            t.copies = (min(kTile, x.n - t.slot0) + p.box - 1) / p.box * S::kSub;
 #pragma unroll
-            for (int j = 0; j < (16 * S::kSub + 31) / 32; ++j) {
+            for (int j = 0; j < kPer; ++j) {
                 const int i = j * 32 + lane;
-                page[j] = p.c.pages;  // outside the pool: reads as zeros
-                if (i < copies) {
-                    const int at = p.c.page_of(x.b, slot0 + i / S::kSub * p.box);
-                    if (at >= 0) page[j] = at;
+                t.page[j] = p.c.pages;  // outside the pool: reads as zeros
+                if (i < t.copies) {
+                    const int at = p.c.page_of(t.b, t.slot0 + i / S::kSub * p.box);
+                    if (at >= 0) t.page[j] = at;
                 }
             }
+        };
+        int item = 0, piece = -1, q_loads = 0;
+        auto wait_warp = [&](uint64_t* b, uint32_t parity) { return __all_sync(kFullMask, wait(b, parity)); };
+        auto load = [&](const Tile& t, const CUtensorMap* map) {
             const int st = item % S::kRing;
             if (item >= S::kRing && !wait_warp(&bar.empty[st], ((item / S::kRing) - 1) & 1)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], copies * p.box * 128);
+            if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], t.copies * p.box * 128);
             __syncwarp();
             unsigned char* dst = ring + st * S::kItem;
 #pragma unroll
-            for (int j = 0; j < (16 * S::kSub + 31) / 32; ++j) {
+            for (int j = 0; j < kPer; ++j) {
                 const int i = j * 32 + lane;
-                if (i < copies) {
+                if (i < t.copies) {
                     const int box = i / S::kSub, sub = i % S::kSub;
                     tma_load_4d(dst + sub * (kTile * 128) + box * p.box * 128, map, sub * 64,
-                                (slot0 + box * p.box) % p.c.page_size, y0, page[j], &bar.full[st], policy);
+                                (t.slot0 + box * p.box) % p.c.page_size, t.row / p.parts, t.page[j], &bar.full[st],
+                                policy);
                 }
             }
             ++item;
             return true;
         };
-        for (int it = 0; ok && it <= count; ++it) {
+        Walk x = w;
+        Tile before, now, after;
+        if (count > 0) fetch(x, now);
+        for (int it = 0; it <= count; ++it) {
+            if (it + 1 < count) {
+                x.next(p);
+                fetch(x, after);
+            }
             if (it < count) {
-                const int h = wk.r / p.parts;
-                if (it == 0 || wk.t == 0) {
+                if (it == 0 || now.slot0 == 0) {
                     ++piece;
                     if (piece >= 2 && !wait_warp(&bar.q_free[piece & 1], ((piece - 2) >> 1) & 1)) break;
                     if (lane == 0) {
@@ -263,19 +277,16 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                         mbar_arrive_expect_tx(b, S::kSub * GP * 128);
                         for (int sub = 0; sub < S::kSub; ++sub)
                             tma_load_3d(q_buf + (piece & 1) * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
-                                        h * p.group + wk.r % p.parts * GP, wk.b, b);
+                                        now.row / p.parts * p.group + now.row % p.parts * GP, now.b, b);
                     }
                     ++q_loads;
                     __syncwarp();
                 }
-                ok = load(wk, &map_k, h);
-                if (!ok) break;
-                wk.next(p);
+                if (!load(now, &map_k)) break;
             }
-            if (it > 0) {
-                ok = load(wv, &map_v, wv.r / p.parts);
-                wv.next(p);
-            }
+            if (it > 0 && !load(before, &map_v)) break;
+            before = now;
+            now = after;
         }
         __syncwarp();
         if (gave_up) {  // wait for the copies in flight, so that none lands after the block's end
@@ -527,7 +538,7 @@ template <int GP>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs p) {
     __shared__ int scan[kJoinThreads / 32 + 8];
     __shared__ float2 ml[GP];
-    __shared__ float acc[kJoinThreads / 32][32];
+    __shared__ float acc[kJoinThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Walk w = find_range<kJoinThreads>(p, scan);
     for (int b = blockIdx.x; b < p.c.seqs; b += gridDim.x) {
@@ -576,25 +587,29 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs 
             if (block == c0 && tid < heads && p.a.lse)
                 p.a.lse[q0 + tid] = ml[tid].y == 0.f ? -INFINITY
                                                      : (ml[tid].x - kBias + log2f(ml[tid].y)) * 0.6931471805599453f;
-            // 32 elements of the output at a time, the blocks in turn; the warps share out the row's pieces.
-            const int elements = heads * p.c.dim;
-            for (int e0 = (block - c0) * 32; e0 < elements; e0 += (c1 - c0 + 1) * 32) {
-                const int i = e0 + lane, g = min(i / p.c.dim, heads - 1);
+            // The row's blocks share out the output's elements; a block's
+            // threads share its elements, and the row's pieces where threads are left.
+            const int elements = heads * p.c.dim, blocks = c1 - c0 + 1;
+            const int each = (elements + blocks - 1) / blocks;
+            const int width = each > 128 ? 256 : each > 64 ? 128 : each > 32 ? 64 : 32, ways = kJoinThreads / width;
+            const int from = (block - c0) * each, to = min(from + each, elements);
+            for (int e0 = from; e0 < to; e0 += width) {
+                const int i = e0 + tid % width, g = min(i / p.c.dim, heads - 1);
                 const float top = ml[g].x;
                 float o = 0.f;
-                for (int c = c0 + warp; c <= c1; c += kJoinThreads / 32) {
-                    const int share = 2 * c + (c == c0);
-                    const float x = p.part_ml[share * GP + g].x;
-                    if (i < elements && x != -INFINITY)
-                        o += p.part_o[(size_t)share * GP * p.c.dim + i] * exp2f(x - top);
-                }
+                if (i < to)
+#pragma unroll 4
+                    for (int c = c0 + tid / width; c <= c1; c += ways) {
+                        const int share = 2 * c + (c == c0);
+                        const float x = p.part_ml[share * GP + g].x, v = p.part_o[(size_t)share * GP * p.c.dim + i];
+                        o += x == -INFINITY ? 0.f : v * exp2f(x - top);
+                    }
                 __syncthreads();
-                acc[warp][lane] = o;
+                acc[tid] = o;
                 __syncthreads();
-                if (warp == 0 && i < elements) {
-                    float v = 0.f;
-                    for (int k = 0; k < kJoinThreads / 32; ++k) v += acc[k][lane];
-                    p.a.out[(size_t)q0 * p.c.dim + i] = from_float(ml[g].y == 0.f ? 0.f : v / ml[g].y, p.c.bf16);
+                if (tid < width && i < to) {
+                    for (int k = 1; k < ways; ++k) o += acc[k * width + tid];
+                    p.a.out[(size_t)q0 * p.c.dim + i] = from_float(ml[g].y == 0.f ? 0.f : o / ml[g].y, p.c.bf16);
                 }
             }
         }
