@@ -37,8 +37,8 @@ namespace topk {
 namespace {
 
 constexpr int kTile = 128;       // slots of a tile
-constexpr int kThreads = 192;    // 4 softmax warps, the copy warp, the product warp
-constexpr int kJoinThreads = 256;
+constexpr int kThreads = 224;    // 4 softmax warps, the copy warp, a warp for each product
+constexpr int kJoinThreads = 512;
 constexpr float kSlack = 8.f;    // p <= 2^(kSlack + kBias) = 2^15: within f16's range
 constexpr float kBias = 7.f;     // and f16's smallest step, 2^-24, is 2^-31 of the largest p
 constexpr int kRingBytes = 192 * 1024;
@@ -146,19 +146,81 @@ struct Shape {
     static constexpr int kRing = kRingBytes / kItem;
     static constexpr int kQBytes = kSub * 16 * 128;       // 16 rows of a query block
     static constexpr int kPCols = 2 * GP;                 // hi and lo of every head
-    static constexpr int kPBytes = kPCols * kTile * 2;
+    static constexpr int kPRow = kPCols * 2;              // bytes of a slot's row of P
+    static constexpr int kPBytes = kPRow * kTile;
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
     static constexpr int kOBlocks = DP / kM;
     static constexpr int kTmemS = 0, kTmemO = 32;         // columns: two S buffers of 16, then O
     static constexpr int kTmemCols = 32 + kOBlocks * kPCols <= 64 ? 64 : 128;
     static constexpr size_t kSmem = 1024 + kRingBytes + 2 * kQBytes + 2 * kPBytes;
+    // Barriers, by their place in bars[].
+    static constexpr int kFull = 0, kEmpty = kRing, kSFull = 2 * kRing, kSFree = kSFull + 2, kPReady = kSFull + 4,
+                         kPFree = kSFull + 6, kQFull = kSFull + 8, kQFree = kSFull + 10, kDrain = kSFull + 12,
+                         kBars = kSFull + 14;
 };
 
-struct Barriers {
-    uint64_t full[12], empty[12];
-    uint64_t s_full[2], s_free[2], p_ready[2], p_free[2], q_full[2], q_free[2];
-    uint64_t drain;
+// The bounded wait's slow side: gives up after kWaitSpins tries, or once
+// another wait of the block has.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, unsigned* status) {
+    for (int i = 0; i < kWaitSpins; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if (*gave_up) return false;
+    }
+    *gave_up = 1;
+    atomicOr(status, kStatusWaitTimeout);
+    return false;
+}
+
+// A place in the ring, moved on by n <= kRing items.
+template <int RING>
+struct Place {
+    int at;
+    uint32_t phase;
+    __device__ __forceinline__ void move(int n) {
+        at += n;
+        if (at >= RING) {
+            at -= RING;
+            phase ^= 1;
+        }
+    }
 };
+
+// Sums of v[g] over the warp's lanes, for GP heads at once: lanes halve the
+// heads they hold as the sums double in width, so this takes GP - 1 + (5 -
+// log2 GP) shuffles instead of 5 * GP.  Returns the sum of head warp_head().
+template <int GP>
+__device__ __forceinline__ float warp_sums(float (&v)[GP], int lane) {
+#pragma unroll
+    for (int n = GP / 2, d = 16; d >= 1; n /= 2, d /= 2) {
+        if (n == 0) {
+            v[0] += __shfl_xor_sync(kFullMask, v[0], d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool high = (lane & d) != 0;
+                const float give = high ? v[i] : v[i + n], keep = high ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor_sync(kFullMask, give, d);
+            }
+        }
+    }
+    return v[0];
+}
+template <int GP>
+__device__ __forceinline__ int warp_head(int lane) { return lane >> (GP == 8 ? 2 : 1); }
+
+// Two numbers as 16-bit elements in one word, and back.
+__device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
+    if (bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&x);
+    }
+    const __half2 x = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t x, int bf16) {
+    if (bf16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
 
 template <int DP, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -166,32 +228,26 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                  const __grid_constant__ CUtensorMap map_q) {
     using S = Shape<DP, GP>;
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* q_buf = ring + kRingBytes;
-    unsigned char* p_buf = q_buf + 2 * S::kQBytes;
-    __shared__ Barriers bar;
+    __shared__ __align__(8) uint64_t bars[S::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int scan[kThreads / 32 + 8];
-    __shared__ __align__(16) float red[2][4][GP];
+    __shared__ __align__(16) float red[4][GP];
     __shared__ volatile int gave_up;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bar0 = smem_addr(bars);
     if (tid == 0) {
-        for (int i = 0; i < S::kRing; ++i) {
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < S::kBars; ++i) {
+            const bool by_threads = i == S::kSFree || i == S::kSFree + 1 || i == S::kPReady || i == S::kPReady + 1;
+            mbar_init(&bars[i], by_threads ? 128 : 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.s_free[i], 128);
-            mbar_init(&bar.p_ready[i], 128);
-            mbar_init(&bar.p_free[i], 1);
-            mbar_init(&bar.q_full[i], 1);
-            mbar_init(&bar.q_free[i], 1);
-        }
-        mbar_init(&bar.drain, 1);
         mbar_init_fence();
         gave_up = 0;
+    }
+    if (warp == 4 && lane == 0) {
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        prefetch_map(&map_q);
     }
     if (warp == 5) tmem_alloc(&tmem_at, S::kTmemCols);
     launch_dependents();  // the join waits for this launch's end before it reads anything of it
@@ -200,17 +256,18 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_at;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, q_buf = ring + kRingBytes, p_buf = q_buf + 2 * S::kQBytes;
     const int count = w.e - w.s;  // tiles of this block
 
-    // A bounded wait; after one gave up, every other gives up too.
-    auto wait = [&](uint64_t* b, uint32_t parity) {
-        for (int i = 0; i < kWaitSpins; ++i) {
-            if (mbar_try_wait(b, parity)) return true;
-            if (gave_up) return false;
-        }
-        gave_up = 1;
-        atomicOr(p.status, kStatusWaitTimeout);
-        return false;
+    auto wait = [&](int bar, uint32_t parity) {
+        if (mbar_try(bar0 + bar * 8, parity)) return true;
+        return wait_slow(bar0 + bar * 8, parity, &gave_up, p.status);
+    };
+    // The block's tiles of the row that x stands in, and the slots of the last of them.
+    auto share_of = [&](const Walk& x, int done, int* last) {
+        const int n = min(x.tiles - x.t, count - done);
+        *last = min(kTile, x.n - (x.t + n - 1) * kTile);
+        return n;
     };
 
     if (warp == 4) {
@@ -219,65 +276,83 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         const uint64_t policy = l2_evict_first_policy();
         constexpr int kPer = (16 * S::kSub + 31) / 32;  // copies of a lane, at most
         struct Tile {
-            int row, b, slot0, copies;
-            int page[kPer];
+            int row, b, copies;
+            int page[kPer], at[kPer];  // of each copy's first slot
         };
         // The pages of a tile, fetched a tile ahead of their use: the load
-        // takes as long as a third of a tile's copy.
-        auto fetch = [&](const Walk& x, Tile& t) {
+        // takes as long as a third of a tile's copy.  A lane's slots move by
+        // a tile at a time, so that only a new row divides.
+        int index[kPer], in[kPer];
+        const int step = kTile / p.c.page_size, rest = kTile % p.c.page_size;
+        auto fetch = [&](const Walk& x, Tile& t, bool enter) {
             t.row = x.r;
             t.b = x.b;
-            t.slot0 = x.t * kTile;
-            t.copies = (min(kTile, x.n - t.slot0) + p.box - 1) / p.box * S::kSub;
+            const int left = x.n - x.t * kTile;
+            t.copies = left >= kTile ? kTile / p.box * S::kSub : (left + p.box - 1) / p.box * S::kSub;
+            const int* table = p.c.table + x.b * p.c.table_stride;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int i = j * 32 + lane;
-                t.page[j] = p.c.pages;  // outside the pool: reads as zeros
-                if (i < t.copies) {
-                    const int at = p.c.page_of(t.b, t.slot0 + i / S::kSub * p.box);
-                    if (at >= 0) t.page[j] = at;
+                if (enter) {
+                    const int slot = x.t * kTile + i / S::kSub * p.box;
+                    index[j] = slot / p.c.page_size;
+                    in[j] = slot - index[j] * p.c.page_size;
+                } else {
+                    index[j] += step;
+                    in[j] += rest;
+                    if (in[j] >= p.c.page_size) {
+                        in[j] -= p.c.page_size;
+                        ++index[j];
+                    }
                 }
+                t.at[j] = in[j];
+                t.page[j] = -1;
+                if (i < t.copies) t.page[j] = table[index[j]];
             }
         };
-        int item = 0, piece = -1, q_loads = 0;
-        auto wait_warp = [&](uint64_t* b, uint32_t parity) { return __all_sync(kFullMask, wait(b, parity)); };
+        Place<S::kRing> put = {0, 0};
+        int items = 0, q_loads = 0;
+        auto wait_warp = [&](int bar, uint32_t parity) { return __all_sync(kFullMask, wait(bar, parity)); };
         auto load = [&](const Tile& t, const CUtensorMap* map) {
-            const int st = item % S::kRing;
-            if (item >= S::kRing && !wait_warp(&bar.empty[st], ((item / S::kRing) - 1) & 1)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], t.copies * p.box * 128);
+            if (items >= S::kRing && !wait_warp(S::kEmpty + put.at, put.phase ^ 1)) return false;
+            const uint32_t full = bar0 + (S::kFull + put.at) * 8, dst = ring + put.at * S::kItem;
+            if (lane == 0) mbar_expect_at(full, t.copies * p.box * 128);
             __syncwarp();
-            unsigned char* dst = ring + st * S::kItem;
+            const int h = p.parts == 1 ? t.row : t.row / p.parts;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int i = j * 32 + lane;
                 if (i < t.copies) {
-                    const int box = i / S::kSub, sub = i % S::kSub;
-                    tma_load_4d(dst + sub * (kTile * 128) + box * p.box * 128, map, sub * 64,
-                                (t.slot0 + box * p.box) % p.c.page_size, t.row / p.parts, t.page[j], &bar.full[st],
-                                policy);
+                    // A page outside the pool reads as zeros.
+                    const int page = (unsigned)t.page[j] < (unsigned)p.c.pages ? t.page[j] : p.c.pages;
+                    tma_load_4d(dst + i % S::kSub * (kTile * 128) + i / S::kSub * p.box * 128, map, i % S::kSub * 64,
+                                t.at[j], h, page, full, policy);
                 }
             }
-            ++item;
+            ++items;
+            put.move(1);
             return true;
         };
         Walk x = w;
         Tile before, now, after;
-        if (count > 0) fetch(x, now);
+        bool enters = true, enters_next = false;
+        if (count > 0) fetch(x, now, true);
         for (int it = 0; it <= count; ++it) {
             if (it + 1 < count) {
                 x.next(p);
-                fetch(x, after);
+                enters_next = x.t == 0;
+                fetch(x, after, enters_next);
             }
             if (it < count) {
-                if (it == 0 || now.slot0 == 0) {
-                    ++piece;
-                    if (piece >= 2 && !wait_warp(&bar.q_free[piece & 1], ((piece - 2) >> 1) & 1)) break;
+                if (enters) {
+                    const int buf = q_loads & 1;
+                    if (q_loads >= 2 && !wait_warp(S::kQFree + buf, ((q_loads - 2) >> 1) & 1)) break;
                     if (lane == 0) {
-                        uint64_t* b = &bar.q_full[piece & 1];
-                        mbar_arrive_expect_tx(b, S::kSub * GP * 128);
+                        const uint32_t full = bar0 + (S::kQFull + buf) * 8;
+                        mbar_expect_at(full, S::kSub * GP * 128);
                         for (int sub = 0; sub < S::kSub; ++sub)
-                            tma_load_3d(q_buf + (piece & 1) * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
-                                        now.row / p.parts * p.group + now.row % p.parts * GP, now.b, b);
+                            tma_load_3d(q_buf + buf * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
+                                        now.row / p.parts * p.group + now.row % p.parts * GP, now.b, full);
                     }
                     ++q_loads;
                     __syncwarp();
@@ -287,203 +362,238 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             if (it > 0 && !load(before, &map_v)) break;
             before = now;
             now = after;
+            enters = enters_next;
         }
         __syncwarp();
         if (gave_up) {  // wait for the copies in flight, so that none lands after the block's end
-            for (int i = max(0, item - S::kRing); i < item; ++i) mbar_wait(&bar.full[i % S::kRing], (i / S::kRing) & 1);
-            for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bar.q_full[i & 1], (i >> 1) & 1);
+            for (int i = max(0, items - S::kRing); i < items; ++i)
+                mbar_wait(&bars[S::kFull + i % S::kRing], (i / S::kRing) & 1);
+            for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
         }
     } else if (warp == 5) {
-        if (lane == 0 && count > 0) {
-            // Products: S(0), S(1), O(0), S(2), O(1), ...
-            const uint32_t id_s = mma_idesc(p.c.bf16, kTile, 16, false);
-            const uint32_t id_o = mma_idesc(p.c.bf16, S::kM, S::kPCols, true);
-            int item = 0, piece = -1;
-            Walk x = w, y = w;  // the tiles of S and of O
-            bool y_first = true;
-            for (int it = 0; it <= count; ++it) {
-                if (it < count) {
-                    const int buf = it & 1, st = item % S::kRing;
-                    if (it == 0 || x.t == 0) {
-                        ++piece;
-                        if (!wait(&bar.q_full[piece & 1], (piece >> 1) & 1)) break;
-                    }
-                    if (!wait(&bar.full[st], (item / S::kRing) & 1)) break;
-                    if (it >= 2 && !wait(&bar.s_free[buf], ((it - 2) >> 1) & 1)) break;
+        if (lane == 0) {  // S = K Q^T
+            const uint32_t id = mma_idesc(p.c.bf16, kTile, 16, false);
+            constexpr uint32_t hi = smem_desc_hi(1024, 128);
+            const uint32_t k_lo = smem_desc_lo(ring, 16), q_lo = smem_desc_lo(q_buf, 16);
+            Place<S::kRing> get = {0, 0};
+            Walk x = w;
+            bool ok = true;
+            for (int it = 0, piece = 0; it < count && ok; ++piece) {
+                int last;
+                const int n = share_of(x, it, &last), qb = piece & 1;
+                if (!wait(S::kQFull + qb, (piece >> 1) & 1)) break;
+                for (int k = 0; k < n; ++k, ++it) {
+                    const int buf = it & 1;
+                    ok = wait(S::kFull + get.at, get.phase) &&
+                         (it < 2 || wait(S::kSFree + buf, ((it >> 1) & 1) ^ 1));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t ka = smem_addr(ring + st * S::kItem);
-                    const uint32_t qa = smem_addr(q_buf + (piece & 1) * S::kQBytes);
+                    const uint32_t a = k_lo + get.at * (S::kItem >> 4), b = q_lo + qb * (S::kQBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < DP / 16; ++j)
-                        mma_f16(tmem + S::kTmemS + buf * 16,
-                                smem_desc_sw128(ka + (j >> 2) * (kTile * 128) + (j & 3) * 32, 16, 1024),
-                                smem_desc_sw128(qa + (j >> 2) * (16 * 128) + (j & 3) * 32, 16, 1024), id_s, j > 0);
-                    mma_commit(&bar.s_full[buf]);
-                    mma_commit(&bar.empty[st]);
-                    const bool last = x.t + 1 == x.tiles;
-                    if (last) mma_commit(&bar.q_free[piece & 1]);
-                    x.next(p);
-                    ++item;
+                        mma_f16(tmem + S::kTmemS + buf * 16, a + (((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4), hi,
+                                b + (((j >> 2) * (16 * 128) + (j & 3) * 32) >> 4), hi, id, j > 0);
+                    mma_commit(bar0 + (S::kSFull + buf) * 8);
+                    mma_commit(bar0 + (S::kEmpty + get.at) * 8);
+                    get.move(it == 0 ? 1 : 2);  // K(t) is item 2t - 1, but K(0) is the first
                 }
-                if (it > 0) {
-                    const int t = it - 1, buf = t & 1, st = item % S::kRing;
-                    if (!wait(&bar.full[st], (item / S::kRing) & 1)) break;
-                    if (!wait(&bar.p_ready[buf], (t >> 1) & 1)) break;
-                    tc_fence_after();
-                    const int valid = min(kTile, y.n - y.t * kTile), steps = (valid + 15) / 16;
-                    const uint32_t va = smem_addr(ring + st * S::kItem), pa = smem_addr(p_buf + buf * S::kPBytes);
-                    for (int j = 0; j < steps; ++j) {
-                        const uint64_t db =
-                            smem_desc_sw128(pa + (j >> 2) * (S::kPCols * 128) + (j & 3) * 32, 16, 1024);
-#pragma unroll
-                        for (int m = 0; m < S::kOBlocks; ++m)
-                            mma_f16(tmem + S::kTmemO + m * S::kPCols,
-                                    smem_desc_sw128(va + m * 2 * (kTile * 128) + j * 2048, kTile * 128, 1024), db,
-                                    id_o, !y_first || j > 0);
-                    }
-                    mma_commit(&bar.empty[st]);
-                    mma_commit(&bar.p_free[buf]);
-                    y_first = y.t + 1 == y.tiles;
-                    y.next(p);
-                    ++item;
-                }
+                mma_commit(bar0 + (S::kQFree + qb) * 8);
+                x.t += n - 1;
+                x.next(p);
             }
             if (gave_up) {  // wait for the products in flight
-                mma_commit(&bar.drain);
-                mbar_wait(&bar.drain, 0);
+                mma_commit(bar0 + S::kDrain * 8);
+                mbar_wait(&bars[S::kDrain], 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        if (lane == 0) {  // O += V^T P^T
+            const uint32_t id = mma_idesc(p.c.bf16, S::kM, S::kPCols, true);
+            constexpr uint32_t hi_v = smem_desc_hi(1024, 128), hi_p = smem_desc_hi(S::kPRow * 8, S::kPRow);
+            const uint32_t v_lo = smem_desc_lo(ring, kTile * 128), p_lo = smem_desc_lo(p_buf, 16);
+            // V(t) is item 2t + 2, but the last one follows V(t - 1).
+            Place<S::kRing> get = {0, 0};
+            get.move(count == 1 ? 1 : 2);
+            Walk x = w;
+            bool ok = true;
+            for (int it = 0; it < count && ok;) {
+                int last;
+                const int n = share_of(x, it, &last);
+                for (int k = 0; k < n; ++k, ++it) {
+                    const int buf = it & 1, steps = k + 1 < n ? 8 : (last + 15) >> 4;
+                    ok = wait(S::kFull + get.at, get.phase) && wait(S::kPReady + buf, (it >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = v_lo + get.at * (S::kItem >> 4), b = p_lo + buf * (S::kPBytes >> 4);
+#pragma unroll
+                    for (int j = 0; j < kTile / 16; ++j) {
+                        if (j >= steps) break;
+#pragma unroll
+                        for (int m = 0; m < S::kOBlocks; ++m)
+                            mma_f16(tmem + S::kTmemO + m * S::kPCols, a + ((m * 2 * (kTile * 128) + j * 2048) >> 4),
+                                    hi_v, b + j * (S::kPRow * 16 >> 4), hi_p, id, k > 0 || j > 0);
+                    }
+                    mma_commit(bar0 + (S::kPFree + buf) * 8);
+                    mma_commit(bar0 + (S::kEmpty + get.at) * 8);
+                    get.move(it + 2 == count ? 1 : 2);
+                }
+                x.t += n - 1;
+                x.next(p);
+            }
+            if (gave_up) {
+                mma_commit(bar0 + (S::kDrain + 1) * 8);
+                mbar_wait(&bars[S::kDrain + 1], 0);
             }
         }
         __syncwarp();
     } else {
         // Softmax: thread tid owns slot tid of each tile, and lane tid of O.
         const float c = p.a.scale * 1.4426950408889634f;
-        const uint32_t lane_base = (uint32_t)warp << 21;  // 32 * warp in the address's lane field
+        const uint32_t my_tmem = tmem + ((uint32_t)warp << 21);  // 32 * warp in the address's lane field
+        // This slot's row of P: 16-byte chunks, swizzled over the row's width.
+        constexpr int kChunks = S::kPRow / 16;
+        const int turn = kChunks == 2 ? (tid >> 2) & 1 : (tid >> 1) & 3;
         float m[GP], l[GP];
         Walk x = w;
-        bool ok = true;  // false once a wait gave up; all 128 threads leave at the next barrier
-        for (int it = 0; it < count; ++it, x.next(p)) {
-            const int buf = it & 1, slot0 = x.t * kTile, valid = min(kTile, x.n - slot0);
-            const bool first = it == 0 || x.t == 0;
-            const int part = x.r % p.parts, heads = min(GP, p.group - part * GP);
-            float s[GP];
-            ok = ok && wait(&bar.s_full[buf], (it >> 1) & 1);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll
-            for (int g = 0; g < GP; g += 8) tmem_ld8(tmem + lane_base + S::kTmemS + buf * 16 + g, s + g);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(&bar.s_free[buf]);
-            const bool mine = tid < valid;
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                const float top = warp_max(mine && g < heads ? s[g] * c : -INFINITY);
-                if (lane == 0) red[buf][warp][g] = top;
-            }
-            if (!bar_all(1, 128, ok)) break;
-            float top[GP];
-            bool up = false;
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                top[g] = fmaxf(fmaxf(red[buf][0][g], red[buf][1][g]), fmaxf(red[buf][2][g], red[buf][3][g]));
-                if (first) {
-                    m[g] = top[g];
-                    l[g] = 0.f;
-                }
-                up = up || top[g] > m[g] + kSlack;
-            }
-            if (up) {  // the same for all 128 threads; the tile before has to be in O
-                ok = wait(&bar.p_free[buf ^ 1], ((it - 1) >> 1) & 1);
+        bool ok = true;    // false once a wait gave up
+        bool leave = false;  // all 128 threads leave at the same barrier
+        for (int it = 0; it < count && !leave;) {
+            int last;
+            const int n = share_of(x, it, &last);
+            const int part = p.parts == 1 ? 0 : x.r % p.parts, heads = min(GP, p.group - part * GP);
+            const int tile0 = w.s + it;
+            for (int k = 0; k < n; ++k, ++it) {
+                const int buf = it & 1, valid = k + 1 < n ? kTile : last;
+                float s[GP];
+                ok = ok && wait(S::kSFull + buf, (it >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                float f[GP];
+#pragma unroll
+                for (int g = 0; g < GP; g += 8) tmem_ld8(my_tmem + S::kTmemS + buf * 16 + g, s + g);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive_at(bar0 + (S::kSFree + buf) * 8);
+                const bool mine = tid < valid;
+                bool over = !ok;
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    const float to = fmaxf(m[g], top[g]);
-                    f[g] = to == m[g] ? 1.f : exp2_approx(m[g] - to);
-                    m[g] = to;
-                    l[g] *= f[g];
+                    if (g >= heads) s[g] = 0.f;  // what a group of fewer heads leaves in its columns
+                    if (k > 0) over = over || (mine && s[g] * c > m[g] + kSlack);
+                }
+                // Some score has passed the reference by kSlack (or there is none yet).
+                if (k == 0 || bar_any(1, 128, over)) {
+                    leave = bar_any(1, 128, !ok);
+                    if (leave) break;
+#pragma unroll
+                    for (int g = 0; g < GP; ++g) {
+                        const float top = warp_max(mine ? s[g] * c : -INFINITY);
+                        if (lane == 0) red[warp][g] = top;
+                    }
+                    bar_sync(1, 128);
+                    float f[GP];
+#pragma unroll
+                    for (int g = 0; g < GP; ++g) {
+                        const float top = fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g]));
+                        if (k == 0) {
+                            m[g] = top;
+                            l[g] = 0.f;
+                        } else {
+                            const float to = fmaxf(m[g], top);
+                            f[g] = to == m[g] ? 1.f : exp2_approx(m[g] - to);
+                            m[g] = to;
+                            l[g] *= f[g];
+                        }
+                    }
+                    if (k > 0) {
+                        ok = wait(S::kPFree + (buf ^ 1), ((it - 1) >> 1) & 1);  // the tile before is in O
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll
+                        for (int o = 0; o < S::kOBlocks * 2; ++o) {  // hi columns and lo columns of each block
+                            float v[GP];
+                            const uint32_t at = my_tmem + S::kTmemO + o * GP;
+#pragma unroll
+                            for (int g = 0; g < GP; g += 8) tmem_ld8(at + g, v + g);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int g = 0; g < GP; ++g) v[g] *= f[g];
+#pragma unroll
+                            for (int g = 0; g < GP; g += 8) tmem_st8(at + g, v + g);
+                            tmem_wait_st();
+                        }
+                        tc_fence_before();
+                    }
                 }
 #pragma unroll
-                for (int o = 0; o < S::kOBlocks * 2; ++o) {  // the hi columns, then the lo columns, of each block
-                    float v[GP];
-                    const uint32_t at = tmem + lane_base + S::kTmemO + o * GP;
-#pragma unroll
-                    for (int g = 0; g < GP; g += 8) tmem_ld8(at + g, v + g);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) v[g] *= f[g];
-#pragma unroll
-                    for (int g = 0; g < GP; g += 8) tmem_st8(at + g, v + g);
-                    tmem_wait_st();
+                for (int g = 0; g < GP; ++g) {
+                    const float e = exp2_approx(fmaf(s[g], c, kBias - (m[g] == -INFINITY ? 0.f : m[g])));
+                    s[g] = mine ? e : 0.f;
+                    l[g] += s[g];
                 }
-                tc_fence_before();
-            }
+                if (p.p) {
+                    float4* to = reinterpret_cast<float4*>(p.p + ((size_t)(tile0 + k) * kTile + tid) * GP);
 #pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                const float ref = m[g] == -INFINITY ? 0.f : m[g];
-                s[g] = mine && g < heads ? exp2_approx(fmaf(s[g], c, kBias - ref)) : 0.f;
-                l[g] += s[g];
-            }
-            if (p.p) {
-                float* to = p.p + ((size_t)(w.s + it) * kTile + tid) * GP;
+                    for (int g = 0; g < GP; g += 4) to[g / 4] = make_float4(s[g], s[g + 1], s[g + 2], s[g + 3]);
+                    if (tid == 0) {
+                        float4* tm = reinterpret_cast<float4*>(p.tile_m + (size_t)(tile0 + k) * GP);
 #pragma unroll
-                for (int g = 0; g < GP; g += 4)
-                    *reinterpret_cast<float4*>(to + g) = make_float4(s[g], s[g + 1], s[g + 2], s[g + 3]);
-                if (tid == 0)
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) p.tile_m[(size_t)(w.s + it) * GP + g] = m[g];
-            }
-            if (it >= 2) ok = ok && wait(&bar.p_free[buf], ((it - 2) >> 1) & 1);
-            unsigned char* pb = p_buf + buf * S::kPBytes + (tid >> 6) * (S::kPCols * 128) + (tid & 7) * 2;
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                uint16_t hi, lo;
-                if (p.c.bf16) {
-                    hi = from_float(s[g], 1);
-                    lo = from_float(s[g] - __uint_as_float((unsigned)hi << 16), 1);
-                } else {
-                    hi = from_float(s[g], 0);
-                    lo = from_float(s[g] - __half2float(__ushort_as_half(hi)), 0);
+                        for (int g = 0; g < GP; g += 4) tm[g / 4] = make_float4(m[g], m[g + 1], m[g + 2], m[g + 3]);
+                    }
                 }
-                const int at = (((tid & 63) >> 3) ^ (g & 7)) << 4;
-                *reinterpret_cast<uint16_t*>(pb + g * 128 + at) = hi;
-                *reinterpret_cast<uint16_t*>(pb + (GP + g) * 128 + at) = lo;
-            }
-            // The tile's copy in the ring: V(t) is item 2t + 2, but the last one is 2 * count - 1.
-            if (valid & 15) {
-                // Rows past the sequence's end inside the last step of 16: zero times NaN is NaN.
-                const int item_v = it + 1 < count ? 2 * it + 2 : 2 * count - 1;
-                ok = ok && wait(&bar.full[item_v % S::kRing], (item_v / S::kRing) & 1);
-                unsigned char* v = ring + (item_v % S::kRing) * S::kItem;
-                const int pad = (16 - (valid & 15)) * S::kSub * 8;
-                for (int i = tid; ok && i < pad; i += 128) {
-                    const int row = valid + i / (S::kSub * 8), sub = i / 8 % S::kSub;
-                    *reinterpret_cast<int4*>(v + sub * (kTile * 128) + row * 128 + (i & 7) * 16) = make_int4(0, 0, 0, 0);
+                uint32_t word[GP];  // hi of all heads, then lo
+#pragma unroll
+                for (int g = 0; g < GP; g += 2) {
+                    word[g / 2] = pack2(s[g], s[g + 1], p.c.bf16);
+                    const float2 hi = unpack2(word[g / 2], p.c.bf16);
+                    word[(GP + g) / 2] = pack2(s[g] - hi.x, s[g + 1] - hi.y, p.c.bf16);
                 }
+                if (it >= 2) ok = ok && wait(S::kPFree + buf, ((it >> 1) & 1) ^ 1);
+                const uint32_t row = p_buf + buf * S::kPBytes + tid * S::kPRow;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((i ^ turn) << 4)),
+                                 "r"(word[4 * i]), "r"(word[4 * i + 1]), "r"(word[4 * i + 2]), "r"(word[4 * i + 3])
+                                 : "memory");
+                if (valid & 15) {
+                    // Rows past the sequence's end inside the last step of 16: zero times NaN is NaN.
+                    const int item = it + 1 < count ? 2 * it + 2 : 2 * count - 1, st = item % S::kRing;
+                    ok = ok && wait(S::kFull + st, (item / S::kRing) & 1);
+                    const int pad = (16 - (valid & 15)) * S::kSub * 8;
+                    for (int i = tid; ok && i < pad; i += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + st * S::kItem + i / 8 % S::kSub * (kTile * 128) +
+                                         (valid + i / (S::kSub * 8)) * 128 + (i & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+                }
+                fence_proxy_async_smem();
+                mbar_arrive_at(bar0 + (S::kPReady + buf) * 8);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar.p_ready[buf]);
-            if (x.t + 1 < x.tiles && it + 1 < count) continue;
+            if (leave) break;
 
             // The end of the row's share: sums over the 128 slots' threads, then O.
-#pragma unroll
-            for (int g = 0; g < GP; ++g)
-                for (int d = 16; d; d >>= 1) l[g] += __shfl_xor_sync(kFullMask, l[g], d);
-            if (!bar_all(1, 128, ok)) break;  // and red is free again
-            if (lane == 0)
-#pragma unroll
-                for (int g = 0; g < GP; ++g) red[buf][warp][g] = l[g];
-            ok = wait(&bar.p_free[buf], (it >> 1) & 1);
-            if (!bar_all(1, 128, ok)) break;
-#pragma unroll
-            for (int g = 0; g < GP; ++g)
-                l[g] = (red[buf][0][g] + red[buf][1][g]) + (red[buf][2][g] + red[buf][3][g]);
+            const int final_it = it - 1;
+            const float sum = warp_sums<GP>(l, lane);
+            ok = ok && wait(S::kPFree + (final_it & 1), (final_it >> 1) & 1);
+            leave = bar_any(1, 128, !ok);
+            if (leave) break;
+            if ((lane & (32 / GP - 1)) == 0) red[warp][warp_head<GP>(lane)] = sum;
+            bar_sync(1, 128);
             tc_fence_after();
-            const int row_start = w.s + it - x.t;  // tile number of the row's first tile
+            const int row_start = tile0 - x.t;  // tile number of the row's first tile
             const bool whole = row_start >= w.s && row_start + x.tiles <= w.e;
             const int share = 2 * blockIdx.x + (row_start >= w.s ? 1 : 0);
-            const int q0 = x.b * p.a.q_heads + x.r / p.parts * p.group + part * GP;
+            const int q0 = x.b * p.a.q_heads + (p.parts == 1 ? x.r : x.r / p.parts) * p.group + part * GP;
+            float v[S::kOBlocks][2 * GP];
+#pragma unroll
+            for (int o = 0; o < S::kOBlocks; ++o)
+#pragma unroll
+                for (int g = 0; g < 2 * GP; g += 8) tmem_ld8(my_tmem + S::kTmemO + o * S::kPCols + g, v[o] + g);
+#pragma unroll
+            for (int g = 0; g < GP; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
+            tmem_wait_ld();
+            tc_fence_before();
             if (tid < heads) {
                 float mm = m[0], ll = l[0];
 #pragma unroll
@@ -492,6 +602,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                         mm = m[g];
                         ll = l[g];
                     }
+                if (ll != ll) mm = 0.f;  // a NaN sum says it all: keep it apart from an empty share
                 if (whole) {
                     p.row_ml[((size_t)x.b * p.rows + x.r) * GP + tid] = make_float2(mm, ll);
                     if (p.a.lse)
@@ -502,28 +613,22 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             }
 #pragma unroll
             for (int o = 0; o < S::kOBlocks; ++o) {
-                float hi[GP], lo[GP];
-                const uint32_t at = tmem + lane_base + S::kTmemO + o * S::kPCols;
-#pragma unroll
-                for (int g = 0; g < GP; g += 8) {
-                    tmem_ld8(at + g, hi + g);
-                    tmem_ld8(at + GP + g, lo + g);
-                }
-                tmem_wait_ld();
                 // 64 rows of a product lie in the first 16 lanes of each warp's 32.
                 const int d = S::kM == 64 ? warp * 16 + lane : o * 128 + tid;
                 if ((S::kM == 64 && lane >= 16) || d >= p.c.dim) continue;
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    if (g >= heads) continue;
-                    const float v = hi[g] + lo[g];
+                    if (g >= heads) break;
+                    const float y = v[o][g] + v[o][GP + g];
                     if (whole)
-                        p.a.out[(size_t)(q0 + g) * p.c.dim + d] = from_float(l[g] == 0.f ? 0.f : v / l[g], p.c.bf16);
+                        p.a.out[(size_t)(q0 + g) * p.c.dim + d] =
+                            from_float(l[g] == 0.f ? 0.f : y * __frcp_rn(l[g]), p.c.bf16);
                     else
-                        p.part_o[((size_t)share * GP + g) * p.c.dim + d] = v;
+                        p.part_o[((size_t)share * GP + g) * p.c.dim + d] = y;
                 }
             }
-            tc_fence_before();
+            x.t += n - 1;
+            x.next(p);
         }
     }
     __syncthreads();
@@ -536,7 +641,8 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
 // that block c of the first launch had, so its p may still be in L2.
 template <int GP>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs p) {
-    __shared__ int scan[kJoinThreads / 32 + 8];
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ int scan[kWarps + 8];
     __shared__ float2 ml[GP];
     __shared__ float acc[kJoinThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -554,32 +660,37 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs 
         const int count = min(w.tiles - w.t, w.e - tile);  // this block's tiles of the row
         const int row_start = tile - w.t, part = w.r % p.parts, h = w.r / p.parts;
         const int c0 = w.block_of(row_start), c1 = w.block_of(row_start + w.tiles - 1);
-        // Statistics of part `pt` of the row's group into ml[]: reference and 1 / sum (0 for an empty row).
+        // Statistics of part `pt` of the row's group into ml[]: reference and sum (0 for an empty row).
         auto stats = [&](int pt) {
             const int start = row_start + (pt - part) * w.tiles;
             const int a0 = w.block_of(start), a1 = w.block_of(start + w.tiles - 1);
             const int heads = min(GP, p.group - pt * GP);
             __syncthreads();
-            for (int g = warp; g < heads; g += kJoinThreads / 32) {
+            for (int g = warp; g < heads; g += kWarps) {
                 float top = -INFINITY, sum = 0.f;
                 if (a0 == a1) {
                     const float2 v = p.row_ml[((size_t)w.b * p.rows + h * p.parts + pt) * GP + g];
                     top = v.x;
                     sum = v.y;
                 } else {
-                    for (int c = a0 + lane; c <= a1; c += 32) top = fmaxf(top, p.part_ml[(2 * c + (c == a0)) * GP + g].x);
-                    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
                     for (int c = a0 + lane; c <= a1; c += 32) {
                         const float2 v = p.part_ml[(2 * c + (c == a0)) * GP + g];
-                        if (v.x != -INFINITY) sum += v.y * exp2f(v.x - top);
+                        if (v.x == -INFINITY) continue;
+                        const float to = fmaxf(top, v.x);
+                        sum = (top == -INFINITY ? 0.f : sum * exp2f(top - to)) + v.y * exp2f(v.x - to);
+                        top = to;
                     }
+                    const float all = warp_max(top);
+                    sum = top == -INFINITY ? 0.f : sum * exp2f(top - all);
                     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+                    top = all;
                 }
                 if (lane == 0) ml[g] = make_float2(top, sum);
             }
             __syncthreads();
         };
-        stats(part);
+        const bool weights = p.p && part == 0;
+        if (c0 != c1 || weights) stats(part);
         if (c0 != c1) {
             const int heads = min(GP, p.group - part * GP);
             const int q0 = w.b * p.a.q_heads + h * p.group + part * GP;
@@ -591,8 +702,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs 
             // threads share its elements, and the row's pieces where threads are left.
             const int elements = heads * p.c.dim, blocks = c1 - c0 + 1;
             const int each = (elements + blocks - 1) / blocks;
-            const int width = each > 128 ? 256 : each > 64 ? 128 : each > 32 ? 64 : 32, ways = kJoinThreads / width;
-            const int from = (block - c0) * each, to = min(from + each, elements);
+            const int width = each > 256 ? 512 : each > 128 ? 256 : each > 64 ? 128 : each > 32 ? 64 : 32;
+            const int ways = kJoinThreads / width, from = (block - c0) * each, to = min(from + each, elements);
             for (int e0 = from; e0 < to; e0 += width) {
                 const int i = e0 + tid % width, g = min(i / p.c.dim, heads - 1);
                 const float top = ml[g].x;
@@ -604,44 +715,54 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs 
                         const float x = p.part_ml[share * GP + g].x, v = p.part_o[(size_t)share * GP * p.c.dim + i];
                         o += x == -INFINITY ? 0.f : v * exp2f(x - top);
                     }
-                __syncthreads();
-                acc[tid] = o;
-                __syncthreads();
-                if (tid < width && i < to) {
-                    for (int k = 1; k < ways; ++k) o += acc[k * width + tid];
-                    p.a.out[(size_t)q0 * p.c.dim + i] = from_float(ml[g].y == 0.f ? 0.f : o / ml[g].y, p.c.bf16);
+                if (ways > 1) {
+                    __syncthreads();
+                    acc[tid] = o;
+                    __syncthreads();
+                    if (tid < width)
+                        for (int k = 1; k < ways; ++k) o += acc[k * width + tid];
                 }
+                if (tid < width && i < to)
+                    p.a.out[(size_t)q0 * p.c.dim + i] = from_float(ml[g].y == 0.f ? 0.f : o / ml[g].y, p.c.bf16);
             }
         }
-        if (p.p && part == 0) {
+        if (weights) {
             const float* wi = p.a.weight.row(w.b, h);
             float* wo = p.a.weight_out.row(w.b, h);
             for (int pt = 0; pt < p.parts; ++pt) {
                 if (pt > 0) stats(pt);
                 const int heads = min(GP, p.group - pt * GP);
-                for (int k = warp; k < count; k += kJoinThreads / 32) {
+                const float2 mine = lane < heads ? ml[lane] : make_float2(0.f, 0.f);
+                for (int k = warp; k < count; k += kWarps) {
+                    // A warp takes a tile; all its loads are in flight at once.
                     const size_t x = tile + k + (size_t)pt * w.tiles;
-                    float f[GP];
+                    const int slot0 = (w.t + k) * kTile + lane;
+                    const float4* v = reinterpret_cast<const float4*>(p.p + (x * kTile + lane) * GP);
+                    const float tm = lane < heads ? p.tile_m[x * GP + lane] : -INFINITY;
+                    float4 y[4][GP / 4];
+                    float old[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int g = 0; g < GP / 4; ++g) y[i][g] = v[i * 32 * (GP / 4) + g];
+                        const int slot = slot0 + i * 32;
+                        old[i] = slot < w.n ? (pt == 0 ? wi[slot] : wo[slot]) : 0.f;
+                    }
+                    float f = 0.f;
+                    if (tm != -INFINITY && mine.y != 0.f) f = exp2f(tm - mine.x) / mine.y;
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
-                        f[g] = 0.f;
-                        if (g < heads) {
-                            const float tm = p.tile_m[x * GP + g];
-                            if (tm != -INFINITY && ml[g].y != 0.f) f[g] = exp2f(tm - ml[g].x) / ml[g].y;
-                        }
-                    }
-                    for (int i = 0; i < 4; ++i) {
-                        const int in = i * 32 + lane, slot = (w.t + k) * kTile + in;
-                        if (slot >= w.n) break;
-                        const float4* v = reinterpret_cast<const float4*>(p.p + (x * kTile + in) * GP);
-                        float sum = 0.f;
+                        const float fg = __shfl_sync(kFullMask, f, g);
+                        if (g >= heads) continue;
 #pragma unroll
-                        for (int g = 0; g < GP; g += 4) {
-                            const float4 y = v[g / 4];
-                            sum += y.x * f[g] + y.y * f[g + 1] + y.z * f[g + 2] + y.w * f[g + 3];
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 q = y[i][g / 4];
+                            old[i] = fmaf(g % 4 == 0 ? q.x : g % 4 == 1 ? q.y : g % 4 == 2 ? q.z : q.w, fg, old[i]);
                         }
-                        wo[slot] = (pt == 0 ? wi[slot] : wo[slot]) + sum;
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (slot0 + i * 32 < w.n) wo[slot0 + i * 32] = old[i];
                 }
             }
         }
@@ -735,7 +856,6 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
 template <int DP, int GP>
 cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, int* launches) {
     using Sh = Shape<DP, GP>;
-    static_assert(Sh::kRing <= 12, "ring barriers");
     auto kernel = kv_attend_kernel<DP, GP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;

@@ -11,36 +11,39 @@
 
 namespace topk {
 
-// Shared-memory operand descriptor, 128-byte swizzle.  Rows of 128 bytes
-// (64 16-bit elements) in groups of eight.  K-major operands: `sbo` is the
-// distance between groups of eight rows and `lbo` is not used.  MN-major
-// operands (a row is one k, its 64 elements run along M or N): `sbo` is the
-// distance between groups of eight k, `lbo` between blocks of 64 along M or N.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+// Shared-memory operand descriptors, as two words.  An operand lies in rows
+// of 128, 64 or 32 bytes, swizzled over their width, in groups of eight.
+// K-major: a row holds consecutive k of one m (or n); `sbo` is the distance
+// between groups of eight rows.  MN-major: a row holds consecutive m (or n)
+// of one k; `sbo` is the distance between groups of eight k and `lbo` that
+// between blocks of a row's width along m (or n).  All in bytes, multiples of
+// 16; the low word takes an offset of the start address by addition.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t smem_desc_hi(uint32_t sbo, int row_bytes) {
+    return (sbo >> 4) | 1u << 14 | (row_bytes == 128 ? 2u : row_bytes == 64 ? 4u : 6u) << 29;
 }
 
 // Instruction descriptor of kind::f16: f32 accumulator, A and B of one 16-bit
-// type, B K-major, A K-major or (a_mn) MN-major.
-__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int m, int n, bool a_mn) {
-    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+// type, both K-major or (mn) both MN-major.
+__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int m, int n, bool mn) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((mn ? 3u : 0u) << 15) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // D[tmem] = A * B (+ D if accumulate); one thread issues it.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
 // Arrive on `bar` once every MMA that this thread issued before has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Whole-warp allocation of tensor memory columns (a power of two, at least
@@ -76,20 +79,42 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const float* r) {
 
 // Tensor-map loads of one box into shared memory; x times the element size
 // is a multiple of 16 bytes.  Parts outside the tensor read as zero.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar, uint64_t policy) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "l"(policy)
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Barriers by their shared-memory address.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // The largest of a warp's values (NaNs are passed over unless all are NaN).
@@ -105,17 +130,19 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// A barrier of `threads` threads, and whether `ok` held for all of them: the
-// way a group of warps leaves a loop together after a wait gave up in some.
-__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
-    uint32_t all;
+// A barrier of `threads` threads, and whether `any` held for one of them.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool any) {
+    uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-        "bar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(all)
-        : "r"(id), "r"(threads), "r"((uint32_t)ok)
+        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)any)
         : "memory");
-    return all != 0;
+    return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace topk
