@@ -1,159 +1,333 @@
 // topk_kv_evict: keep the `budget` best slots of each (sequence, head).
 //
-// Two launches.  The first selects: a radix select over 32-bit keys (8-bit
-// digits) finds the budget-th key, and a pass in slot order lists the holes
-// below the budget and the kept slots above it.  The second moves the kept
-// slots into the holes.  Sources lie at or above the budget and targets below
-// it, so the moves cannot collide and need no order.
+// Bound by HBM: a weight and a position are read per slot, and a kept slot
+// above the budget is read and written once.  Two launches.
+//
+// The first selects.  A row belongs to a cluster of 1 to 8 blocks, each with
+// a contiguous part of its slots, whose 32-bit keys it reads once and keeps
+// in shared memory.  Three histograms of 11, 11 and 10 bits, added up over
+// the cluster by reading one another's shared memory, give the budget-th key
+// ("edge") and how many keys equal to it are kept.  Then, with K(s) the
+// number of kept slots below s, which is a prefix sum of counts,
+//     slot s < budget that is not kept is hole number s - K(s),
+//     slot s >= budget that is kept is kept slot number K(s),
+// and hole j takes kept slot number K(budget) + j.  So holes and movers are
+// listed in order without sorting anything.
+//
+// The second moves the movers into the holes.  Sources lie at or above the
+// budget and targets below it, so the moves cannot collide and need no order.
+#include <cooperative_groups.h>
+
 #include "topk_device.cuh"
 #include "topk_kv.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace topk {
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kBins = 2048;
+constexpr int kMoveThreads = 256;
 
 struct EvictArgs {
     KvCache c;
     KvEvict e;
     int* lens;    // [seqs] lengths before, clamped
-    int* moves;   // [seqs * heads] number of moves
-    int* holes;   // [seqs * heads][room]
-    int* movers;  // [seqs * heads][room]
+    int* moves;   // [seqs * heads] number of moves M of each row
+    int* holes;   // [seqs * heads][room]: holes 0 to M - 1
+    int* movers;  // [seqs * heads][room]: the movers, in the row's last M places
     int room;     // moves a row's lists have room for
     int chunks;   // blocks of the second launch per row
+    int part;     // slots a block of the first has room for in shared memory
 };
 
 // Order-preserving key: protected above NaN above every number, -0 equal to +0.
-__device__ __forceinline__ unsigned evict_key(const EvictArgs& a, float w, int pos, int next_pos) {
-    if (pos < a.e.sink || (long long)pos >= (long long)next_pos - a.e.recent) return 0xFFFFFFFFu;
+__device__ __forceinline__ unsigned evict_key(float w, int pos, int sink, long long recent_from) {
+    if (pos < sink || pos >= recent_from) return 0xFFFFFFFFu;
     if (w != w) return 0xFFFFFFFEu;
     const unsigned u = __float_as_uint(w + 0.0f);
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix of v over the block's threads, and the total in *total.
-__device__ int block_scan(int v, int* warp_sums, int* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(kFullMask, x, d);
-        if (lane >= d) x += y;
+// Count one bin; a warp whose lanes all count the same bin (rows of equal or
+// protected slots) adds once, which spares it 32 turns at one address.
+__device__ __forceinline__ void count_bin(int* hist, int bin, bool on, int lane) {
+    const unsigned active = __ballot_sync(kFullMask, on);
+    if (!active) return;
+    const int leader = __ffs(active) - 1;
+    const int first = __shfl_sync(kFullMask, bin, leader);
+    if (__ballot_sync(kFullMask, on && bin == first) == active) {
+        if (lane == leader) atomicAdd(&hist[first], __popc(active));
+    } else if (on) {
+        atomicAdd(&hist[bin], 1);
     }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    *total = all;
-    return before + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[kSelThreads / 32];
-    __shared__ unsigned s_prefix;
-    __shared__ int s_need;
-    const int row = blockIdx.x, b = row / a.c.heads, h = row % a.c.heads;
-    const int n = a.c.len(b), next_pos = a.e.next_pos[b], budget = a.e.budget;
+// kHeld: the block's keys fit its shared memory; otherwise they are made anew
+// from global memory (L2) in each pass.
+template <int THREADS, bool kHeld>
+__global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
+    constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;
+    extern __shared__ unsigned keys[];
+    __shared__ int hist[3][kBins];
+    __shared__ int scan[kWarps];
+    __shared__ int found[2];                       // the bin, and how many of its keys are kept
+    __shared__ int tally[4];                       // this block: above and at the edge; the same below the budget
+    __shared__ int warp_above[kWarps], warp_ties[kWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int row = blockIdx.x / blocks, b = row / a.c.heads, h = row % a.c.heads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = a.c.len(b), budget = a.e.budget;
     const float* w = a.e.weight.row(b, h);
     const int* pos = a.e.pos.row(b, h);
     float* wo = a.e.weight_out.row(b, h);
     int* po = a.e.pos_out.row(b, h);
-    const int tid = threadIdx.x;
-    if (tid == 0 && h == 0) a.lens[b] = n;
-    if (n <= budget) {
-        for (int i = tid; i < n; i += kSelThreads) {
-            wo[i] = w[i];
-            po[i] = pos[i];
+    const bool copy_w = wo != w, copy_p = po != pos;
+    launch_dependents();  // the moves wait for this launch's end
+    if (tid == 0 && h == 0 && rank == 0) a.lens[b] = n;
+    // This block's slots: multiples of the warps' rounds.
+    const int part = ((n + blocks - 1) / blocks + 31) & ~31, lo = min(rank * part, n), hi = min(lo + part, n);
+    if (n <= budget) {  // the whole cluster leaves here
+        for (int i = lo + tid; i < hi; i += THREADS) {
+            if (copy_w) wo[i] = w[i];
+            if (copy_p) po[i] = pos[i];
         }
-        if (tid == 0) a.moves[row] = 0;
+        if (tid == 0 && rank == 0) a.moves[row] = 0;
         return;
     }
-    if (tid == 0) {
-        s_prefix = 0;
-        s_need = budget;
-    }
+    const int sink = a.e.sink;
+    const long long recent_from = (long long)a.e.next_pos[b] - a.e.recent;
+    for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
+    if (tid < 4) tally[tid] = 0;
     __syncthreads();
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        const unsigned prefix = s_prefix;
-        const int need = s_need;
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
-            const unsigned key = evict_key(a, w[i], pos[i], next_pos);
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
+    auto key_at = [&](int i) { return kHeld ? keys[i - lo] : evict_key(w[i], pos[i], sink, recent_from); };
+
+    for (int base = lo; base < hi; base += 4 * THREADS) {
+        float wv[4];
+        int pv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = base + j * THREADS + tid;
+            wv[j] = i < hi ? w[i] : 0.f;
+            pv[j] = i < hi ? pos[i] : 0;
         }
-        __syncthreads();
-        if (tid == 0) {
-            int left = need, d = 255;
-            while (d > 0 && hist[d] < left) left -= hist[d--];
-            s_prefix = prefix | ((unsigned)d << shift);
-            s_need = left;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = base + j * THREADS + tid;
+            const unsigned key = evict_key(wv[j], pv[j], sink, recent_from);
+            if (i < hi) {
+                if (kHeld) keys[i - lo] = key;
+                if (i < budget) {
+                    if (copy_w) wo[i] = wv[j];
+                    if (copy_p) po[i] = pv[j];
+                }
+            }
+            count_bin(hist[0], key >> 21, i < hi, lane);
         }
-        __syncthreads();
     }
-    const unsigned edge = s_prefix;
-    const int ties = s_need;  // keys equal to `edge` to keep, lowest slots first
-    int tie_base = 0, hole_base = 0, mover_base = 0;
+    unsigned prefix = 0;
+    int need = budget;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        constexpr int kShift[3] = {21, 10, 0}, kWidth[3] = {kBins, kBins, kBins / 2};
+        if (pass > 0) {
+            for (int base = lo; base < hi; base += THREADS) {
+                const int i = base + tid;
+                const unsigned key = i < hi ? key_at(i) : 0;
+                const int up = kShift[pass - 1];
+                count_bin(hist[pass], (key >> kShift[pass]) & (kWidth[pass] - 1), i < hi && (key >> up) == (prefix >> up),
+                          lane);
+            }
+        }
+        if (blocks > 1) cluster.sync(); else __syncthreads();
+        // Thread t sums bins from the top: kPer of them, t = 0 the highest.
+        int own[kPer], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int bin = kBins - 1 - (tid * kPer + j);
+            int v = 0;
+            if (blocks == 1) {
+                v = hist[pass][bin];
+            } else {
+                for (int r = 0; r < blocks; ++r) v += cluster.map_shared_rank(&hist[pass][0], r)[bin];
+            }
+            own[j] = v;
+            sum += v;
+        }
+        int x = sum;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFullMask, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int before = x - sum;
+        for (int v = 0; v < warp; ++v) before += scan[v];
+        if (before < need && need <= before + sum) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (before < need && need <= before + own[j]) {
+                    found[0] = kBins - 1 - (tid * kPer + j);
+                    found[1] = need - before;
+                }
+                before += own[j];
+            }
+        }
+        __syncthreads();
+        prefix |= (unsigned)found[0] << kShift[pass];
+        need = found[1];
+    }
+    const unsigned edge = prefix;  // keys above it are kept, and the first `need` that equal it
+
+    // Counts, by warps with a contiguous part each.
+    const int mine = ((part + kWarps - 1) / kWarps + 31) & ~31;
+    const int from = min(lo + warp * mine, hi), to = min(from + mine, hi);
+    int above = 0, ties = 0, above_low = 0, ties_low = 0;
+    for (int base = from; base < to; base += 32) {
+        const int i = base + lane;
+        const unsigned key = i < to ? key_at(i) : 0;
+        const unsigned up = __ballot_sync(kFullMask, i < to && key > edge);
+        const unsigned at = __ballot_sync(kFullMask, i < to && key == edge);
+        const int under = budget - base;
+        const unsigned low = under >= 32 ? kFullMask : under <= 0 ? 0u : (1u << under) - 1;
+        above += __popc(up);
+        ties += __popc(at);
+        above_low += __popc(up & low);
+        ties_low += __popc(at & low);
+    }
+    if (lane == 0) {
+        warp_above[warp] = above;
+        warp_ties[warp] = ties;
+        atomicAdd(&tally[0], above);
+        atomicAdd(&tally[1], ties);
+        atomicAdd(&tally[2], above_low);
+        atomicAdd(&tally[3], ties_low);
+    }
+    if (blocks > 1) cluster.sync(); else __syncthreads();
+    int up_before = 0, ties_before = 0, up_low = 0, all_ties_low = 0;
+    for (int r = 0; r < blocks; ++r) {
+        const int* t = blocks == 1 ? tally : cluster.map_shared_rank(&tally[0], r);
+        if (r < rank) {
+            up_before += t[0];
+            ties_before += t[1];
+        }
+        up_low += t[2];
+        all_ties_low += t[3];
+    }
+    for (int v = 0; v < warp; ++v) {
+        up_before += warp_above[v];
+        ties_before += warp_ties[v];
+    }
+    if (tid == 0 && rank == 0) a.moves[row] = budget - up_low - min(all_ties_low, need);
     int* holes = a.holes + (size_t)row * a.room;
-    int* movers = a.movers + (size_t)row * a.room;
-    for (int base = 0; base < n; base += kSelThreads) {
-        const int i = base + tid;
-        const unsigned key = i < n ? evict_key(a, w[i], pos[i], next_pos) : 0;
-        const bool tie = i < n && key == edge;
-        int total;
-        const int rank = tie_base + block_scan(tie, warp_sums, &total);
-        tie_base += total;
-        const bool kept = i < n && (key > edge || (tie && rank < ties));
-        const bool hole = i < n && i < budget && !kept, mover = kept && i >= budget;
-        if (kept && i < budget) {
-            wo[i] = w[i];
-            po[i] = pos[i];
+    int* movers = a.movers + (size_t)row * a.room + (a.room - budget);
+    for (int base = from; base < to; base += 32) {
+        const int i = base + lane;
+        const unsigned key = i < to ? key_at(i) : 0;
+        const unsigned up = __ballot_sync(kFullMask, i < to && key > edge);
+        const unsigned at = __ballot_sync(kFullMask, i < to && key == edge);
+        const int t = ties_before + __popc(at & lanemask_lt());
+        const int kept_before = up_before + __popc(up & lanemask_lt()) + min(t, need);
+        const bool kept = key > edge || (key == edge && t < need);
+        if (i < to) {
+            if (i < budget) {
+                if (!kept) holes[i - kept_before] = i;
+            } else if (kept) {
+                movers[kept_before] = i;
+            }
         }
-        const int hr = hole_base + block_scan(hole, warp_sums, &total);
-        hole_base += total;
-        if (hole) holes[hr] = i;
-        const int mr = mover_base + block_scan(mover, warp_sums, &total);
-        mover_base += total;
-        if (mover) movers[mr] = i;
+        up_before += __popc(up);
+        ties_before += __popc(at);
     }
-    if (tid == 0) a.moves[row] = mover_base;
+    if (blocks > 1) cluster.sync();  // no block leaves while another reads its counts
 }
 
-__global__ void __launch_bounds__(256) kv_move_kernel(const EvictArgs a) {
+// A warp takes 32 moves: a lane looks up one move's pages, then all lanes
+// copy the 32 moves' vectors, kUnroll of them in flight per lane.
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
+    constexpr int kUnroll = 8;
+    __shared__ int4 where[kMoveThreads / 32][32];  // source page and slot in it, target page and slot
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, b = row / a.c.heads, h = row % a.c.heads;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int vecs = a.c.dim / 8;  // 16-byte vectors of a key
+    const uint16_t *k = a.c.k + h * a.c.ks[2], *v = a.c.v + h * a.c.vs[2];
+    grid_dependency_wait();
     if (chunk == 0 && h == 0 && threadIdx.x == 0) {
         const int n = a.lens[b];
         a.e.lens_out[b] = n < a.e.budget ? n : a.e.budget;
     }
     const int moves = a.moves[row];
-    for (int j = chunk * 8 + (threadIdx.x >> 5); j < moves; j += a.chunks * 8) {
-        const int to = a.holes[(size_t)row * a.room + j], from = a.movers[(size_t)row * a.room + j];
-        if (lane == 0) {
+    const int* holes = a.holes + (size_t)row * a.room;
+    const int* movers = a.movers + (size_t)row * a.room + (a.room - moves);
+    for (int j0 = (chunk * (kMoveThreads / 32) + warp) * 32; j0 < moves; j0 += a.chunks * kMoveThreads) {
+        const int j = j0 + lane;
+        int4 at = make_int4(-1, 0, -1, 0);
+        if (j < moves) {
+            const int from = movers[j], to = holes[j];
+            const int fi = from / a.c.page_size, ti = to / a.c.page_size;
+            const int* table = a.c.table + b * a.c.table_stride;
+            at = make_int4(table[fi], from - fi * a.c.page_size, table[ti], to - ti * a.c.page_size);
             a.e.weight_out.row(b, h)[to] = a.e.weight.row(b, h)[from];
             a.e.pos_out.row(b, h)[to] = a.e.pos.row(b, h)[from];
+            // A move from or to a page that the table does not name is dropped.
+            if ((unsigned)at.x >= (unsigned)a.c.pages || (unsigned)at.z >= (unsigned)a.c.pages) at.x = -1;
         }
-        const int dp = a.c.page_of(b, to), sp = a.c.page_of(b, from);
-        if (dp < 0 || sp < 0) continue;
-        const int ds = to % a.c.page_size, ss = from % a.c.page_size;
-        const bool v = lane >= 16;
-        uint16_t* pool = v ? a.c.v : a.c.k;
-        const long long* st = v ? a.c.vs : a.c.ks;
-        uint16_t* dst = pool + dp * st[0] + ds * st[1] + h * st[2];
-        const uint16_t* src = pool + sp * st[0] + ss * st[1] + h * st[2];
-        for (int x = (lane & 15) * 8; x < a.c.dim; x += 128)
-            *reinterpret_cast<int4*>(dst + x) = *reinterpret_cast<const int4*>(src + x);
+        __syncwarp();
+        where[warp][lane] = at;
+        __syncwarp();
+        const int total = min(32, moves - j0) * 2 * vecs;
+        for (int i0 = lane; i0 < total; i0 += 32 * kUnroll) {
+            int4 data[kUnroll];
+            uint16_t* dst[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + 32 * u, m = i / (2 * vecs), in = i - m * 2 * vecs;
+                dst[u] = nullptr;
+                if (i < total) {
+                    const int4 q = where[warp][m];
+                    if (q.x >= 0) {
+                        const bool second = in >= vecs;
+                        const uint16_t* base = second ? v : k;
+                        const long long page = second ? a.c.vs[0] : a.c.ks[0], slot = second ? a.c.vs[1] : a.c.ks[1];
+                        const int x = (second ? in - vecs : in) * 8;
+                        data[u] = *reinterpret_cast<const int4*>(base + q.x * page + q.y * slot + x);
+                        dst[u] = const_cast<uint16_t*>(base) + q.z * page + q.w * slot + x;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (dst[u]) *reinterpret_cast<int4*>(dst[u]) = data[u];
+        }
     }
 }
 
 int room_of(const KvCache& c, const KvEvict& e) {
     const int above = c.capacity() - e.budget;
     return above < 1 ? 1 : above < e.budget ? above : e.budget;
+}
+
+template <int THREADS, bool kHeld>
+cudaError_t select(const EvictArgs& a, int rows, int blocks, cudaStream_t s) {
+    auto kernel = kv_select_kernel<THREADS, kHeld>;
+    const size_t smem = kHeld ? (size_t)a.part * 4 : 0;
+    if (smem > 16 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * blocks));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -172,15 +346,25 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     a.moves = a.lens + c.seqs;
     a.holes = a.moves + rows;
     a.movers = a.holes + (size_t)rows * a.room;
-    kv_select_kernel<<<rows, kSelThreads, 0, s>>>(a);
-    cudaError_t err = cudaGetLastError();
+    // Blocks per row: as many as keep the SMs busy twice over, and leave each
+    // block 1024 slots at least.
+    constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
+    int blocks = 1;
+    while (blocks < 8 && (rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024)) blocks *= 2;
+    while (blocks < 8 && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
+    a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
+    const bool held = a.part <= kMostHeld;
+    cudaError_t err;
+    if (rows * blocks <= 304)
+        err = held ? select<1024, true>(a, rows, blocks, s) : select<1024, false>(a, rows, blocks, s);
+    else
+        err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
     if (err != cudaSuccess) return err;
     ++*launches;
-    a.chunks = (a.room + 63) / 64;
+    a.chunks = (a.room + kMoveThreads - 1) / kMoveThreads;
     const long long most = (1 << 20) / rows + 1;
     if (a.chunks > most) a.chunks = (int)most;
-    kv_move_kernel<<<rows * a.chunks, 256, 0, s>>>(a);
-    err = cudaGetLastError();
+    err = launch_pdl(kv_move_kernel, dim3(rows * a.chunks), dim3(kMoveThreads), 0, s, a);
     if (err == cudaSuccess) ++*launches;
     return err;
 }
