@@ -68,7 +68,7 @@ __device__ __forceinline__ void count_bin(int* hist, int bin, bool on, int lane)
 template <int THREADS, bool kHeld>
 __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;
-    extern __shared__ unsigned keys[];
+    extern __shared__ __align__(16) unsigned keys[];
     __shared__ int hist[3][kBins];
     __shared__ int scan[kWarps];
     __shared__ int found[2];                       // the bin, and how many of its keys are kept
@@ -101,9 +101,26 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
     if (tid < 4) tally[tid] = 0;
     __syncthreads();
-    auto key_at = [&](int i) { return kHeld ? keys[i - lo] : evict_key(w[i], pos[i], sink, recent_from); };
+    // The key of slot i of this block's part; past its end 0, which is no
+    // slot's key, below every edge, and never in an edge's bin.
+    auto key_at = [&](int i) {
+        return kHeld ? keys[i - lo] : i < hi ? evict_key(w[i], pos[i], sink, recent_from) : 0u;
+    };
+    const int end = lo < hi ? lo + part : lo;  // a multiple of 32 slots
+    auto keys_at = [&](int i, int stop, unsigned (&key)[4]) {  // slots i to i + 3
+        if (kHeld) {
+            const uint4 q = i < stop ? *reinterpret_cast<const uint4*>(keys + (i - lo)) : make_uint4(0, 0, 0, 0);
+            key[0] = q.x;
+            key[1] = q.y;
+            key[2] = q.z;
+            key[3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) key[j] = i < stop ? key_at(i + j) : 0;
+        }
+    };
 
-    for (int base = lo; base < hi; base += 4 * THREADS) {
+    for (int base = lo; base < end; base += 4 * THREADS) {
         float wv[4];
         int pv[4];
 #pragma unroll
@@ -115,13 +132,11 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = base + j * THREADS + tid;
-            const unsigned key = evict_key(wv[j], pv[j], sink, recent_from);
-            if (i < hi) {
-                if (kHeld) keys[i - lo] = key;
-                if (i < budget) {
-                    if (copy_w) wo[i] = wv[j];
-                    if (copy_p) po[i] = pv[j];
-                }
+            const unsigned key = i < hi ? evict_key(wv[j], pv[j], sink, recent_from) : 0;
+            if (kHeld && i < end) keys[i - lo] = key;
+            if (i < hi && i < budget) {
+                if (copy_w) wo[i] = wv[j];
+                if (copy_p) po[i] = pv[j];
             }
             count_bin(hist[0], key >> 21, i < hi, lane);
         }
@@ -132,12 +147,17 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     for (int pass = 0; pass < 3; ++pass) {
         constexpr int kShift[3] = {21, 10, 0}, kWidth[3] = {kBins, kBins, kBins / 2};
         if (pass > 0) {
-            for (int base = lo; base < hi; base += THREADS) {
-                const int i = base + tid;
-                const unsigned key = i < hi ? key_at(i) : 0;
-                const int up = kShift[pass - 1];
-                count_bin(hist[pass], (key >> kShift[pass]) & (kWidth[pass] - 1), i < hi && (key >> up) == (prefix >> up),
-                          lane);
+            const int up = kShift[pass - 1];
+            for (int base = lo; base < end; base += 4 * THREADS) {
+                unsigned key[4];
+                bool in[4];
+                keys_at(base + 4 * tid, end, key);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) in[j] = ((key[j] ^ prefix) >> up) == 0;
+                if (!__any_sync(kFullMask, in[0] || in[1] || in[2] || in[3])) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    count_bin(hist[pass], (key[j] >> kShift[pass]) & (kWidth[pass] - 1), in[j], lane);
             }
         }
         if (blocks > 1) cluster.sync(); else __syncthreads();
@@ -181,21 +201,26 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     const unsigned edge = prefix;  // keys above it are kept, and the first `need` that equal it
 
     // Counts, by warps with a contiguous part each.
-    const int mine = ((part + kWarps - 1) / kWarps + 31) & ~31;
-    const int from = min(lo + warp * mine, hi), to = min(from + mine, hi);
+    const int mine = ((part + kWarps - 1) / kWarps + 127) & ~127;
+    const int from = min(lo + warp * mine, end), to = min(from + mine, end);
     int above = 0, ties = 0, above_low = 0, ties_low = 0;
-    for (int base = from; base < to; base += 32) {
-        const int i = base + lane;
-        const unsigned key = i < to ? key_at(i) : 0;
-        const unsigned up = __ballot_sync(kFullMask, i < to && key > edge);
-        const unsigned at = __ballot_sync(kFullMask, i < to && key == edge);
-        const int under = budget - base;
-        const unsigned low = under >= 32 ? kFullMask : under <= 0 ? 0u : (1u << under) - 1;
-        above += __popc(up);
-        ties += __popc(at);
-        above_low += __popc(up & low);
-        ties_low += __popc(at & low);
+    for (int base = from; base < to; base += 128) {
+        const int i = base + 4 * lane;
+        unsigned key[4];
+        keys_at(i, to, key);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int up = key[j] > edge, at = key[j] == edge;
+            above += up;
+            ties += at;
+            above_low += i + j < budget ? up : 0;
+            ties_low += i + j < budget ? at : 0;
+        }
     }
+    above = __reduce_add_sync(kFullMask, above);
+    ties = __reduce_add_sync(kFullMask, ties);
+    above_low = __reduce_add_sync(kFullMask, above_low);
+    ties_low = __reduce_add_sync(kFullMask, ties_low);
     if (lane == 0) {
         warp_above[warp] = above;
         warp_ties[warp] = ties;
@@ -222,23 +247,27 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     if (tid == 0 && rank == 0) a.moves[row] = budget - up_low - min(all_ties_low, need);
     int* holes = a.holes + (size_t)row * a.room;
     int* movers = a.movers + (size_t)row * a.room + (a.room - budget);
-    for (int base = from; base < to; base += 32) {
-        const int i = base + lane;
-        const unsigned key = i < to ? key_at(i) : 0;
-        const unsigned up = __ballot_sync(kFullMask, i < to && key > edge);
-        const unsigned at = __ballot_sync(kFullMask, i < to && key == edge);
-        const int t = ties_before + __popc(at & lanemask_lt());
-        const int kept_before = up_before + __popc(up & lanemask_lt()) + min(t, need);
-        const bool kept = key > edge || (key == edge && t < need);
-        if (i < to) {
+    for (int base = from; base < to; base += 128) {
+        unsigned key[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key[j] = base + j * 32 < to ? key_at(base + j * 32 + lane) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (base + j * 32 >= to) break;
+            const int i = base + j * 32 + lane;
+            const unsigned up = __ballot_sync(kFullMask, key[j] > edge);
+            const unsigned at = __ballot_sync(kFullMask, key[j] == edge);
+            const int t = ties_before + __popc(at & lanemask_lt());
+            const int kept_before = up_before + __popc(up & lanemask_lt()) + min(t, need);
+            const bool kept = key[j] > edge || (key[j] == edge && t < need);
             if (i < budget) {
                 if (!kept) holes[i - kept_before] = i;
             } else if (kept) {
                 movers[kept_before] = i;
             }
+            up_before += __popc(up);
+            ties_before += __popc(at);
         }
-        up_before += __popc(up);
-        ties_before += __popc(at);
     }
     if (blocks > 1) cluster.sync();  // no block leaves while another reads its counts
 }
@@ -355,7 +384,7 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
     const bool held = a.part <= kMostHeld;
     cudaError_t err;
-    if (rows * blocks <= 304)
+    if (rows * blocks <= 152)
         err = held ? select<1024, true>(a, rows, blocks, s) : select<1024, false>(a, rows, blocks, s);
     else
         err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
