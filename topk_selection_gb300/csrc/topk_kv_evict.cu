@@ -18,6 +18,8 @@
 // budget and targets below it, so the moves cannot collide and need no order.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "topk_device.cuh"
 #include "topk_kv.cuh"
 
@@ -27,6 +29,7 @@ namespace topk {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr int kMostBlocks = 8;  // of a cluster
 constexpr int kMoveThreads = 256;
 
 struct EvictArgs {
@@ -41,26 +44,14 @@ struct EvictArgs {
     int part;     // slots a block of the first has room for in shared memory
 };
 
-// Order-preserving key: protected above NaN above every number, -0 equal to +0.
-__device__ __forceinline__ unsigned evict_key(float w, int pos, int sink, long long recent_from) {
-    if (pos < sink || pos >= recent_from) return 0xFFFFFFFFu;
-    if (w != w) return 0xFFFFFFFEu;
+// Order-preserving key: protected above NaN above every number, -0 equal to
+// +0.  No key is 0.
+__device__ __forceinline__ unsigned evict_key(float w, int pos, int sink, int recent_from) {
     const unsigned u = __float_as_uint(w + 0.0f);
-    return (u >> 31) ? ~u : u | 0x80000000u;
-}
-
-// Count one bin; a warp whose lanes all count the same bin (rows of equal or
-// protected slots) adds once, which spares it 32 turns at one address.
-__device__ __forceinline__ void count_bin(int* hist, int bin, bool on, int lane) {
-    const unsigned active = __ballot_sync(kFullMask, on);
-    if (!active) return;
-    const int leader = __ffs(active) - 1;
-    const int first = __shfl_sync(kFullMask, bin, leader);
-    if (__ballot_sync(kFullMask, on && bin == first) == active) {
-        if (lane == leader) atomicAdd(&hist[first], __popc(active));
-    } else if (on) {
-        atomicAdd(&hist[bin], 1);
-    }
+    unsigned key = u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+    if (w != w) key = 0xFFFFFFFEu;
+    if (pos < sink || pos >= recent_from) key = 0xFFFFFFFFu;
+    return key;
 }
 
 // kHeld: the block's keys fit its shared memory; otherwise they are made anew
@@ -69,10 +60,10 @@ template <int THREADS, bool kHeld>
 __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;
     extern __shared__ __align__(16) unsigned keys[];
-    __shared__ int hist[3][kBins];
+    __shared__ __align__(16) int hist[3][kBins];
     __shared__ int scan[kWarps];
     __shared__ int found[2];                       // the bin, and how many of its keys are kept
-    __shared__ int tally[4];                       // this block: above and at the edge; the same below the budget
+    __shared__ int4 tally;                         // this block: above and at the edge; the same below the budget
     __shared__ int warp_above[kWarps], warp_ties[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -97,10 +88,8 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         return;
     }
     const int sink = a.e.sink;
-    const long long recent_from = (long long)a.e.next_pos[b] - a.e.recent;
-    for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
-    if (tid < 4) tally[tid] = 0;
-    __syncthreads();
+    const long long recent_from64 = (long long)a.e.next_pos[b] - a.e.recent;
+    const int recent_from = recent_from64 < INT_MIN ? INT_MIN : (int)recent_from64;
     // The key of slot i of this block's part; past its end 0, which is no
     // slot's key, below every edge, and never in an edge's bin.
     auto key_at = [&](int i) {
@@ -120,25 +109,45 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         }
     };
 
-    for (int base = lo; base < end; base += 4 * THREADS) {
-        float wv[4];
-        int pv[4];
+    // Four slots a thread at a time, the next four in flight meanwhile; the
+    // first four while the histograms are cleared.  Adding 1 at an address
+    // that many lanes share is one operation of the hardware, so equal keys
+    // (protected slots, slots nothing looked at) cost nothing more.
+    float wv[4];
+    int pv[4];
+    auto fetch = [&](int base) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = base + j * THREADS + tid;
             wv[j] = i < hi ? w[i] : 0.f;
             pv[j] = i < hi ? pos[i] : 0;
         }
+    };
+    fetch(lo);
+    for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
+    if (tid == 0) tally = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int base = lo; base < end; base += 4 * THREADS) {
+        float wn[4];
+        int pn[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            wn[j] = wv[j];
+            pn[j] = pv[j];
+        }
+        if (base + 4 * THREADS < end) fetch(base + 4 * THREADS);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = base + j * THREADS + tid;
-            const unsigned key = i < hi ? evict_key(wv[j], pv[j], sink, recent_from) : 0;
+            const unsigned key = i < hi ? evict_key(wn[j], pn[j], sink, recent_from) : 0;
             if (kHeld && i < end) keys[i - lo] = key;
-            if (i < hi && i < budget) {
-                if (copy_w) wo[i] = wv[j];
-                if (copy_p) po[i] = pv[j];
+            if (i < hi) {
+                atomicAdd(&hist[0][key >> 21], 1);
+                if (i < budget) {
+                    if (copy_w) wo[i] = wn[j];
+                    if (copy_p) po[i] = pn[j];
+                }
             }
-            count_bin(hist[0], key >> 21, i < hi, lane);
         }
     }
     unsigned prefix = 0;
@@ -150,31 +159,29 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
             const int up = kShift[pass - 1];
             for (int base = lo; base < end; base += 4 * THREADS) {
                 unsigned key[4];
-                bool in[4];
                 keys_at(base + 4 * tid, end, key);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) in[j] = ((key[j] ^ prefix) >> up) == 0;
-                if (!__any_sync(kFullMask, in[0] || in[1] || in[2] || in[3])) continue;
-#pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    count_bin(hist[pass], (key[j] >> kShift[pass]) & (kWidth[pass] - 1), in[j], lane);
+                    if (((key[j] ^ prefix) >> up) == 0)
+                        atomicAdd(&hist[pass][(key[j] >> kShift[pass]) & (kWidth[pass] - 1)], 1);
             }
         }
         if (blocks > 1) cluster.sync(); else __syncthreads();
         // Thread t sums bins from the top: kPer of them, t = 0 the highest.
-        int own[kPer], sum = 0;
+        using Vec = typename std::conditional<kPer == 2, int2, int4>::type;
+        const int low_bin = kBins - kPer * (tid + 1);
+        int own[kPer] = {}, sum = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int bin = kBins - 1 - (tid * kPer + j);
-            int v = 0;
-            if (blocks == 1) {
-                v = hist[pass][bin];
-            } else {
-                for (int r = 0; r < blocks; ++r) v += cluster.map_shared_rank(&hist[pass][0], r)[bin];
-            }
-            own[j] = v;
-            sum += v;
+        for (int r = 0; r < kMostBlocks; ++r) {
+            if (r >= blocks) break;
+            const int* from = blocks == 1 ? &hist[pass][0] : cluster.map_shared_rank(&hist[pass][0], r);
+            const Vec v = *reinterpret_cast<const Vec*>(from + low_bin);
+            const int* x = reinterpret_cast<const int*>(&v);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) own[j] += x[kPer - 1 - j];
         }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += own[j];
         int x = sum;
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(kFullMask, x, d);
@@ -182,8 +189,8 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         }
         if (lane == 31) scan[warp] = x;
         __syncthreads();
-        int before = x - sum;
-        for (int v = 0; v < warp; ++v) before += scan[v];
+        const int before_warp = __reduce_add_sync(kFullMask, lane < warp ? scan[lane] : 0);
+        int before = before_warp + x - sum;
         if (before < need && need <= before + sum) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
@@ -203,50 +210,58 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     // Counts, by warps with a contiguous part each.
     const int mine = ((part + kWarps - 1) / kWarps + 127) & ~127;
     const int from = min(lo + warp * mine, end), to = min(from + mine, end);
-    int above = 0, ties = 0, above_low = 0, ties_low = 0;
-    for (int base = from; base < to; base += 128) {
-        const int i = base + 4 * lane;
-        unsigned key[4];
-        keys_at(i, to, key);
+    auto count = [&](int from, int to, int* above, int* ties) {
+        int up = 0, at = 0;
+        for (int base = from; base < to; base += 128) {
+            unsigned key[4];
+            keys_at(base + 4 * lane, to, key);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int up = key[j] > edge, at = key[j] == edge;
-            above += up;
-            ties += at;
-            above_low += i + j < budget ? up : 0;
-            ties_low += i + j < budget ? at : 0;
+            for (int j = 0; j < 4; ++j) {
+                up += key[j] > edge;
+                at += key[j] == edge;
+            }
         }
+        *above = __reduce_add_sync(kFullMask, up);
+        *ties = __reduce_add_sync(kFullMask, at);
+    };
+    int above, ties, above_low = 0, ties_low = 0;
+    count(from, to, &above, &ties);
+    if (to <= budget) {
+        above_low = above;
+        ties_low = ties;
+    } else if (from < budget) {  // the warp whose part the budget lies in
+        int up = 0, at = 0;
+        for (int i = from + lane; i < budget; i += 32) {
+            const unsigned key = key_at(i);
+            up += key > edge;
+            at += key == edge;
+        }
+        above_low = __reduce_add_sync(kFullMask, up);
+        ties_low = __reduce_add_sync(kFullMask, at);
     }
-    above = __reduce_add_sync(kFullMask, above);
-    ties = __reduce_add_sync(kFullMask, ties);
-    above_low = __reduce_add_sync(kFullMask, above_low);
-    ties_low = __reduce_add_sync(kFullMask, ties_low);
     if (lane == 0) {
         warp_above[warp] = above;
         warp_ties[warp] = ties;
-        atomicAdd(&tally[0], above);
-        atomicAdd(&tally[1], ties);
-        atomicAdd(&tally[2], above_low);
-        atomicAdd(&tally[3], ties_low);
+        atomicAdd(&tally.x, above);
+        atomicAdd(&tally.y, ties);
+        atomicAdd(&tally.z, above_low);
+        atomicAdd(&tally.w, ties_low);
     }
     if (blocks > 1) cluster.sync(); else __syncthreads();
-    int up_before = 0, ties_before = 0, up_low = 0, all_ties_low = 0;
-    for (int r = 0; r < blocks; ++r) {
-        const int* t = blocks == 1 ? tally : cluster.map_shared_rank(&tally[0], r);
-        if (r < rank) {
-            up_before += t[0];
-            ties_before += t[1];
-        }
-        up_low += t[2];
-        all_ties_low += t[3];
-    }
-    for (int v = 0; v < warp; ++v) {
-        up_before += warp_above[v];
-        ties_before += warp_ties[v];
-    }
+    int4 t = make_int4(0, 0, 0, 0);
+    if (lane < blocks) t = blocks == 1 ? tally : *cluster.map_shared_rank(&tally, lane);
+    const int up_low = __reduce_add_sync(kFullMask, t.z), all_ties_low = __reduce_add_sync(kFullMask, t.w);
+    const bool lower = lane < rank;
+    int up_before = __reduce_add_sync(kFullMask, (lower ? t.x : 0) + (lane < warp ? warp_above[lane] : 0));
+    int ties_before = __reduce_add_sync(kFullMask, (lower ? t.y : 0) + (lane < warp ? warp_ties[lane] : 0));
     if (tid == 0 && rank == 0) a.moves[row] = budget - up_low - min(all_ties_low, need);
     int* holes = a.holes + (size_t)row * a.room;
     int* movers = a.movers + (size_t)row * a.room + (a.room - budget);
+    // Of the keys at the edge, all of this warp's are kept or none, but in the
+    // one warp of the row where the last of them is.
+    const bool some = ties_before < need && need < ties_before + ties;
+    const unsigned least = ties_before + ties <= need ? edge : edge + 1;  // edge + 1 == 0 has no key at it
+    int kept_before = up_before + min(ties_before, need);
     for (int base = from; base < to; base += 128) {
         unsigned key[4];
 #pragma unroll
@@ -255,18 +270,20 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         for (int j = 0; j < 4; ++j) {
             if (base + j * 32 >= to) break;
             const int i = base + j * 32 + lane;
-            const unsigned up = __ballot_sync(kFullMask, key[j] > edge);
-            const unsigned at = __ballot_sync(kFullMask, key[j] == edge);
-            const int t = ties_before + __popc(at & lanemask_lt());
-            const int kept_before = up_before + __popc(up & lanemask_lt()) + min(t, need);
-            const bool kept = key[j] > edge || (key[j] == edge && t < need);
-            if (i < budget) {
-                if (!kept) holes[i - kept_before] = i;
-            } else if (kept) {
-                movers[kept_before] = i;
+            bool kept = key[j] >= least && least != 0;
+            if (some) {
+                const unsigned at = __ballot_sync(kFullMask, key[j] == edge);
+                kept = key[j] > edge || (key[j] == edge && ties_before + __popc(at & lanemask_lt()) < need);
+                ties_before += __popc(at);
             }
-            up_before += __popc(up);
-            ties_before += __popc(at);
+            const unsigned all = __ballot_sync(kFullMask, kept);
+            const int before = kept_before + __popc(all & lanemask_lt());
+            if (i < budget) {
+                if (!kept) holes[i - before] = i;
+            } else if (kept) {
+                movers[before] = i;
+            }
+            kept_before += __popc(all);
         }
     }
     if (blocks > 1) cluster.sync();  // no block leaves while another reads its counts
@@ -379,8 +396,8 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     // block 1024 slots at least.
     constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
     int blocks = 1;
-    while (blocks < 8 && (rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024)) blocks *= 2;
-    while (blocks < 8 && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
+    while (blocks < kMostBlocks && (rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024)) blocks *= 2;
+    while (blocks < kMostBlocks && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
     a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
     const bool held = a.part <= kMostHeld;
     cudaError_t err;
