@@ -74,6 +74,9 @@ struct Workspace {
     unsigned sort_epoch = 0;    // tags the sort's look-back words, one per call
     void* kv = nullptr;         // key-value cache operators' scratch
     size_t kv_bytes = 0;
+    void* kv_count = nullptr;   // their counters (zero between calls), and the calls so far
+    size_t kv_count_bytes = 0;
+    unsigned kv_epoch = 0;
 };
 
 std::mutex g_ws_mutex;
@@ -202,6 +205,19 @@ int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigne
     mark_not_released(w);
     *scratch = w->kv;
     *status = reinterpret_cast<unsigned*>(static_cast<char*>(w->ctrl_cand) + kI32StatusOffset);
+    return TOPK_OK;
+}
+int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch) {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    Workspace& w = g_ws[{device, reinterpret_cast<uintptr_t>(s)}];
+    if (w.kv_count_bytes < bytes) {
+        const int rc = grow(&w.kv_count, &w.kv_count_bytes, bytes);
+        if (rc != TOPK_OK) return rc;
+        const cudaError_t e = cudaMemsetAsync(w.kv_count, 0, bytes, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    *counters = static_cast<unsigned*>(w.kv_count);
+    *epoch = w.kv_epoch++;
     return TOPK_OK;
 }
 int device_pointer(const void* p) {
@@ -647,7 +663,7 @@ int topk_release_workspace(void) {
     for (auto& kv : g_ws) {
         Workspace& w = kv.second;
         cudaSetDevice(kv.first.first);
-        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk, w.kv})
+        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk, w.kv, w.kv_count})
             if (p && cudaFree(p) != cudaSuccess) rc = TOPK_ERR_CUDA;
     }
     g_ws.clear();

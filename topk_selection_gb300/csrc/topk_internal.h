@@ -219,6 +219,9 @@ void note_launch();
 // word; the call after them does not start early.  Returns a topk_status.
 void note_launches(int n);
 int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status);
+// `bytes` bytes that are zero before the first call on the stream, and a number
+// that counts the calls.
+int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch);
 // TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
 int device_pointer(const void* p);
 

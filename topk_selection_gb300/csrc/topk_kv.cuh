@@ -59,8 +59,11 @@ struct KvAttend {
     KvRows<float> weight_out;
 };
 size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a);
+// counters: kKvCounters words, in two halves that calls use in turn by their
+// epoch; a call finds its half zero and leaves it zero.
+constexpr int kKvCounters = 1536;  // three for each of at most 256 blocks
 cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, void* scratch,
-                             unsigned* status, int* launches);
+                             unsigned* counters, unsigned epoch, unsigned* status, int* launches);
 
 struct KvEvict {
     KvRows<const float> weight;

@@ -166,10 +166,12 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
     a.weight_out = rows_of<float>(weight_out);
     void* scratch = nullptr;
     unsigned* status = nullptr;
+    unsigned *counters = nullptr, epoch = 0;
     rc = topk::kv_scratch(device, s, topk::kv_attend_scratch(device, c, a), &scratch, &status);
+    if (rc == TOPK_OK) rc = topk::kv_counters(device, s, topk::kKvCounters * sizeof(unsigned), &counters, &epoch);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    e = topk::kv_attend_launch(device, s, c, a, scratch, status, &launches);
+    e = topk::kv_attend_launch(device, s, c, a, scratch, counters, epoch, status, &launches);
     topk::note_launches(launches);
     return e == cudaSuccess ? TOPK_OK : cuda_fail(e);
 }

@@ -23,8 +23,9 @@
 // Work is split evenly whatever the lengths are: all (sequence, head) rows'
 // tiles of 128 slots are numbered in order, and block c takes the range
 // [c * T / n, (c + 1) * T / n) of them.  A row that lies in one block is
-// finished there; a row that several blocks share is joined by the second
-// launch, which also turns the stored p into weights.
+// finished there; the shares of a row that several blocks have are joined by
+// the last of them to finish (no block waits for another).  With weights, the
+// p are stored, and a second launch adds them up once the sums are known.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,8 +38,11 @@ namespace topk {
 namespace {
 
 constexpr int kTile = 128;       // slots of a tile
-constexpr int kThreads = 224;    // 4 softmax warps, the copy warp, a warp for each product
-constexpr int kJoinThreads = 512;
+constexpr int kThreads = 256;    // 4 softmax warps, copies of keys, of values, and the two products
+constexpr int kSoftmax = 128;    // threads of the softmax
+constexpr int kCopyK = 4, kCopyV = 5, kMmaS = 6, kMmaO = 7;  // warps
+constexpr int kWeightThreads = 256;
+constexpr int kJoin = 16;        // shares that one block joins at most
 constexpr float kSlack = 8.f;    // p <= 2^(kSlack + kBias) = 2^15: within f16's range
 constexpr float kBias = 7.f;     // and f16's smallest step, 2^-24, is 2^-31 of the largest p
 constexpr int kRingBytes = 192 * 1024;
@@ -46,6 +50,8 @@ constexpr int kRingBytes = 192 * 1024;
 __device__ __forceinline__ uint16_t from_float(float x, int bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
 }
+
+static_assert(kKvCounters / 6 <= kJoin * kJoin, "a row's pieces are joined in two steps");
 
 struct AttendArgs {
     KvCache c;
@@ -56,7 +62,9 @@ struct AttendArgs {
     int box;       // slots that one copy takes: a power of two that divides page_size
     float* part_o;    // [2 * blocks][GP][dim]: unnormalised output of a row's share
     float2* part_ml;  // [2 * blocks][GP]: its reference and sum
-    float2* row_ml;   // [seqs * rows][GP]: the same of rows that one block finished
+    float2* row_ml;   // [seqs * rows][GP]: the same of finished rows
+    unsigned* done;   // [3 * blocks]: shares that have arrived, zero before and after
+    unsigned* clear;  // the next call's, cleared here in case a call before was cut short
     float* p;         // [tile][slot][GP], when weights are wanted
     float* tile_m;    // [tile][GP]: the reference of each tile's p
     unsigned* status;
@@ -145,7 +153,7 @@ struct Shape {
     static constexpr int kItem = kTile * DP * 2;          // bytes of a tile's keys or values
     static constexpr int kRing = kRingBytes / kItem;
     static constexpr int kQBytes = kSub * 16 * 128;       // 16 rows of a query block
-    static constexpr int kPCols = 2 * GP;                 // hi and lo of every head
+    static constexpr int kPCols = GP <= 8 ? 16 : 2 * GP;  // hi of every head, then lo; the rest is not looked at
     static constexpr int kPRow = kPCols * 2;              // bytes of a slot's row of P
     static constexpr int kPBytes = kPRow * kTile;
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
@@ -206,20 +214,47 @@ __device__ __forceinline__ float warp_sums(float (&v)[GP], int lane) {
     return v[0];
 }
 template <int GP>
-__device__ __forceinline__ int warp_head(int lane) { return lane >> (GP == 8 ? 2 : 1); }
+__device__ __forceinline__ int warp_head(int lane) { return lane / (32 / GP); }
 
-// Two numbers as 16-bit elements in one word, and back.
-__device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
-    if (bf16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&x);
+// N numbers as 16-bit elements hi and lo = p - hi, all hi and then all lo.
+template <bool BF16, int N>
+__device__ __forceinline__ void split(const float (&p)[N], uint32_t* words) {
+    uint16_t e[2 * N];
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+        if constexpr (BF16) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(p[g]);
+            e[g] = __bfloat16_as_ushort(hi);
+            e[N + g] = __bfloat16_as_ushort(__float2bfloat16_rn(p[g] - __bfloat162float(hi)));
+        } else {
+            const __half hi = __float2half_rn(p[g]);
+            e[g] = __half_as_ushort(hi);
+            e[N + g] = __half_as_ushort(__float2half_rn(p[g] - __half2float(hi)));
+        }
     }
-    const __half2 x = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) words[i] = (uint32_t)e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t x, int bf16) {
-    if (bf16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+
+// N consecutive floats, as wide as they come.
+template <int N>
+__device__ __forceinline__ void store_row(float* to, const float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int g = 0; g < N; g += 4)
+            *reinterpret_cast<float4*>(to + g) = make_float4(v[g], v[g + 1], v[g + 2], v[g + 3]);
+    } else {
+#pragma unroll
+        for (int g = 0; g < N; ++g) to[g] = v[g];
+    }
+}
+
+// kBias - m, what is added to a scaled score; a head without a score above
+// -inf yet gets a number that makes any such score pass kSlack.
+__device__ __forceinline__ float offset_of(float m) { return m > -INFINITY ? kBias - m : 3.4e38f; }
+
+__device__ __forceinline__ float lse_of(float2 ml) {
+    return ml.y == 0.f ? -INFINITY : (ml.x - kBias + log2f(ml.y)) * 0.6931471805599453f;
 }
 
 template <int DP, int GP>
@@ -232,6 +267,9 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
     __shared__ uint32_t tmem_at;
     __shared__ int scan[kThreads / 32 + 8];
     __shared__ __align__(16) float red[4][GP];
+    __shared__ float factor[kJoin][GP];
+    __shared__ float2 joined[GP];
+    __shared__ unsigned arrived;
     __shared__ volatile int gave_up;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -244,13 +282,14 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         mbar_init_fence();
         gave_up = 0;
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == kCopyK && lane == 0) {
         prefetch_map(&map_k);
-        prefetch_map(&map_v);
         prefetch_map(&map_q);
     }
-    if (warp == 5) tmem_alloc(&tmem_at, S::kTmemCols);
-    launch_dependents();  // the join waits for this launch's end before it reads anything of it
+    if (warp == kCopyV && lane == 0) prefetch_map(&map_v);
+    if (tid < 3) p.clear[blockIdx.x * 3 + tid] = 0;
+    if (warp == kMmaS) tmem_alloc(&tmem_at, S::kTmemCols);
+    launch_dependents();  // the weights' launch waits for this one's end before it reads anything of it
     Walk w = find_range<kThreads>(p, scan);
     tc_fence_before();
     __syncthreads();
@@ -270,107 +309,93 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         return n;
     };
 
-    if (warp == 4) {
-        // Copies, in the order in which the products use them:
-        // K(0), K(1), V(0), K(2), V(1), ..., V(count - 1).
+    if (warp == kCopyK || warp == kCopyV) {
+        // Copies into the ring, in the order in which the products use them:
+        // K(0), K(1), V(0), K(2), V(1), ..., V(count - 1).  One warp has the
+        // keys, one the values: a copy takes its issuer some 50 clocks, and a
+        // tile of small pages is many copies.
+        const bool keys = warp == kCopyK;
+        const CUtensorMap* map = keys ? &map_k : &map_v;
         const uint64_t policy = l2_evict_first_policy();
-        constexpr int kPer = (16 * S::kSub + 31) / 32;  // copies of a lane, at most
-        struct Tile {
-            int row, b, copies;
-            int page[kPer], at[kPer];  // of each copy's first slot
-        };
-        // The pages of a tile, fetched a tile ahead of their use: the load
-        // takes as long as a third of a tile's copy.  A lane's slots move by
-        // a tile at a time, so that only a new row divides.
-        int index[kPer], in[kPer];
+        // Lane i holds the page of the tile's i-th box, fetched a tile ahead
+        // of its use: the load takes as long as a third of a tile's copy.  A
+        // lane's slot moves by a tile at a time, so that only a new row divides.
+        int index = 0, in = 0, page, page_next = 0;
         const int step = kTile / p.c.page_size, rest = kTile % p.c.page_size;
-        auto fetch = [&](const Walk& x, Tile& t, bool enter) {
-            t.row = x.r;
-            t.b = x.b;
-            const int left = x.n - x.t * kTile;
-            t.copies = left >= kTile ? kTile / p.box * S::kSub : (left + p.box - 1) / p.box * S::kSub;
-            const int* table = p.c.table + x.b * p.c.table_stride;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int i = j * 32 + lane;
-                if (enter) {
-                    const int slot = x.t * kTile + i / S::kSub * p.box;
-                    index[j] = slot / p.c.page_size;
-                    in[j] = slot - index[j] * p.c.page_size;
-                } else {
-                    index[j] += step;
-                    in[j] += rest;
-                    if (in[j] >= p.c.page_size) {
-                        in[j] -= p.c.page_size;
-                        ++index[j];
-                    }
+        auto fetch = [&](const Walk& x, bool enter) {
+            const int first = x.t * kTile + lane * p.box;
+            if (enter) {
+                index = first / p.c.page_size;
+                in = first - index * p.c.page_size;
+            } else {
+                index += step;
+                in += rest;
+                if (in >= p.c.page_size) {
+                    in -= p.c.page_size;
+                    ++index;
                 }
-                t.at[j] = in[j];
-                t.page[j] = -1;
-                if (i < t.copies) t.page[j] = table[index[j]];
             }
+            int at = -1;
+            if (lane * p.box < kTile && first < x.n) at = p.c.table[x.b * p.c.table_stride + index];
+            return at;  // not looked at here: that would wait for the load
         };
-        Place<S::kRing> put = {0, 0};
-        int items = 0, q_loads = 0;
         auto wait_warp = [&](int bar, uint32_t parity) { return __all_sync(kFullMask, wait(bar, parity)); };
-        auto load = [&](const Tile& t, const CUtensorMap* map) {
-            if (items >= S::kRing && !wait_warp(S::kEmpty + put.at, put.phase ^ 1)) return false;
-            const uint32_t full = bar0 + (S::kFull + put.at) * 8, dst = ring + put.at * S::kItem;
-            if (lane == 0) mbar_expect_at(full, t.copies * p.box * 128);
-            __syncwarp();
-            const int h = p.parts == 1 ? t.row : t.row / p.parts;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int i = j * 32 + lane;
-                if (i < t.copies) {
-                    // A page outside the pool reads as zeros.
-                    const int page = (unsigned)t.page[j] < (unsigned)p.c.pages ? t.page[j] : p.c.pages;
-                    tma_load_4d(dst + i % S::kSub * (kTile * 128) + i / S::kSub * p.box * 128, map, i % S::kSub * 64,
-                                t.at[j], h, page, full, policy);
+        Place<S::kRing> put = {0, 0};
+        if (!keys) put.move(count == 1 ? 1 : 2);
+        int items = 0, q_loads = 0;
+        Walk x = w, y = w;  // the tile to copy, and the one after it
+        bool enters = true;
+        page = count > 0 ? fetch(y, true) : 0;
+        int in_now = in;
+        for (int it = 0; it < count; ++it) {
+            if (it + 1 < count) {
+                y.next(p);
+                page_next = fetch(y, y.t == 0);
+            }
+            if (keys && enters) {
+                const int buf = q_loads & 1;
+                if (q_loads >= 2 && !wait_warp(S::kQFree + buf, ((q_loads - 2) >> 1) & 1)) break;
+                if (lane == 0) {
+                    const uint32_t full = bar0 + (S::kQFull + buf) * 8;
+                    mbar_expect_at(full, S::kSub * GP * 128);
+                    for (int sub = 0; sub < S::kSub; ++sub)
+                        tma_load_3d(q_buf + buf * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
+                                    x.r / p.parts * p.group + x.r % p.parts * GP, x.b, full);
                 }
+                ++q_loads;
+                __syncwarp();
+            }
+            // The place was used before when its item number is kRing or more.
+            const int item = keys ? (it == 0 ? 0 : 2 * it - 1) : (it + 1 < count ? 2 * it + 2 : 2 * it + 1);
+            if (item >= S::kRing && !wait_warp(S::kEmpty + put.at, put.phase ^ 1)) break;
+            const uint32_t full = bar0 + (S::kFull + put.at) * 8, dst = ring + put.at * S::kItem;
+            const int left = x.n - x.t * kTile, boxes = left >= kTile ? kTile / p.box : (left + p.box - 1) / p.box;
+            if (lane == 0) mbar_expect_at(full, boxes * S::kSub * p.box * 128);
+            const int h = p.parts == 1 ? x.r : x.r / p.parts;
+            if ((unsigned)page >= (unsigned)p.c.pages) page = p.c.pages;  // outside the pool: reads as zeros
+            for (int i = 0; i < boxes; ++i) {
+                const int pg = __shfl_sync(kFullMask, page, i), at = __shfl_sync(kFullMask, in_now, i);
+                if (lane == 0)
+#pragma unroll
+                    for (int sub = 0; sub < S::kSub; ++sub)
+                        tma_load_4d(dst + sub * (kTile * 128) + i * p.box * 128, map, sub * 64, at, h, pg, full, policy);
             }
             ++items;
-            put.move(1);
-            return true;
-        };
-        Walk x = w;
-        Tile before, now, after;
-        bool enters = true, enters_next = false;
-        if (count > 0) fetch(x, now, true);
-        for (int it = 0; it <= count; ++it) {
-            if (it + 1 < count) {
-                x.next(p);
-                enters_next = x.t == 0;
-                fetch(x, after, enters_next);
-            }
-            if (it < count) {
-                if (enters) {
-                    const int buf = q_loads & 1;
-                    if (q_loads >= 2 && !wait_warp(S::kQFree + buf, ((q_loads - 2) >> 1) & 1)) break;
-                    if (lane == 0) {
-                        const uint32_t full = bar0 + (S::kQFull + buf) * 8;
-                        mbar_expect_at(full, S::kSub * GP * 128);
-                        for (int sub = 0; sub < S::kSub; ++sub)
-                            tma_load_3d(q_buf + buf * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
-                                        now.row / p.parts * p.group + now.row % p.parts * GP, now.b, full);
-                    }
-                    ++q_loads;
-                    __syncwarp();
-                }
-                if (!load(now, &map_k)) break;
-            }
-            if (it > 0 && !load(before, &map_v)) break;
-            before = now;
-            now = after;
-            enters = enters_next;
+            put.move(keys ? (it == 0 ? 1 : 2) : (it + 2 == count ? 1 : 2));
+            x = y;
+            enters = y.t == 0;
+            page = page_next;
+            in_now = in;
         }
         __syncwarp();
-        if (gave_up) {  // wait for the copies in flight, so that none lands after the block's end
-            for (int i = max(0, items - S::kRing); i < items; ++i)
-                mbar_wait(&bars[S::kFull + i % S::kRing], (i / S::kRing) & 1);
+        if (gave_up) {  // wait for this warp's copies in flight, so that none lands after the block's end
+            for (int it = max(0, items - S::kRing); it < items; ++it) {
+                const int item = keys ? (it == 0 ? 0 : 2 * it - 1) : (it + 1 < count ? 2 * it + 2 : 2 * it + 1);
+                mbar_wait(&bars[S::kFull + item % S::kRing], (item / S::kRing) & 1);
+            }
             for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
         }
-    } else if (warp == 5) {
+    } else if (warp == kMmaS) {
         if (lane == 0) {  // S = K Q^T
             const uint32_t id = mma_idesc(p.c.bf16, kTile, 16, false);
             constexpr uint32_t hi = smem_desc_hi(1024, 128);
@@ -407,7 +432,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == kMmaO) {
         if (lane == 0) {  // O += V^T P^T
             const uint32_t id = mma_idesc(p.c.bf16, S::kM, S::kPCols, true);
             constexpr uint32_t hi_v = smem_desc_hi(1024, 128), hi_p = smem_desc_hi(S::kPRow * 8, S::kPRow);
@@ -454,9 +479,9 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         // This slot's row of P: 16-byte chunks, swizzled over the row's width.
         constexpr int kChunks = S::kPRow / 16;
         const int turn = kChunks == 2 ? (tid >> 2) & 1 : (tid >> 1) & 3;
-        float m[GP], l[GP];
+        float m[GP], l[GP], offset[GP];
         Walk x = w;
-        bool ok = true;    // false once a wait gave up
+        bool ok = true;      // false once a wait gave up
         bool leave = false;  // all 128 threads leave at the same barrier
         for (int it = 0; it < count && !leave;) {
             int last;
@@ -464,103 +489,100 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             const int part = p.parts == 1 ? 0 : x.r % p.parts, heads = min(GP, p.group - part * GP);
             const int tile0 = w.s + it;
             for (int k = 0; k < n; ++k, ++it) {
+                // Columns of heads past `heads` hold whatever lies there, and nothing looks at what comes of them.
                 const int buf = it & 1, valid = k + 1 < n ? kTile : last;
-                float s[GP];
+                float s[GP], e[GP];
                 ok = ok && wait(S::kSFull + buf, (it >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < GP; g += 8) tmem_ld8(my_tmem + S::kTmemS + buf * 16 + g, s + g);
+                for (int g = 0; g < GP; g += 8) tmem_ld<GP < 8 ? GP : 8>(my_tmem + S::kTmemS + buf * 16 + g, s + g);
                 tmem_wait_ld();
                 tc_fence_before();
                 mbar_arrive_at(bar0 + (S::kSFree + buf) * 8);
-                const bool mine = tid < valid;
-                bool over = !ok;
+                bool over = true;
+                if (k > 0) {
+                    float top = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    if (g >= heads) s[g] = 0.f;  // what a group of fewer heads leaves in its columns
-                    if (k > 0) over = over || (mine && s[g] * c > m[g] + kSlack);
+                    for (int g = 0; g < GP; ++g) {
+                        e[g] = fmaf(s[g], c, offset[g]);
+                        top = fmaxf(top, e[g]);
+                    }
+                    over = bar_any(1, kSoftmax, (top > kSlack + kBias && tid < valid) || !ok);
                 }
-                // Some score has passed the reference by kSlack (or there is none yet).
-                if (k == 0 || bar_any(1, 128, over)) {
-                    leave = bar_any(1, 128, !ok);
+                // Some score has passed the reference by kSlack, or there is no reference yet.
+                if (over) {
+                    leave = bar_any(1, kSoftmax, !ok);
                     if (leave) break;
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
-                        const float top = warp_max(mine ? s[g] * c : -INFINITY);
+                        const float top = warp_max(tid < valid ? s[g] * c : -INFINITY);
                         if (lane == 0) red[warp][g] = top;
                     }
-                    bar_sync(1, 128);
+                    bar_sync(1, kSoftmax);
                     float f[GP];
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
                         const float top = fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g]));
-                        if (k == 0) {
-                            m[g] = top;
-                            l[g] = 0.f;
-                        } else {
-                            const float to = fmaxf(m[g], top);
-                            f[g] = to == m[g] ? 1.f : exp2_approx(m[g] - to);
-                            m[g] = to;
-                            l[g] *= f[g];
-                        }
+                        const float to = k == 0 ? top : fmaxf(m[g], top);
+                        f[g] = k == 0 ? 0.f : to == m[g] ? 1.f : exp2_approx(m[g] - to);
+                        l[g] = k == 0 ? 0.f : l[g] * f[g];
+                        m[g] = to;
+                        offset[g] = offset_of(to);
+                        e[g] = fmaf(s[g], c, offset[g]);
                     }
                     if (k > 0) {
                         ok = wait(S::kPFree + (buf ^ 1), ((it - 1) >> 1) & 1);  // the tile before is in O
                         __syncwarp();
                         tc_fence_after();
+                        constexpr int kStep = 2 * GP < 8 ? 2 * GP : 8;
 #pragma unroll
-                        for (int o = 0; o < S::kOBlocks * 2; ++o) {  // hi columns and lo columns of each block
-                            float v[GP];
-                            const uint32_t at = my_tmem + S::kTmemO + o * GP;
+                        for (int o = 0; o < S::kOBlocks; ++o) {
 #pragma unroll
-                            for (int g = 0; g < GP; g += 8) tmem_ld8(at + g, v + g);
-                            tmem_wait_ld();
+                            for (int j = 0; j < 2 * GP; j += kStep) {
+                                float v[kStep];
+                                const uint32_t at = my_tmem + S::kTmemO + o * S::kPCols + j;
+                                tmem_ld<kStep>(at, v);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int g = 0; g < GP; ++g) v[g] *= f[g];
-#pragma unroll
-                            for (int g = 0; g < GP; g += 8) tmem_st8(at + g, v + g);
-                            tmem_wait_st();
+                                for (int i = 0; i < kStep; ++i) v[i] *= f[(j + i) % GP];
+                                tmem_st<kStep>(at, v);
+                                tmem_wait_st();
+                            }
                         }
                         tc_fence_before();
                     }
                 }
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    const float e = exp2_approx(fmaf(s[g], c, kBias - (m[g] == -INFINITY ? 0.f : m[g])));
-                    s[g] = mine ? e : 0.f;
-                    l[g] += s[g];
-                }
+                for (int g = 0; g < GP; ++g) e[g] = exp2_approx(e[g]);
+                if (tid >= valid)
+#pragma unroll
+                    for (int g = 0; g < GP; ++g) e[g] = 0.f;
+#pragma unroll
+                for (int g = 0; g < GP; ++g) l[g] += e[g];
                 if (p.p) {
-                    float4* to = reinterpret_cast<float4*>(p.p + ((size_t)(tile0 + k) * kTile + tid) * GP);
-#pragma unroll
-                    for (int g = 0; g < GP; g += 4) to[g / 4] = make_float4(s[g], s[g + 1], s[g + 2], s[g + 3]);
-                    if (tid == 0) {
-                        float4* tm = reinterpret_cast<float4*>(p.tile_m + (size_t)(tile0 + k) * GP);
-#pragma unroll
-                        for (int g = 0; g < GP; g += 4) tm[g / 4] = make_float4(m[g], m[g + 1], m[g + 2], m[g + 3]);
-                    }
+                    store_row<GP>(p.p + ((size_t)(tile0 + k) * kTile + tid) * GP, e);
+                    if (tid == 0) store_row<GP>(p.tile_m + (size_t)(tile0 + k) * GP, m);
                 }
-                uint32_t word[GP];  // hi of all heads, then lo
-#pragma unroll
-                for (int g = 0; g < GP; g += 2) {
-                    word[g / 2] = pack2(s[g], s[g + 1], p.c.bf16);
-                    const float2 hi = unpack2(word[g / 2], p.c.bf16);
-                    word[(GP + g) / 2] = pack2(s[g] - hi.x, s[g + 1] - hi.y, p.c.bf16);
-                }
+                uint32_t word[GP];
+                if (p.c.bf16) split<true, GP>(e, word); else split<false, GP>(e, word);
                 if (it >= 2) ok = ok && wait(S::kPFree + buf, ((it >> 1) & 1) ^ 1);
                 const uint32_t row = p_buf + buf * S::kPBytes + tid * S::kPRow;
+                if constexpr (GP == 1) {
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (turn << 4)), "r"(word[0]) : "memory");
+                } else {
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((i ^ turn) << 4)),
-                                 "r"(word[4 * i]), "r"(word[4 * i + 1]), "r"(word[4 * i + 2]), "r"(word[4 * i + 3])
-                                 : "memory");
+                    for (int i = 0; i < GP / 4; ++i)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((i ^ turn) << 4)),
+                                     "r"(word[4 * i]), "r"(word[4 * i + 1]), "r"(word[4 * i + 2]), "r"(word[4 * i + 3])
+                                     : "memory");
+                }
                 if (valid & 15) {
                     // Rows past the sequence's end inside the last step of 16: zero times NaN is NaN.
                     const int item = it + 1 < count ? 2 * it + 2 : 2 * count - 1, st = item % S::kRing;
                     ok = ok && wait(S::kFull + st, (item / S::kRing) & 1);
                     const int pad = (16 - (valid & 15)) * S::kSub * 8;
-                    for (int i = tid; ok && i < pad; i += 128)
+                    for (int i = tid; ok && i < pad; i += kSoftmax)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          ring + st * S::kItem + i / 8 % S::kSub * (kTile * 128) +
                                          (valid + i / (S::kSub * 8)) * 128 + (i & 7) * 16),
@@ -576,41 +598,38 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             const int final_it = it - 1;
             const float sum = warp_sums<GP>(l, lane);
             ok = ok && wait(S::kPFree + (final_it & 1), (final_it >> 1) & 1);
-            leave = bar_any(1, 128, !ok);
+            leave = bar_any(1, kSoftmax, !ok);
             if (leave) break;
             if ((lane & (32 / GP - 1)) == 0) red[warp][warp_head<GP>(lane)] = sum;
-            bar_sync(1, 128);
+            bar_sync(1, kSoftmax);
             tc_fence_after();
             const int row_start = tile0 - x.t;  // tile number of the row's first tile
             const bool whole = row_start >= w.s && row_start + x.tiles <= w.e;
             const int share = 2 * blockIdx.x + (row_start >= w.s ? 1 : 0);
             const int q0 = x.b * p.a.q_heads + (p.parts == 1 ? x.r : x.r / p.parts) * p.group + part * GP;
+            float2* row_ml = p.row_ml + ((size_t)x.b * p.rows + x.r) * GP;
+            constexpr int kStep = 2 * GP < 8 ? 2 * GP : 8;
             float v[S::kOBlocks][2 * GP];
 #pragma unroll
             for (int o = 0; o < S::kOBlocks; ++o)
 #pragma unroll
-                for (int g = 0; g < 2 * GP; g += 8) tmem_ld8(my_tmem + S::kTmemO + o * S::kPCols + g, v[o] + g);
+                for (int j = 0; j < 2 * GP; j += kStep)
+                    tmem_ld<kStep>(my_tmem + S::kTmemO + o * S::kPCols + j, v[o] + j);
 #pragma unroll
             for (int g = 0; g < GP; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
             tmem_wait_ld();
             tc_fence_before();
             if (tid < heads) {
-                float mm = m[0], ll = l[0];
+                float2 ml = make_float2(m[0], l[0]);
 #pragma unroll
                 for (int g = 1; g < GP; ++g)
-                    if (g == tid) {
-                        mm = m[g];
-                        ll = l[g];
-                    }
-                if (ll != ll) mm = 0.f;  // a NaN sum says it all: keep it apart from an empty share
-                if (whole) {
-                    p.row_ml[((size_t)x.b * p.rows + x.r) * GP + tid] = make_float2(mm, ll);
-                    if (p.a.lse)
-                        p.a.lse[q0 + tid] = ll == 0.f ? -INFINITY : (mm - kBias + log2f(ll)) * 0.6931471805599453f;
-                } else {
-                    p.part_ml[share * GP + tid] = make_float2(mm, ll);
-                }
+                    if (g == tid) ml = make_float2(m[g], l[g]);
+                if (ml.y != ml.y) ml.x = 0.f;  // a NaN sum says it all
+                (whole ? row_ml : p.part_ml + share * GP)[tid] = ml;
+                if (whole && p.a.lse) p.a.lse[q0 + tid] = lse_of(ml);
             }
+#pragma unroll
+            for (int g = 0; g < GP; ++g) l[g] = !whole ? 1.f : l[g] == 0.f ? 0.f : __frcp_rn(l[g]);
 #pragma unroll
             for (int o = 0; o < S::kOBlocks; ++o) {
                 // 64 rows of a product lie in the first 16 lanes of each warp's 32.
@@ -621,10 +640,85 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                     if (g >= heads) break;
                     const float y = v[o][g] + v[o][GP + g];
                     if (whole)
-                        p.a.out[(size_t)(q0 + g) * p.c.dim + d] =
-                            from_float(l[g] == 0.f ? 0.f : y * __frcp_rn(l[g]), p.c.bf16);
+                        p.a.out[(size_t)(q0 + g) * p.c.dim + d] = from_float(l[g] == 0.f ? 0.f : y * l[g], p.c.bf16);
                     else
                         p.part_o[((size_t)share * GP + g) * p.c.dim + d] = y;
+                }
+            }
+            if (!whole) {
+                const int c0 = w.block_of(row_start), c1 = w.block_of(row_start + x.tiles - 1), pieces = c1 - c0 + 1;
+                // Adds up the shares of `n` blocks, `stride` apart from `first` on: into the
+                // output, or (not the row's last step) into the first one's share.
+                auto join = [&](int first, int stride, int n, bool final) {
+                    for (int g = warp; g < heads; g += kSoftmax / 32) {
+                        float2 ml = make_float2(0.f, 0.f);
+                        const int c = first + lane * stride;
+                        if (lane < n) ml = __ldcg(&p.part_ml[(2 * c + (c == c0)) * GP + g]);
+                        const float top = warp_max(ml.y == 0.f ? -INFINITY : ml.x);
+                        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+                        float sum = ml.y * f;
+                        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+                        if (lane < n) factor[lane][g] = f;
+                        if (lane == 0) joined[g] = make_float2(top, sum);
+                    }
+                    bar_sync(1, kSoftmax);
+                    const int quads = heads * p.c.dim / 4;
+                    for (int i = tid; i < quads; i += kSoftmax) {
+                        const int g = 4 * i / p.c.dim;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                        for (int j = 0; j < n; ++j) {
+                            const int c = first + j * stride;
+                            const float4* from = reinterpret_cast<const float4*>(
+                                p.part_o + (size_t)(2 * c + (c == c0)) * GP * p.c.dim);
+                            const float4 y = __ldcg(from + i);
+                            const float f = factor[j][g];
+                            o.x = fmaf(y.x, f, o.x);
+                            o.y = fmaf(y.y, f, o.y);
+                            o.z = fmaf(y.z, f, o.z);
+                            o.w = fmaf(y.w, f, o.w);
+                        }
+                        if (final) {
+                            const float sum = joined[g].y, r = sum == 0.f ? 0.f : __frcp_rn(sum);
+                            uint2 word;
+                            word.x = from_float(sum == 0.f ? 0.f : o.x * r, p.c.bf16) |
+                                     (uint32_t)from_float(sum == 0.f ? 0.f : o.y * r, p.c.bf16) << 16;
+                            word.y = from_float(sum == 0.f ? 0.f : o.z * r, p.c.bf16) |
+                                     (uint32_t)from_float(sum == 0.f ? 0.f : o.w * r, p.c.bf16) << 16;
+                            *reinterpret_cast<uint2*>(p.a.out + (size_t)q0 * p.c.dim + 4 * i) = word;
+                        } else {
+                            reinterpret_cast<float4*>(p.part_o + (size_t)(2 * first + (first == c0)) * GP * p.c.dim)[i] = o;
+                        }
+                    }
+                    if (tid < heads) {
+                        float2 ml = joined[tid];
+                        if (ml.y != ml.y || ml.y == 0.f) ml.x = 0.f;
+                        (final ? row_ml : p.part_ml + (2 * first + (first == c0)) * GP)[tid] = ml;
+                        if (final && p.a.lse) p.a.lse[q0 + tid] = lse_of(ml);
+                    }
+                };
+                // Whether this block is the last of n to arrive at a counter, which is then zero again.
+                auto last_of = [&](unsigned* counter, int n) {
+                    bar_sync(1, kSoftmax);
+                    if (tid == 0) {  // releases what the barrier collected, and acquires the others'
+                        unsigned before;
+                        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+                        if (before + 1 == (unsigned)n) *counter = 0;
+                        arrived = before + 1;
+                    }
+                    bar_sync(1, kSoftmax);
+                    return arrived == (unsigned)n;
+                };
+                if (pieces <= kJoin) {
+                    if (last_of(p.done + 2 * c0 + 1, pieces)) join(c0, 1, pieces, true);
+                } else {
+                    // Two steps: kJoin neighbours each, then what they left (at most kJoin * kJoin pieces).
+                    const int first = c0 + ((int)blockIdx.x - c0) / kJoin * kJoin, n = min(kJoin, c1 - first + 1);
+                    if (last_of(p.done + 2 * first + (first == c0), n)) {
+                        join(first, 1, n, false);
+                        const int groups = (pieces + kJoin - 1) / kJoin;
+                        if (last_of(p.done + 2 * gridDim.x + c0, groups)) join(c0, kJoin, groups, true);
+                    }
                 }
             }
             x.t += n - 1;
@@ -633,137 +727,72 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_dealloc(tmem, S::kTmemCols);
-}
-
-// Joins the rows that several blocks share, writes what sequences without
-// slots give, and adds the shares to the weights.  Block c takes the tiles
-// that block c of the first launch had, so its p may still be in L2.
-template <int GP>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttendArgs p) {
-    constexpr int kWarps = kJoinThreads / 32;
-    __shared__ int scan[kWarps + 8];
-    __shared__ float2 ml[GP];
-    __shared__ float acc[kJoinThreads];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Walk w = find_range<kJoinThreads>(p, scan);
+    if (warp == kMmaS) tmem_dealloc(tmem, S::kTmemCols);
+    // What sequences without slots give.
     for (int b = blockIdx.x; b < p.c.seqs; b += gridDim.x) {
         if (p.c.len(b) > 0) continue;
-        for (int i = tid; i < p.a.q_heads * p.c.dim; i += kJoinThreads)
-            p.a.out[(size_t)b * p.a.q_heads * p.c.dim + i] = 0;
+        const size_t first = (size_t)b * p.a.q_heads;
+        for (int i = tid; i < p.a.q_heads * (p.c.dim / 8); i += kThreads)
+            reinterpret_cast<int4*>(p.a.out + first * p.c.dim)[i] = make_int4(0, 0, 0, 0);
         if (p.a.lse)
-            for (int i = tid; i < p.a.q_heads; i += kJoinThreads) p.a.lse[(size_t)b * p.a.q_heads + i] = -INFINITY;
+            for (int i = tid; i < p.a.q_heads; i += kThreads) p.a.lse[first + i] = -INFINITY;
     }
+}
+
+// Adds the heads' shares to the weights: p * 2^(tile's reference - row's) /
+// sum.  Block c takes the tiles that block c of the first launch had, so its
+// p may still be in L2; a warp takes a tile, all its loads in flight at once.
+template <int GP>
+__global__ void __launch_bounds__(kWeightThreads) kv_weight_kernel(const AttendArgs p) {
+    constexpr int kWarps = kWeightThreads / 32;
+    __shared__ int scan[kWarps + 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Walk w = find_range<kWeightThreads>(p, scan);
     grid_dependency_wait();
-    int tile = w.s;
-    while (tile < w.e) {
+    for (int tile = w.s; tile < w.e;) {
         const int count = min(w.tiles - w.t, w.e - tile);  // this block's tiles of the row
-        const int row_start = tile - w.t, part = w.r % p.parts, h = w.r / p.parts;
-        const int c0 = w.block_of(row_start), c1 = w.block_of(row_start + w.tiles - 1);
-        // Statistics of part `pt` of the row's group into ml[]: reference and sum (0 for an empty row).
-        auto stats = [&](int pt) {
-            const int start = row_start + (pt - part) * w.tiles;
-            const int a0 = w.block_of(start), a1 = w.block_of(start + w.tiles - 1);
+        const int part = w.r % p.parts, h = w.r / p.parts;
+        // Of a group in several parts, the block that has the first adds up all.
+        for (int pt = 0; part == 0 && pt < p.parts; ++pt) {
             const int heads = min(GP, p.group - pt * GP);
-            __syncthreads();
-            for (int g = warp; g < heads; g += kWarps) {
-                float top = -INFINITY, sum = 0.f;
-                if (a0 == a1) {
-                    const float2 v = p.row_ml[((size_t)w.b * p.rows + h * p.parts + pt) * GP + g];
-                    top = v.x;
-                    sum = v.y;
-                } else {
-                    for (int c = a0 + lane; c <= a1; c += 32) {
-                        const float2 v = p.part_ml[(2 * c + (c == a0)) * GP + g];
-                        if (v.x == -INFINITY) continue;
-                        const float to = fmaxf(top, v.x);
-                        sum = (top == -INFINITY ? 0.f : sum * exp2f(top - to)) + v.y * exp2f(v.x - to);
-                        top = to;
-                    }
-                    const float all = warp_max(top);
-                    sum = top == -INFINITY ? 0.f : sum * exp2f(top - all);
-                    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-                    top = all;
-                }
-                if (lane == 0) ml[g] = make_float2(top, sum);
-            }
-            __syncthreads();
-        };
-        const bool weights = p.p && part == 0;
-        if (c0 != c1 || weights) stats(part);
-        if (c0 != c1) {
-            const int heads = min(GP, p.group - part * GP);
-            const int q0 = w.b * p.a.q_heads + h * p.group + part * GP;
-            const int block = blockIdx.x;
-            if (block == c0 && tid < heads && p.a.lse)
-                p.a.lse[q0 + tid] = ml[tid].y == 0.f ? -INFINITY
-                                                     : (ml[tid].x - kBias + log2f(ml[tid].y)) * 0.6931471805599453f;
-            // The row's blocks share out the output's elements; a block's
-            // threads share its elements, and the row's pieces where threads are left.
-            const int elements = heads * p.c.dim, blocks = c1 - c0 + 1;
-            const int each = (elements + blocks - 1) / blocks;
-            const int width = each > 256 ? 512 : each > 128 ? 256 : each > 64 ? 128 : each > 32 ? 64 : 32;
-            const int ways = kJoinThreads / width, from = (block - c0) * each, to = min(from + each, elements);
-            for (int e0 = from; e0 < to; e0 += width) {
-                const int i = e0 + tid % width, g = min(i / p.c.dim, heads - 1);
-                const float top = ml[g].x;
-                float o = 0.f;
-                if (i < to)
-#pragma unroll 4
-                    for (int c = c0 + tid / width; c <= c1; c += ways) {
-                        const int share = 2 * c + (c == c0);
-                        const float x = p.part_ml[share * GP + g].x, v = p.part_o[(size_t)share * GP * p.c.dim + i];
-                        o += x == -INFINITY ? 0.f : v * exp2f(x - top);
-                    }
-                if (ways > 1) {
-                    __syncthreads();
-                    acc[tid] = o;
-                    __syncthreads();
-                    if (tid < width)
-                        for (int k = 1; k < ways; ++k) o += acc[k * width + tid];
-                }
-                if (tid < width && i < to)
-                    p.a.out[(size_t)q0 * p.c.dim + i] = from_float(ml[g].y == 0.f ? 0.f : o / ml[g].y, p.c.bf16);
-            }
-        }
-        if (weights) {
-            const float* wi = p.a.weight.row(w.b, h);
+            const float* wi = pt == 0 ? p.a.weight.row(w.b, h) : p.a.weight_out.row(w.b, h);
             float* wo = p.a.weight_out.row(w.b, h);
-            for (int pt = 0; pt < p.parts; ++pt) {
-                if (pt > 0) stats(pt);
-                const int heads = min(GP, p.group - pt * GP);
-                const float2 mine = lane < heads ? ml[lane] : make_float2(0.f, 0.f);
-                for (int k = warp; k < count; k += kWarps) {
-                    // A warp takes a tile; all its loads are in flight at once.
-                    const size_t x = tile + k + (size_t)pt * w.tiles;
-                    const int slot0 = (w.t + k) * kTile + lane;
-                    const float4* v = reinterpret_cast<const float4*>(p.p + (x * kTile + lane) * GP);
-                    const float tm = lane < heads ? p.tile_m[x * GP + lane] : -INFINITY;
-                    float4 y[4][GP / 4];
-                    float old[4];
+            float2 ml = make_float2(0.f, 0.f);
+            if (lane < heads) ml = p.row_ml[((size_t)w.b * p.rows + w.r + pt) * GP + lane];
+            for (int k = warp; k < count; k += kWarps) {
+                const size_t x = tile + k + (size_t)pt * w.tiles;
+                const int slot0 = (w.t + k) * kTile + lane;
+                float y[4][GP], sum[4];
+                const float tm = lane < heads ? p.tile_m[x * GP + lane] : 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {
+                    const float* v = p.p + (x * kTile + i * 32 + lane) * GP;
+                    if constexpr (GP % 4 == 0) {
 #pragma unroll
-                        for (int g = 0; g < GP / 4; ++g) y[i][g] = v[i * 32 * (GP / 4) + g];
-                        const int slot = slot0 + i * 32;
-                        old[i] = slot < w.n ? (pt == 0 ? wi[slot] : wo[slot]) : 0.f;
-                    }
-                    float f = 0.f;
-                    if (tm != -INFINITY && mine.y != 0.f) f = exp2f(tm - mine.x) / mine.y;
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) {
-                        const float fg = __shfl_sync(kFullMask, f, g);
-                        if (g >= heads) continue;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 q = y[i][g / 4];
-                            old[i] = fmaf(g % 4 == 0 ? q.x : g % 4 == 1 ? q.y : g % 4 == 2 ? q.z : q.w, fg, old[i]);
+                        for (int g = 0; g < GP; g += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(v + g);
+                            y[i][g] = q.x;
+                            y[i][g + 1] = q.y;
+                            y[i][g + 2] = q.z;
+                            y[i][g + 3] = q.w;
                         }
-                    }
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (slot0 + i * 32 < w.n) wo[slot0 + i * 32] = old[i];
+                        for (int g = 0; g < GP; ++g) y[i][g] = v[g];
+                    }
+                    sum[i] = slot0 + i * 32 < w.n ? wi[slot0 + i * 32] : 0.f;
                 }
+                const float f = ml.y == 0.f || tm == -INFINITY ? 0.f : exp2f(tm - ml.x) / ml.y;
+#pragma unroll
+                for (int g = 0; g < GP; ++g) {
+                    const float fg = __shfl_sync(kFullMask, f, g);
+                    if (g >= heads) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(y[i][g], fg, sum[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (slot0 + i * 32 < w.n) wo[slot0 + i * 32] = sum[i];
             }
         }
         tile += count;
@@ -804,7 +833,12 @@ cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, int rank, co
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int group_part(const KvCache& c, const KvAttend& a) { return a.q_heads / c.heads <= 8 ? 8 : 16; }
+// Query heads that a block handles together: a thread's work on a tile goes
+// with them.
+int group_part(const KvCache& c, const KvAttend& a) {
+    const int group = a.q_heads / c.heads;
+    return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 ? 8 : 16;
+}
 
 int sm_count(int device) {
     static int counts[64];
@@ -833,6 +867,7 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
     const size_t rows = (size_t)c.seqs * p.rows, tiles = rows * ((c.capacity() + kTile - 1) / kTile);
     plan.blocks = sm_count(device);
     if ((size_t)plan.blocks > tiles) plan.blocks = (int)tiles;
+    if (plan.blocks > kKvCounters / 6) plan.blocks = kKvCounters / 6;
     char* at = static_cast<char*>(scratch);
     size_t bytes = 0;
     auto take = [&](size_t n) {
@@ -863,9 +898,20 @@ cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, in
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = launch_pdl(kv_join_kernel<GP>, dim3(plan.blocks), dim3(kJoinThreads), 0, s, plan.args);
+    if (!plan.args.p) return cudaSuccess;
+    e = launch_pdl(kv_weight_kernel<GP>, dim3(plan.blocks), dim3(kWeightThreads), 0, s, plan.args);
     if (e == cudaSuccess) ++*launches;
     return e;
+}
+
+template <int DP>
+cudaError_t launch_dim(const Plan& plan, int gp, cudaStream_t s, const CUtensorMap* maps, int* launches) {
+    switch (gp) {
+        case 1: return launch<DP, 1>(plan, s, maps, launches);
+        case 4: return launch<DP, 4>(plan, s, maps, launches);
+        case 8: return launch<DP, 8>(plan, s, maps, launches);
+        default: return launch<DP, 16>(plan, s, maps, launches);
+    }
 }
 
 }  // namespace
@@ -875,9 +921,11 @@ size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a) {
 }
 
 cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, void* scratch,
-                             unsigned* status, int* launches) {
+                             unsigned* counters, unsigned epoch, unsigned* status, int* launches) {
     Plan plan = make_plan(device, c, a, scratch);
     plan.args.status = status;
+    plan.args.done = counters + (epoch & 1) * (kKvCounters / 2);
+    plan.args.clear = counters + (~epoch & 1) * (kKvCounters / 2);
     const int gp = group_part(c, a);
     CUtensorMap maps[3];
     const cuuint64_t pool[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
@@ -889,9 +937,9 @@ cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const
     if (e == cudaSuccess) e = make_map(&maps[1], c.v, c.bf16, 4, pool, vs, pool_box);
     if (e == cudaSuccess) e = make_map(&maps[2], a.q, c.bf16, 3, queries, qs, query_box);
     if (e != cudaSuccess) return e;
-    if (c.dim <= 64) return gp == 8 ? launch<64, 8>(plan, s, maps, launches) : launch<64, 16>(plan, s, maps, launches);
-    if (c.dim <= 128) return gp == 8 ? launch<128, 8>(plan, s, maps, launches) : launch<128, 16>(plan, s, maps, launches);
-    return gp == 8 ? launch<256, 8>(plan, s, maps, launches) : launch<256, 16>(plan, s, maps, launches);
+    if (c.dim <= 64) return launch_dim<64>(plan, gp, s, maps, launches);
+    if (c.dim <= 128) return launch_dim<128>(plan, gp, s, maps, launches);
+    return launch_dim<256>(plan, gp, s, maps, launches);
 }
 
 }  // namespace topk

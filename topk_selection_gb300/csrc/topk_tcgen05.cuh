@@ -62,19 +62,42 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Load or store 8 columns of this warp's 32 lanes (lane l of the warp holds
-// tensor memory lane 32 * (warp % 4) + l).  A load's registers are ready
-// after tmem_wait_ld().
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, float* r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-                 : "r"(addr)
-                 : "memory");
+// Load or store N columns (1, 2, 4 or 8) of this warp's 32 lanes (lane l of
+// the warp holds tensor memory lane 32 * (warp % 4) + l).  A load's registers
+// are ready after tmem_wait_ld().
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* r) {
+    static_assert(N == 1 || N == 2 || N == 4 || N == 8, "columns");
+    if constexpr (N == 1)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                     : "=f"(r[0])
+                     : "r"(addr)
+                     : "memory");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                     : "=f"(r[0]), "=f"(r[1])
+                     : "r"(addr)
+                     : "memory");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                     : "r"(addr)
+                     : "memory");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                     : "r"(addr)
+                     : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const float* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(r[0]),
-                 "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "r"(addr)
-                 : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const float* r) {
+    static_assert(N == 2 || N == 8, "columns");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"f"(r[0]), "f"(r[1]), "r"(addr)
+                     : "memory");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "r"(addr)
+                     : "memory");
 }
 
 // Tensor-map loads of one box into shared memory; x times the element size
