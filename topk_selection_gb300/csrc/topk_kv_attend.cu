@@ -38,11 +38,11 @@ namespace topk {
 namespace {
 
 constexpr int kTile = 128;       // slots of a tile
-constexpr int kThreads = 256;    // 4 softmax warps, copies of keys, of values, and the two products
-constexpr int kSoftmax = 128;    // threads of the softmax
-constexpr int kCopyK = 4, kCopyV = 5, kMmaS = 6, kMmaO = 7;  // warps
-constexpr int kWeightThreads = 256;
-constexpr int kJoin = 16;        // shares that one block joins at most
+constexpr int kThreads = 384;    // 2 x 4 softmax warps, copies of keys, of values, and the two products
+constexpr int kSoftmax = 128;    // threads of a softmax group
+constexpr int kCopyK = 8, kCopyV = 9, kMmaS = 10, kMmaO = 11;  // warps
+constexpr int kWeightThreads = 512;
+constexpr int kJoin = 32;        // shares that one block joins at most
 constexpr float kSlack = 8.f;    // p <= 2^(kSlack + kBias) = 2^15: within f16's range
 constexpr float kBias = 7.f;     // and f16's smallest step, 2^-24, is 2^-31 of the largest p
 constexpr int kRingBytes = 192 * 1024;
@@ -65,83 +65,117 @@ struct AttendArgs {
     float2* row_ml;   // [seqs * rows][GP]: the same of finished rows
     unsigned* done;   // [3 * blocks]: shares that have arrived, zero before and after
     unsigned* clear;  // the next call's, cleared here in case a call before was cut short
-    float* p;         // [tile][slot][GP], when weights are wanted
+    int* walk;        // [blocks][Walk::kWords]: where each block begins, when weights are wanted
+    float* p;         // [tile][slot][GP]
     float* tile_m;    // [tile][GP]: the reference of each tile's p
     unsigned* status;
 };
 
+// The code of a launch is fetched anew when the cache it streams has pushed
+// it out of L2, and most of it runs once a row or once a launch: that part is
+// kept in functions of their own and in loops, not unrolled.
+
+// The first sequence from b on that has slots (seqs: none).
+__device__ __noinline__ int seq_from(const int* lens, int b, int seqs) {
+    while (b < seqs && lens[b] <= 0) ++b;
+    return b;
+}
+
+// The first tile of block c's share when `blocks` of them share `total`
+// tiles: floor(c * total / blocks), in 32 bits.
+__device__ __forceinline__ int share_start(int c, int blocks, int total) {
+    const int q = total / blocks;
+    return c * q + (int)((unsigned)(c * (total - q * blocks)) / (unsigned)blocks);
+}
+
+// The block that tile number x belongs to.
+__device__ __noinline__ int block_of(int x, int blocks, int total) {
+    int c = min((int)((float)x * (float)blocks / (float)total), blocks - 1);
+    while (c > 0 && share_start(c, blocks, total) > x) --c;
+    while (c + 1 < blocks && share_start(c + 1, blocks, total) <= x) ++c;
+    return c;
+}
+
 // Where a block's share of the tiles begins and ends, and a walk over it.
 struct Walk {
-    int b, r, t;    // sequence, row of the sequence, tile of the row
-    int n, tiles;   // the sequence's slots and tiles
-    int s, e;       // the block's range of tile numbers
+    int b, h, part, t;  // sequence, key-value head, part of its group, tile of that row
+    int n, tiles;       // the sequence's slots and tiles
+    int s, e;           // the block's range of tile numbers
     int total, blocks;
 
-    __device__ void enter(const AttendArgs& p) {
-        while (b < p.c.seqs) {
-            n = p.c.len(b);
-            if (n > 0) break;
-            ++b;
-        }
-        tiles = (n + kTile - 1) / kTile;
-    }
-    __device__ void next(const AttendArgs& p) {
+    __device__ __forceinline__ void next(const AttendArgs& p) {
         if (++t < tiles) return;
         t = 0;
-        if (++r < p.rows) return;
-        r = 0;
-        ++b;
-        enter(p);
+        if (++part < p.parts) return;
+        part = 0;
+        if (++h < p.c.heads) return;
+        h = 0;
+        b = seq_from(p.c.lens, b + 1, p.c.seqs);
+        if (b < p.c.seqs) {
+            n = p.c.len(b);
+            tiles = (n + kTile - 1) / kTile;
+        }
     }
-    // The block that tile number x belongs to.
-    __device__ int block_of(int x) const { return (int)((((long long)x + 1) * blocks - 1) / total); }
+    // To and from memory.
+    static constexpr int kWords = 12;
+    __device__ __forceinline__ void store(int* to) const {
+        reinterpret_cast<int4*>(to)[0] = make_int4(b, h, part, t);
+        reinterpret_cast<int4*>(to)[1] = make_int4(n, tiles, s, e);
+        reinterpret_cast<int4*>(to)[2] = make_int4(total, blocks, 0, 0);
+    }
+    __device__ __forceinline__ void load(const int* from) {
+        const int4 x = reinterpret_cast<const int4*>(from)[0], y = reinterpret_cast<const int4*>(from)[1];
+        b = x.x, h = x.y, part = x.z, t = x.w, n = y.x, tiles = y.y, s = y.z, e = y.w;
+    }
+    __device__ __forceinline__ int row(const AttendArgs& p) const { return (b * p.c.heads + h) * p.parts + part; }
 };
 
 // Every thread of the block calls it; sh: THREADS / 32 + 8 words of shared memory.
 template <int THREADS>
-__device__ Walk find_range(const AttendArgs& p, int* sh) {
+__device__ __forceinline__ Walk find_range(const AttendArgs& p, int* sh) {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, seqs = p.c.seqs;
     const int chunk = (seqs + THREADS - 1) / THREADS, lo = tid * chunk, hi = min(lo + chunk, seqs);
     int mine = 0;
+#pragma unroll 1
     for (int b = lo; b < hi; ++b) mine += (p.c.len(b) + kTile - 1) / kTile * p.rows;
     int x = mine;
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(kFullMask, x, d);
         if (lane >= d) x += y;
     }
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    int before = x - mine, total = 0;
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) before += sh[w];
-        total += sh[w];
-    }
+    const int v = lane < W ? sh[lane] : 0;
+    const int before = __reduce_add_sync(kFullMask, lane < warp ? v : 0) + x - mine;
     Walk k;
-    k.total = total;
-    k.blocks = min((int)gridDim.x, total);
-    k.s = k.e = k.b = k.r = k.t = k.n = k.tiles = 0;
+    k.total = __reduce_add_sync(kFullMask, v);
+    k.blocks = min((int)gridDim.x, k.total);
+    k.s = k.e = k.b = k.h = k.part = k.t = k.n = k.tiles = 0;
     if ((int)blockIdx.x < k.blocks) {  // uniform over the block
-        k.s = (int)((long long)blockIdx.x * total / k.blocks);
-        k.e = (int)(((long long)blockIdx.x + 1) * total / k.blocks);
+        k.s = share_start(blockIdx.x, k.blocks, k.total);
+        k.e = share_start(blockIdx.x + 1, k.blocks, k.total);
         if (before <= k.s && k.s < before + mine) {
-            int at = before, b = lo;
+            int at = before, b = lo, tiles;
+#pragma unroll 1
             for (;; ++b) {
-                const int tiles = (p.c.len(b) + kTile - 1) / kTile;
-                if (k.s < at + tiles * p.rows) {
-                    sh[W] = b;
-                    sh[W + 1] = (k.s - at) / tiles;
-                    sh[W + 2] = (k.s - at) % tiles;
-                    break;
-                }
+                tiles = (p.c.len(b) + kTile - 1) / kTile;
+                if (k.s < at + tiles * p.rows) break;
                 at += tiles * p.rows;
             }
+            const int row = (k.s - at) / tiles;
+            sh[W] = b;
+            sh[W + 1] = row;
+            sh[W + 2] = k.s - at - row * tiles;
+            sh[W + 3] = p.c.len(b);
         }
         __syncthreads();
         k.b = sh[W];
-        k.r = sh[W + 1];
+        k.h = sh[W + 1] / p.parts;
+        k.part = sh[W + 1] - k.h * p.parts;
         k.t = sh[W + 2];
-        k.n = p.c.len(k.b);
+        k.n = sh[W + 3];
         k.tiles = (k.n + kTile - 1) / kTile;
     }
     return k;
@@ -158,18 +192,21 @@ struct Shape {
     static constexpr int kPBytes = kPRow * kTile;
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
     static constexpr int kOBlocks = DP / kM;
-    static constexpr int kTmemS = 0, kTmemO = 32;         // columns: two S buffers of 16, then O
-    static constexpr int kTmemCols = 32 + kOBlocks * kPCols <= 64 ? 64 : 128;
+    // Tensor memory columns: two S buffers of 16, then O of each softmax
+    // group for this row, and of both for the row before.
+    static constexpr int kTmemS = 0, kTmemO = 32, kOCols = kOBlocks * kPCols;
+    static constexpr int kTmemCols = 32 + 4 * kOCols <= 128 ? 128 : 256;
     static constexpr size_t kSmem = 1024 + kRingBytes + 2 * kQBytes + 2 * kPBytes;
     // Barriers, by their place in bars[].
     static constexpr int kFull = 0, kEmpty = kRing, kSFull = 2 * kRing, kSFree = kSFull + 2, kPReady = kSFull + 4,
                          kPFree = kSFull + 6, kQFull = kSFull + 8, kQFree = kSFull + 10, kDrain = kSFull + 12,
-                         kBars = kSFull + 14;
+                         kTold = kSFull + 14, kBars = kSFull + 18;
 };
 
 // The bounded wait's slow side: gives up after kWaitSpins tries, or once
 // another wait of the block has.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, unsigned* status) {
+#pragma unroll 1
     for (int i = 0; i < kWaitSpins; ++i) {
         if (mbar_try(bar, parity)) return true;
         if (*gave_up) return false;
@@ -249,6 +286,23 @@ __device__ __forceinline__ void store_row(float* to, const float (&v)[N]) {
     }
 }
 
+template <int N>
+__device__ __forceinline__ void load_row(const float* from, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int g = 0; g < N; g += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(from + g);
+            v[g] = x.x;
+            v[g + 1] = x.y;
+            v[g + 2] = x.z;
+            v[g + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < N; ++g) v[g] = from[g];
+    }
+}
+
 // kBias - m, what is added to a scaled score; a head without a score above
 // -inf yet gets a number that makes any such score pass kSlack.
 __device__ __forceinline__ float offset_of(float m) { return m > -INFINITY ? kBias - m : 3.4e38f; }
@@ -257,27 +311,148 @@ __device__ __forceinline__ float lse_of(float2 ml) {
     return ml.y == 0.f ? -INFINITY : (ml.x - kBias + log2f(ml.y)) * 0.6931471805599453f;
 }
 
+// Adds up the shares of `n` blocks, `stride` apart from `first` on: into the
+// output, or (not the row's last step) into the first one's share.  128
+// threads call it together; `bar` is their barrier.
+template <int GP>
+__device__ __forceinline__ void join_shares(const AttendArgs& p, int c0, int first, int stride, int n, bool final, int q0,
+                                         int heads, float2* row_ml, float (*factor)[GP], float2* joined, int bar,
+                                         int me) {
+    // A warp has every fourth head, a lane one share; all loads are in flight at once.
+    constexpr int kMine = GP < 4 ? 1 : GP / 4, kFly = 16;
+    const int lane = me & 31, quarter = me >> 5;
+    float2 ml[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int c = first + lane * stride, g = quarter + 4 * i;
+        ml[i] = make_float2(0.f, 0.f);
+        if (lane < n && g < heads) ml[i] = __ldcg(&p.part_ml[(2 * c + (c == c0)) * GP + g]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int g = quarter + 4 * i;
+        const float top = warp_max(ml[i].y == 0.f ? -INFINITY : ml[i].x);
+        const float f = ml[i].y == 0.f ? 0.f : exp2_approx(ml[i].x - top);
+        float sum = ml[i].y * f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+        if (g < heads) {
+            if (lane < n) factor[lane][g] = f;
+            if (lane == 0) joined[g] = make_float2(top, sum);
+        }
+    }
+    bar_sync(bar, kSoftmax);
+    const int quads = heads * p.c.dim / 4;
+    const size_t share = (size_t)GP * p.c.dim / 4 * 2 * stride;  // from one share to the next
+#pragma unroll 1
+    for (int i = me; i < quads; i += kSoftmax) {
+        const int g = 4 * i / p.c.dim;
+        const float4* from = reinterpret_cast<const float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim) + i;
+        const float4* from0 = from + (first == c0 ? GP * p.c.dim / 4 : 0);  // the row's first block has its own place
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int j0 = 0; j0 < n; j0 += kFly) {
+            float4 y[kFly];
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < n) y[j] = __ldcg(j0 + j == 0 ? from0 : from + (j0 + j) * share);
+            }
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                const float f = j0 + j < n ? factor[j0 + j][g] : 0.f;
+                o.x = fmaf(y[j].x, f, o.x);
+                o.y = fmaf(y[j].y, f, o.y);
+                o.z = fmaf(y[j].z, f, o.z);
+                o.w = fmaf(y[j].w, f, o.w);
+            }
+        }
+        if (final) {
+            const float sum = joined[g].y, r = sum == 0.f ? 0.f : __frcp_rn(sum);
+            if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint2 word;
+            word.x = from_float(o.x * r, p.c.bf16) | (uint32_t)from_float(o.y * r, p.c.bf16) << 16;
+            word.y = from_float(o.z * r, p.c.bf16) | (uint32_t)from_float(o.w * r, p.c.bf16) << 16;
+            *reinterpret_cast<uint2*>(p.a.out + (size_t)q0 * p.c.dim + 4 * i) = word;
+        } else {
+            reinterpret_cast<float4*>(p.part_o + (size_t)(2 * first + (first == c0)) * GP * p.c.dim)[i] = o;
+        }
+    }
+    if (me < heads) {
+        float2 ml = joined[me];
+        if (ml.y != ml.y || ml.y == 0.f) ml.x = 0.f;
+        (final ? row_ml : p.part_ml + (2 * first + (first == c0)) * GP)[me] = ml;
+        if (final && p.a.lse) p.a.lse[q0 + me] = lse_of(ml);
+    }
+}
+
+// Whether this block is the last of n to arrive at a counter, which is then zero again.
+__device__ __forceinline__ bool last_of(unsigned* counter, int n, unsigned* arrived, int bar, int me) {
+    bar_sync(bar, kSoftmax);
+    if (me == 0) {  // releases what the barrier collected, and acquires the others'
+        unsigned before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+        if (before + 1 == (unsigned)n) *counter = 0;
+        *arrived = before + 1;
+    }
+    bar_sync(bar, kSoftmax);
+    return *arrived == (unsigned)n;
+}
+
+// After this block's share of a row that several blocks have: the last of
+// them to come here joins them.  Up to kJoin shares at once; more (at most
+// kJoin * kJoin) in two steps, neighbours first.
+template <int GP>
+__device__ __forceinline__ void join_row(const AttendArgs& p, int total, int blocks, int row_start, int tiles, int q0,
+                                      int heads, float2* row_ml, float (*factor)[GP], float2* joined,
+                                      unsigned* arrived, int bar, int me) {
+    const int c0 = block_of(row_start, blocks, total), c1 = block_of(row_start + tiles - 1, blocks, total);
+    const int pieces = c1 - c0 + 1, groups = (pieces + kJoin - 1) / kJoin;
+    int first = c0, stride = 1, n = pieces;
+    bool final = true;
+    if (groups > 1) {
+        first = c0 + ((int)blockIdx.x - c0) / kJoin * kJoin;
+        n = min(kJoin, c1 - first + 1);
+        final = false;
+    }
+    unsigned* counter = p.done + 2 * first + (first == c0);
+#pragma unroll 1
+    while (last_of(counter, n, arrived, bar, me)) {
+        join_shares<GP>(p, c0, first, stride, n, final, q0, heads, row_ml, factor, joined, bar, me);
+        if (final) break;
+        first = c0;
+        stride = kJoin;
+        n = groups;
+        final = true;
+        counter = p.done + 2 * gridDim.x + c0;
+    }
+}
+
 template <int DP, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
-kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_q) {
     using S = Shape<DP, GP>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[S::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int scan[kThreads / 32 + 8];
-    __shared__ __align__(16) float red[4][GP];
-    __shared__ float factor[kJoin][GP];
-    __shared__ float2 joined[GP];
-    __shared__ unsigned arrived;
+    constexpr int kRow = GP < 4 ? 4 : GP;
+    __shared__ float red[2][4][GP];                        // of each softmax group and its warps
+    __shared__ __align__(16) float each[2][2][kRow];       // two numbers of each head for the group's threads
+    __shared__ float told_m[4][GP], told_l[4][4][GP];      // what one group tells the other at a row's end
+    __shared__ float factor[2][kJoin][GP];
+    __shared__ float2 joined[2][GP];
+    __shared__ unsigned arrived[2];
     __shared__ volatile int gave_up;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t bar0 = smem_addr(bars);
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < S::kBars; ++i) {
-            const bool by_threads = i == S::kSFree || i == S::kSFree + 1 || i == S::kPReady || i == S::kPReady + 1;
-            mbar_init(&bars[i], by_threads ? 128 : 1);
+            const bool by_threads = i / 2 == S::kSFree / 2 || i / 2 == S::kPReady / 2 || i >= S::kTold;
+            mbar_init(&bars[i], by_threads ? kSoftmax : 1);
         }
         mbar_init_fence();
         gave_up = 0;
@@ -287,6 +462,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         prefetch_map(&map_q);
     }
     if (warp == kCopyV && lane == 0) prefetch_map(&map_v);
+    grid_dependency_wait();
     if (tid < 3) p.clear[blockIdx.x * 3 + tid] = 0;
     if (warp == kMmaS) tmem_alloc(&tmem_at, S::kTmemCols);
     launch_dependents();  // the weights' launch waits for this one's end before it reads anything of it
@@ -297,6 +473,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
     const uint32_t tmem = tmem_at;
     const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u, q_buf = ring + kRingBytes, p_buf = q_buf + 2 * S::kQBytes;
     const int count = w.e - w.s;  // tiles of this block
+    if (p.p && tid == kSoftmax) w.store(p.walk + blockIdx.x * Walk::kWords);
 
     auto wait = [&](int bar, uint32_t parity) {
         if (mbar_try(bar0 + bar * 8, parity)) return true;
@@ -347,6 +524,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         bool enters = true;
         page = count > 0 ? fetch(y, true) : 0;
         int in_now = in;
+#pragma unroll 1
         for (int it = 0; it < count; ++it) {
             if (it + 1 < count) {
                 y.next(p);
@@ -360,7 +538,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                     mbar_expect_at(full, S::kSub * GP * 128);
                     for (int sub = 0; sub < S::kSub; ++sub)
                         tma_load_3d(q_buf + buf * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
-                                    x.r / p.parts * p.group + x.r % p.parts * GP, x.b, full);
+                                    x.h * p.group + x.part * GP, x.b, full);
                 }
                 ++q_loads;
                 __syncwarp();
@@ -371,14 +549,25 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             const uint32_t full = bar0 + (S::kFull + put.at) * 8, dst = ring + put.at * S::kItem;
             const int left = x.n - x.t * kTile, boxes = left >= kTile ? kTile / p.box : (left + p.box - 1) / p.box;
             if (lane == 0) mbar_expect_at(full, boxes * S::kSub * p.box * 128);
-            const int h = p.parts == 1 ? x.r : x.r / p.parts;
             if ((unsigned)page >= (unsigned)p.c.pages) page = p.c.pages;  // outside the pool: reads as zeros
-            for (int i = 0; i < boxes; ++i) {
-                const int pg = __shfl_sync(kFullMask, page, i), at = __shfl_sync(kFullMask, in_now, i);
+#pragma unroll 1
+            for (int i0 = 0; i0 < boxes; i0 += 4) {
+                int pg[4], at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pg[i] = __shfl_sync(kFullMask, page, i0 + i);
+                    at[i] = __shfl_sync(kFullMask, in_now, i0 + i);
+                }
                 if (lane == 0)
 #pragma unroll
-                    for (int sub = 0; sub < S::kSub; ++sub)
-                        tma_load_4d(dst + sub * (kTile * 128) + i * p.box * 128, map, sub * 64, at, h, pg, full, policy);
+                    for (int i = 0; i < 4; ++i) {
+                        if (i0 + i >= boxes) break;
+#pragma unroll
+                        for (int sub = 0; sub < S::kSub; ++sub)
+                            tma_load_4d(dst + sub * (kTile * 128) + (i0 + i) * p.box * 128, map, sub * 64, at[i], x.h,
+                                        pg[i], full, policy);
+                    }
+                __syncwarp();
             }
             ++items;
             put.move(keys ? (it == 0 ? 1 : 2) : (it + 2 == count ? 1 : 2));
@@ -389,10 +578,12 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         }
         __syncwarp();
         if (gave_up) {  // wait for this warp's copies in flight, so that none lands after the block's end
+#pragma unroll 1
             for (int it = max(0, items - S::kRing); it < items; ++it) {
                 const int item = keys ? (it == 0 ? 0 : 2 * it - 1) : (it + 1 < count ? 2 * it + 2 : 2 * it + 1);
                 mbar_wait(&bars[S::kFull + item % S::kRing], (item / S::kRing) & 1);
             }
+#pragma unroll 1
             for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
         }
     } else if (warp == kMmaS) {
@@ -403,10 +594,12 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             Place<S::kRing> get = {0, 0};
             Walk x = w;
             bool ok = true;
+#pragma unroll 1
             for (int it = 0, piece = 0; it < count && ok; ++piece) {
                 int last;
                 const int n = share_of(x, it, &last), qb = piece & 1;
                 if (!wait(S::kQFull + qb, (piece >> 1) & 1)) break;
+#pragma unroll 1
                 for (int k = 0; k < n; ++k, ++it) {
                     const int buf = it & 1;
                     ok = wait(S::kFull + get.at, get.phase) &&
@@ -442,11 +635,14 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
             get.move(count == 1 ? 1 : 2);
             Walk x = w;
             bool ok = true;
-            for (int it = 0; it < count && ok;) {
+#pragma unroll 1
+            for (int it = 0, piece = 0; it < count && ok; ++piece) {
                 int last;
                 const int n = share_of(x, it, &last);
+#pragma unroll 1
                 for (int k = 0; k < n; ++k, ++it) {
                     const int buf = it & 1, steps = k + 1 < n ? 8 : (last + 15) >> 4;
+                    const uint32_t o = tmem + S::kTmemO + ((piece & 1) * 2 + buf) * S::kOCols;
                     ok = wait(S::kFull + get.at, get.phase) && wait(S::kPReady + buf, (it >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -456,8 +652,8 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                         if (j >= steps) break;
 #pragma unroll
                         for (int m = 0; m < S::kOBlocks; ++m)
-                            mma_f16(tmem + S::kTmemO + m * S::kPCols, a + ((m * 2 * (kTile * 128) + j * 2048) >> 4),
-                                    hi_v, b + j * (S::kPRow * 16 >> 4), hi_p, id, k > 0 || j > 0);
+                            mma_f16(o + m * S::kPCols, a + ((m * 2 * (kTile * 128) + j * 2048) >> 4),
+                                    hi_v, b + j * (S::kPRow * 16 >> 4), hi_p, id, k > 1 || j > 0);
                     }
                     mma_commit(bar0 + (S::kPFree + buf) * 8);
                     mma_commit(bar0 + (S::kEmpty + get.at) * 8);
@@ -473,66 +669,87 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
         }
         __syncwarp();
     } else {
-        // Softmax: thread tid owns slot tid of each tile, and lane tid of O.
+        // Softmax.  The two groups of 128 threads take the tiles in turn, each
+        // with its own buffers of S and P, reference, sum and O, so that one
+        // group's waits are the other's work; the group that has a row's
+        // last tile puts the two together.  Thread `me` owns slot `me` of
+        // each of its group's tiles, and lane `me` of O.
+        const int group = warp >> 2, me = tid & (kSoftmax - 1), quarter = warp & 3;
         const float c = p.a.scale * 1.4426950408889634f;
-        const uint32_t my_tmem = tmem + ((uint32_t)warp << 21);  // 32 * warp in the address's lane field
+        const uint32_t my_tmem = tmem + ((uint32_t)quarter << 21);  // 32 * quarter in the address's lane field
+        const uint32_t my_s = my_tmem + S::kTmemS + group * 16;
         // This slot's row of P: 16-byte chunks, swizzled over the row's width.
         constexpr int kChunks = S::kPRow / 16;
-        const int turn = kChunks == 2 ? (tid >> 2) & 1 : (tid >> 1) & 3;
-        float m[GP], l[GP], offset[GP];
+        const int turn = kChunks == 2 ? (me >> 2) & 1 : (me >> 1) & 3;
+        const uint32_t my_p = p_buf + group * S::kPBytes + me * S::kPRow;
+        // What goes with a head alone is worked out by thread g of the group
+        // for head g, and handed to the others in `each`.
+        float l[GP], offset[GP], my_m = 0.f;
+        float* const first_of = each[group][0];
+        float* const second_of = each[group][1];
         Walk x = w;
         bool ok = true;      // false once a wait gave up
-        bool leave = false;  // all 128 threads leave at the same barrier
-        for (int it = 0; it < count && !leave;) {
+        bool leave = false;  // all threads of the group leave at the same barrier
+#pragma unroll 1
+        for (int it0 = 0, piece = 0; it0 < count && !leave; ++piece) {
             int last;
-            const int n = share_of(x, it, &last);
-            const int part = p.parts == 1 ? 0 : x.r % p.parts, heads = min(GP, p.group - part * GP);
-            const int tile0 = w.s + it;
-            for (int k = 0; k < n; ++k, ++it) {
+            const int n = share_of(x, it0, &last);
+            const int heads = min(GP, p.group - x.part * GP);
+            const int tile0 = w.s + it0;
+            const uint32_t my_o = my_tmem + S::kTmemO + ((piece & 1) * 2 + group) * S::kOCols;
+            const int k0 = (it0 ^ group) & 1;
+#pragma unroll 1
+            for (int k = k0; k < n; k += 2) {
                 // Columns of heads past `heads` hold whatever lies there, and nothing looks at what comes of them.
-                const int buf = it & 1, valid = k + 1 < n ? kTile : last;
+                const int it = it0 + k, valid = k + 1 < n ? kTile : last;
                 float s[GP], e[GP];
-                ok = ok && wait(S::kSFull + buf, (it >> 1) & 1);
+                ok = ok && wait(S::kSFull + group, (it >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < GP; g += 8) tmem_ld<GP < 8 ? GP : 8>(my_tmem + S::kTmemS + buf * 16 + g, s + g);
+                for (int g = 0; g < GP; g += 8) tmem_ld<GP < 8 ? GP : 8>(my_s + g, s + g);
                 tmem_wait_ld();
                 tc_fence_before();
-                mbar_arrive_at(bar0 + (S::kSFree + buf) * 8);
+                mbar_arrive_at(bar0 + (S::kSFree + group) * 8);
                 bool over = true;
-                if (k > 0) {
+                if (k > k0) {
                     float top = -INFINITY;
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
                         e[g] = fmaf(s[g], c, offset[g]);
                         top = fmaxf(top, e[g]);
                     }
-                    over = bar_any(1, kSoftmax, (top > kSlack + kBias && tid < valid) || !ok);
+                    over = bar_any(1 + group, kSoftmax, (top > kSlack + kBias && me < valid) || !ok);
                 }
                 // Some score has passed the reference by kSlack, or there is no reference yet.
                 if (over) {
-                    leave = bar_any(1, kSoftmax, !ok);
+                    leave = bar_any(1 + group, kSoftmax, !ok);
                     if (leave) break;
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
-                        const float top = warp_max(tid < valid ? s[g] * c : -INFINITY);
-                        if (lane == 0) red[warp][g] = top;
+                        const float top = warp_max(me < valid ? s[g] * c : -INFINITY);
+                        if (lane == 0) red[group][quarter][g] = top;
                     }
-                    bar_sync(1, kSoftmax);
+                    bar_sync(1 + group, kSoftmax);
+                    if (me < GP) {
+                        const float top = fmaxf(fmaxf(red[group][0][me], red[group][1][me]),
+                                                fmaxf(red[group][2][me], red[group][3][me]));
+                        const float to = k == k0 ? top : fmaxf(my_m, top);
+                        first_of[me] = k == k0 ? 0.f : to == my_m ? 1.f : exp2_approx(my_m - to);
+                        second_of[me] = offset_of(to);
+                        my_m = to;
+                    }
+                    bar_sync(1 + group, kSoftmax);
                     float f[GP];
+                    load_row<GP>(first_of, f);
+                    load_row<GP>(second_of, offset);
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
-                        const float top = fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g]));
-                        const float to = k == 0 ? top : fmaxf(m[g], top);
-                        f[g] = k == 0 ? 0.f : to == m[g] ? 1.f : exp2_approx(m[g] - to);
-                        l[g] = k == 0 ? 0.f : l[g] * f[g];
-                        m[g] = to;
-                        offset[g] = offset_of(to);
+                        l[g] = k == k0 ? 0.f : l[g] * f[g];
                         e[g] = fmaf(s[g], c, offset[g]);
                     }
-                    if (k > 0) {
-                        ok = wait(S::kPFree + (buf ^ 1), ((it - 1) >> 1) & 1);  // the tile before is in O
+                    if (k > k0) {
+                        ok = wait(S::kPFree + group, ((it >> 1) & 1) ^ 1);  // the group's tile before is in O
                         __syncwarp();
                         tc_fence_after();
                         constexpr int kStep = 2 * GP < 8 ? 2 * GP : 8;
@@ -541,7 +758,7 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
 #pragma unroll
                             for (int j = 0; j < 2 * GP; j += kStep) {
                                 float v[kStep];
-                                const uint32_t at = my_tmem + S::kTmemO + o * S::kPCols + j;
+                                const uint32_t at = my_o + o * S::kPCols + j;
                                 tmem_ld<kStep>(at, v);
                                 tmem_wait_ld();
 #pragma unroll
@@ -555,25 +772,24 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                 }
 #pragma unroll
                 for (int g = 0; g < GP; ++g) e[g] = exp2_approx(e[g]);
-                if (tid >= valid)
+                if (me >= valid)
 #pragma unroll
                     for (int g = 0; g < GP; ++g) e[g] = 0.f;
 #pragma unroll
                 for (int g = 0; g < GP; ++g) l[g] += e[g];
                 if (p.p) {
-                    store_row<GP>(p.p + ((size_t)(tile0 + k) * kTile + tid) * GP, e);
-                    if (tid == 0) store_row<GP>(p.tile_m + (size_t)(tile0 + k) * GP, m);
+                    store_row<GP>(p.p + ((size_t)(tile0 + k) * kTile + me) * GP, e);
+                    if (me < GP) p.tile_m[(size_t)(tile0 + k) * GP + me] = my_m;
                 }
                 uint32_t word[GP];
                 if (p.c.bf16) split<true, GP>(e, word); else split<false, GP>(e, word);
-                if (it >= 2) ok = ok && wait(S::kPFree + buf, ((it >> 1) & 1) ^ 1);
-                const uint32_t row = p_buf + buf * S::kPBytes + tid * S::kPRow;
+                if (it >= 2) ok = ok && wait(S::kPFree + group, ((it >> 1) & 1) ^ 1);
                 if constexpr (GP == 1) {
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + (turn << 4)), "r"(word[0]) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(my_p + (turn << 4)), "r"(word[0]) : "memory");
                 } else {
 #pragma unroll
                     for (int i = 0; i < GP / 4; ++i)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((i ^ turn) << 4)),
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(my_p + ((i ^ turn) << 4)),
                                      "r"(word[4 * i]), "r"(word[4 * i + 1]), "r"(word[4 * i + 2]), "r"(word[4 * i + 3])
                                      : "memory");
                 }
@@ -582,7 +798,8 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                     const int item = it + 1 < count ? 2 * it + 2 : 2 * count - 1, st = item % S::kRing;
                     ok = ok && wait(S::kFull + st, (item / S::kRing) & 1);
                     const int pad = (16 - (valid & 15)) * S::kSub * 8;
-                    for (int i = tid; ok && i < pad; i += kSoftmax)
+#pragma unroll 1
+                    for (int i = me; ok && i < pad; i += kSoftmax)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          ring + st * S::kItem + i / 8 % S::kSub * (kTile * 128) +
                                          (valid + i / (S::kSub * 8)) * 128 + (i & 7) * 16),
@@ -590,137 +807,113 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
                                      : "memory");
                 }
                 fence_proxy_async_smem();
-                mbar_arrive_at(bar0 + (S::kPReady + buf) * 8);
+                mbar_arrive_at(bar0 + (S::kPReady + group) * 8);
             }
             if (leave) break;
 
-            // The end of the row's share: sums over the 128 slots' threads, then O.
-            const int final_it = it - 1;
-            const float sum = warp_sums<GP>(l, lane);
-            ok = ok && wait(S::kPFree + (final_it & 1), (final_it >> 1) & 1);
-            leave = bar_any(1, kSoftmax, !ok);
-            if (leave) break;
-            if ((lane & (32 / GP - 1)) == 0) red[warp][warp_head<GP>(lane)] = sum;
-            bar_sync(1, kSoftmax);
-            tc_fence_after();
+            // The end of the row's share: sums over the slots' threads, of this
+            // group and of the other.  A group without a tile of the row has
+            // nothing to tell, but says so; it is never more than three rows
+            // ahead of the other, since products are made in order.
+            const int final_it = it0 + n - 1, slot4 = piece & 3;
+            it0 += n;
+            if (k0 < n) {
+                const float sum = warp_sums<GP>(l, lane);
+                if ((final_it & 1) != group) {
+                    if ((lane & (32 / GP - 1)) == 0) told_l[slot4][quarter][warp_head<GP>(lane)] = sum;
+                    if (me < GP) told_m[slot4][me] = my_m;
+                } else {
+                    ok = ok && wait(S::kTold + slot4, (piece >> 2) & 1);
+                    ok = ok && wait(S::kPFree + group, (final_it >> 1) & 1);  // and all products before it
+                    leave = bar_any(1 + group, kSoftmax, !ok);
+                    if (leave) break;
+                    if ((lane & (32 / GP - 1)) == 0) red[group][quarter][warp_head<GP>(lane)] = sum;
+                    bar_sync(1 + group, kSoftmax);
+                }
+            }
+            if ((final_it & 1) != group) {
+                mbar_arrive_at(bar0 + (S::kTold + slot4) * 8);
+                x.t += n - 1;
+                x.next(p);
+                continue;
+            }
             const int row_start = tile0 - x.t;  // tile number of the row's first tile
             const bool whole = row_start >= w.s && row_start + x.tiles <= w.e;
             const int share = 2 * blockIdx.x + (row_start >= w.s ? 1 : 0);
-            const int q0 = x.b * p.a.q_heads + (p.parts == 1 ? x.r : x.r / p.parts) * p.group + part * GP;
-            float2* row_ml = p.row_ml + ((size_t)x.b * p.rows + x.r) * GP;
-            constexpr int kStep = 2 * GP < 8 ? 2 * GP : 8;
-            float v[S::kOBlocks][2 * GP];
-#pragma unroll
-            for (int o = 0; o < S::kOBlocks; ++o)
-#pragma unroll
-                for (int j = 0; j < 2 * GP; j += kStep)
-                    tmem_ld<kStep>(my_tmem + S::kTmemO + o * S::kPCols + j, v[o] + j);
-#pragma unroll
-            for (int g = 0; g < GP; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
-            tmem_wait_ld();
-            tc_fence_before();
-            if (tid < heads) {
-                float2 ml = make_float2(m[0], l[0]);
-#pragma unroll
-                for (int g = 1; g < GP; ++g)
-                    if (g == tid) ml = make_float2(m[g], l[g]);
-                if (ml.y != ml.y) ml.x = 0.f;  // a NaN sum says it all
-                (whole ? row_ml : p.part_ml + share * GP)[tid] = ml;
-                if (whole && p.a.lse) p.a.lse[q0 + tid] = lse_of(ml);
+            const int q0 = x.b * p.a.q_heads + x.h * p.group + x.part * GP;
+            float2* row_ml = p.row_ml + (size_t)x.row(p) * GP;
+            if (me < GP) {
+                // The two groups' sums on a common reference, and the factor of each one's O.
+                float2 ml = make_float2(my_m, (red[group][0][me] + red[group][1][me]) +
+                                                  (red[group][2][me] + red[group][3][me]));
+                float fa = 1.f, fb = 0.f;
+                if (n > 1) {
+                    const float mb = told_m[slot4][me], lb = (told_l[slot4][0][me] + told_l[slot4][1][me]) +
+                                                             (told_l[slot4][2][me] + told_l[slot4][3][me]);
+                    const float to = fmaxf(ml.y == 0.f ? -INFINITY : ml.x, lb == 0.f ? -INFINITY : mb);
+                    fa = ml.y == 0.f ? 0.f : exp2_approx(ml.x - to);
+                    fb = lb == 0.f ? 0.f : exp2_approx(mb - to);
+                    ml = make_float2(to, ml.y * fa + lb * fb);
+                }
+                if (ml.y != ml.y || ml.y == 0.f) ml.x = 0.f;  // a NaN sum, or none, says it all
+                if (me < heads) {
+                    (whole ? row_ml : p.part_ml + share * GP)[me] = ml;
+                    if (whole && p.a.lse) p.a.lse[q0 + me] = lse_of(ml);
+                }
+                if (whole) {
+                    const float r = ml.y == 0.f ? 0.f : __frcp_rn(ml.y);
+                    fa *= r;
+                    fb *= r;
+                }
+                first_of[me] = fa;
+                second_of[me] = fb;
             }
-#pragma unroll
-            for (int g = 0; g < GP; ++g) l[g] = !whole ? 1.f : l[g] == 0.f ? 0.f : __frcp_rn(l[g]);
-#pragma unroll
+            bar_sync(1 + group, kSoftmax);
+            tc_fence_after();
+#pragma unroll 1
             for (int o = 0; o < S::kOBlocks; ++o) {
                 // 64 rows of a product lie in the first 16 lanes of each warp's 32.
-                const int d = S::kM == 64 ? warp * 16 + lane : o * 128 + tid;
-                if ((S::kM == 64 && lane >= 16) || d >= p.c.dim) continue;
+                const int d = S::kM == 64 ? quarter * 16 + lane : o * 128 + me;
+                const bool in = (S::kM == 128 || lane < 16) && d < p.c.dim;
+                constexpr int kStep = GP < 8 ? GP : 8;
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    if (g >= heads) break;
-                    const float y = v[o][g] + v[o][GP + g];
-                    if (whole)
-                        p.a.out[(size_t)(q0 + g) * p.c.dim + d] = from_float(l[g] == 0.f ? 0.f : y * l[g], p.c.bf16);
-                    else
-                        p.part_o[((size_t)share * GP + g) * p.c.dim + d] = y;
-                }
-            }
-            if (!whole) {
-                const int c0 = w.block_of(row_start), c1 = w.block_of(row_start + x.tiles - 1), pieces = c1 - c0 + 1;
-                // Adds up the shares of `n` blocks, `stride` apart from `first` on: into the
-                // output, or (not the row's last step) into the first one's share.
-                auto join = [&](int first, int stride, int n, bool final) {
-                    for (int g = warp; g < heads; g += kSoftmax / 32) {
-                        float2 ml = make_float2(0.f, 0.f);
-                        const int c = first + lane * stride;
-                        if (lane < n) ml = __ldcg(&p.part_ml[(2 * c + (c == c0)) * GP + g]);
-                        const float top = warp_max(ml.y == 0.f ? -INFINITY : ml.x);
-                        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
-                        float sum = ml.y * f;
-                        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-                        if (lane < n) factor[lane][g] = f;
-                        if (lane == 0) joined[g] = make_float2(top, sum);
+                for (int j = 0; j < GP; j += kStep) {
+                    // hi and lo columns of this group's O, then of the other's
+                    float v[4][kStep], fa[kStep], fb[kStep];
+                    const uint32_t at = my_o + o * S::kPCols + j;
+                    const uint32_t other = group == 0 ? at + S::kOCols : at - S::kOCols;
+                    tmem_ld<kStep>(at, v[0]);
+                    tmem_ld<kStep>(at + GP, v[1]);
+                    if (n > 1) {
+                        tmem_ld<kStep>(other, v[2]);
+                        tmem_ld<kStep>(other + GP, v[3]);
                     }
-                    bar_sync(1, kSoftmax);
-                    const int quads = heads * p.c.dim / 4;
-                    for (int i = tid; i < quads; i += kSoftmax) {
-                        const int g = 4 * i / p.c.dim;
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int j = 0; j < n; ++j) {
-                            const int c = first + j * stride;
-                            const float4* from = reinterpret_cast<const float4*>(
-                                p.part_o + (size_t)(2 * c + (c == c0)) * GP * p.c.dim);
-                            const float4 y = __ldcg(from + i);
-                            const float f = factor[j][g];
-                            o.x = fmaf(y.x, f, o.x);
-                            o.y = fmaf(y.y, f, o.y);
-                            o.z = fmaf(y.z, f, o.z);
-                            o.w = fmaf(y.w, f, o.w);
-                        }
-                        if (final) {
-                            const float sum = joined[g].y, r = sum == 0.f ? 0.f : __frcp_rn(sum);
-                            uint2 word;
-                            word.x = from_float(sum == 0.f ? 0.f : o.x * r, p.c.bf16) |
-                                     (uint32_t)from_float(sum == 0.f ? 0.f : o.y * r, p.c.bf16) << 16;
-                            word.y = from_float(sum == 0.f ? 0.f : o.z * r, p.c.bf16) |
-                                     (uint32_t)from_float(sum == 0.f ? 0.f : o.w * r, p.c.bf16) << 16;
-                            *reinterpret_cast<uint2*>(p.a.out + (size_t)q0 * p.c.dim + 4 * i) = word;
-                        } else {
-                            reinterpret_cast<float4*>(p.part_o + (size_t)(2 * first + (first == c0)) * GP * p.c.dim)[i] = o;
-                        }
+                    load_row<kStep>(first_of + j, fa);
+                    load_row<kStep>(second_of + j, fb);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) {
+                        // A head with no sum has a factor of 0, also where its products are not numbers.
+                        v[0][i] = fa[i] == 0.f ? 0.f : (v[0][i] + v[1][i]) * fa[i];
+                        if (n > 1 && fb[i] != 0.f) v[0][i] += (v[2][i] + v[3][i]) * fb[i];
                     }
-                    if (tid < heads) {
-                        float2 ml = joined[tid];
-                        if (ml.y != ml.y || ml.y == 0.f) ml.x = 0.f;
-                        (final ? row_ml : p.part_ml + (2 * first + (first == c0)) * GP)[tid] = ml;
-                        if (final && p.a.lse) p.a.lse[q0 + tid] = lse_of(ml);
-                    }
-                };
-                // Whether this block is the last of n to arrive at a counter, which is then zero again.
-                auto last_of = [&](unsigned* counter, int n) {
-                    bar_sync(1, kSoftmax);
-                    if (tid == 0) {  // releases what the barrier collected, and acquires the others'
-                        unsigned before;
-                        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-                        if (before + 1 == (unsigned)n) *counter = 0;
-                        arrived = before + 1;
-                    }
-                    bar_sync(1, kSoftmax);
-                    return arrived == (unsigned)n;
-                };
-                if (pieces <= kJoin) {
-                    if (last_of(p.done + 2 * c0 + 1, pieces)) join(c0, 1, pieces, true);
-                } else {
-                    // Two steps: kJoin neighbours each, then what they left (at most kJoin * kJoin pieces).
-                    const int first = c0 + ((int)blockIdx.x - c0) / kJoin * kJoin, n = min(kJoin, c1 - first + 1);
-                    if (last_of(p.done + 2 * first + (first == c0), n)) {
-                        join(first, 1, n, false);
-                        const int groups = (pieces + kJoin - 1) / kJoin;
-                        if (last_of(p.done + 2 * gridDim.x + c0, groups)) join(c0, kJoin, groups, true);
+                    if (whole) {
+                        uint16_t* to = p.a.out + (size_t)(q0 + j) * p.c.dim + d;
+#pragma unroll
+                        for (int i = 0; i < kStep; ++i)
+                            if (in && j + i < heads) to[i * p.c.dim] = from_float(v[0][i], p.c.bf16);
+                    } else {
+                        float* to = p.part_o + ((size_t)share * GP + j) * p.c.dim + d;
+#pragma unroll
+                        for (int i = 0; i < kStep; ++i)
+                            if (in && j + i < heads) to[i * p.c.dim] = v[0][i];
                     }
                 }
             }
+            tc_fence_before();
+            if (!whole)
+                join_row<GP>(p, x.total, x.blocks, row_start, x.tiles, q0, heads, row_ml, factor[group], joined[group],
+                             &arrived[group], 1 + group, me);
             x.t += n - 1;
             x.next(p);
         }
@@ -729,12 +922,15 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
     tc_fence_after();
     if (warp == kMmaS) tmem_dealloc(tmem, S::kTmemCols);
     // What sequences without slots give.
+#pragma unroll 1
     for (int b = blockIdx.x; b < p.c.seqs; b += gridDim.x) {
-        if (p.c.len(b) > 0) continue;
+        if (p.c.lens[b] > 0) continue;
         const size_t first = (size_t)b * p.a.q_heads;
+#pragma unroll 1
         for (int i = tid; i < p.a.q_heads * (p.c.dim / 8); i += kThreads)
             reinterpret_cast<int4*>(p.a.out + first * p.c.dim)[i] = make_int4(0, 0, 0, 0);
         if (p.a.lse)
+#pragma unroll 1
             for (int i = tid; i < p.a.q_heads; i += kThreads) p.a.lse[first + i] = -INFINITY;
     }
 }
@@ -743,22 +939,25 @@ kv_attend_kernel(const AttendArgs p, const __grid_constant__ CUtensorMap map_k, 
 // sum.  Block c takes the tiles that block c of the first launch had, so its
 // p may still be in L2; a warp takes a tile, all its loads in flight at once.
 template <int GP>
-__global__ void __launch_bounds__(kWeightThreads) kv_weight_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kWeightThreads) kv_weight_kernel(const __grid_constant__ AttendArgs p) {
     constexpr int kWarps = kWeightThreads / 32;
-    __shared__ int scan[kWarps + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Walk w = find_range<kWeightThreads>(p, scan);
+    launch_dependents();
     grid_dependency_wait();
+    Walk w;
+    w.load(p.walk + blockIdx.x * Walk::kWords);
+#pragma unroll 1
     for (int tile = w.s; tile < w.e;) {
         const int count = min(w.tiles - w.t, w.e - tile);  // this block's tiles of the row
-        const int part = w.r % p.parts, h = w.r / p.parts;
         // Of a group in several parts, the block that has the first adds up all.
-        for (int pt = 0; part == 0 && pt < p.parts; ++pt) {
+#pragma unroll 1
+        for (int pt = 0; w.part == 0 && pt < p.parts; ++pt) {
             const int heads = min(GP, p.group - pt * GP);
-            const float* wi = pt == 0 ? p.a.weight.row(w.b, h) : p.a.weight_out.row(w.b, h);
-            float* wo = p.a.weight_out.row(w.b, h);
+            const float* wi = pt == 0 ? p.a.weight.row(w.b, w.h) : p.a.weight_out.row(w.b, w.h);
+            float* wo = p.a.weight_out.row(w.b, w.h);
             float2 ml = make_float2(0.f, 0.f);
-            if (lane < heads) ml = p.row_ml[((size_t)w.b * p.rows + w.r + pt) * GP + lane];
+            if (lane < heads) ml = p.row_ml[((size_t)w.row(p) + pt) * GP + lane];
+#pragma unroll 1
             for (int k = warp; k < count; k += kWarps) {
                 const size_t x = tile + k + (size_t)pt * w.tiles;
                 const int slot0 = (w.t + k) * kTile + lane;
@@ -837,7 +1036,7 @@ cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, int rank, co
 // with them.
 int group_part(const KvCache& c, const KvAttend& a) {
     const int group = a.q_heads / c.heads;
-    return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 ? 8 : 16;
+    return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 || c.dim > 128 ? 8 : 16;
 }
 
 int sm_count(int device) {
@@ -880,7 +1079,9 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
     p.row_ml = static_cast<float2*>(take(rows * gp * 8));
     p.p = nullptr;
     p.tile_m = nullptr;
+    p.walk = nullptr;
     if (a.weight.data) {
+        p.walk = static_cast<int*>(take(plan.blocks * Walk::kWords * 4));
         p.p = static_cast<float*>(take(tiles * kTile * gp * 4));
         p.tile_m = static_cast<float*>(take(tiles * gp * 4));
     }
@@ -894,8 +1095,8 @@ cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, in
     auto kernel = kv_attend_kernel<DP, GP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<plan.blocks, kThreads, Sh::kSmem, s>>>(plan.args, maps[0], maps[1], maps[2]);
-    e = cudaGetLastError();
+    // Started early, it sets up its barriers and waits for the launch before it.
+    e = launch_pdl(kernel, dim3(plan.blocks), dim3(kThreads), Sh::kSmem, s, plan.args, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess) return e;
     ++*launches;
     if (!plan.args.p) return cudaSuccess;
@@ -910,8 +1111,10 @@ cudaError_t launch_dim(const Plan& plan, int gp, cudaStream_t s, const CUtensorM
         case 1: return launch<DP, 1>(plan, s, maps, launches);
         case 4: return launch<DP, 4>(plan, s, maps, launches);
         case 8: return launch<DP, 8>(plan, s, maps, launches);
-        default: return launch<DP, 16>(plan, s, maps, launches);
+        default: break;
     }
+    if constexpr (DP <= 128) return launch<DP, 16>(plan, s, maps, launches);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
