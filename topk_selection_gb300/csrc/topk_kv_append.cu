@@ -1,13 +1,19 @@
 // topk_kv_append: copy new tokens' keys and values into their pages.
 //
-// Nothing is computed: bound by HBM for prompts and by the launch for a
-// decoding step.  A warp takes one token's head and moves its key and value
-// as 16-byte vectors, half of the warp each.
+// Nothing is computed: bound by HBM for prompts (every element is read and
+// written once) and by the launch for a decoding step.  An item is one
+// token's head, its key and value copied as 16-byte vectors.  A warp takes up
+// to 32 items: a lane looks up one item's place, and all lanes copy, eight
+// vectors in flight each.  With few items a warp takes one, so that a step of
+// decoding is spread over the GPU.  The copies' reads do not depend on the
+// look-up, so the first are under way while it runs.
 #include "topk_device.cuh"
 #include "topk_kv.cuh"
 
 namespace topk {
 namespace {
+
+constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
     KvCache c;
@@ -18,39 +24,84 @@ struct AppendArgs {
     KvRows<float> weight;
     KvRows<int> pos;
     const int* next_pos;
+    int per;    // items of a warp
+    int shift;  // log2 of the places that an item's vectors take
 };
 
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int t = (int)(item / a.c.heads), h = (int)(item % a.c.heads);
-    if (t >= a.tokens) return;
-    int b = t, i = 0;
-    if (a.starts) {
-        if (t >= a.starts[a.c.seqs]) return;
-        int lo = 0, hi = a.c.seqs - 1;  // the last sequence whose tokens start at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.starts[mid] <= t) lo = mid; else hi = mid - 1;
+// The last sequence whose tokens start at or before t: 32 candidates a round.
+__device__ __forceinline__ int find_seq(const int* starts, int seqs, int t, int lane) {
+    int base = 0, range = seqs;
+    while (range > 1) {
+        const int step = (range + 31) / 32, at = base + lane * step;
+        const bool on = lane * step < range && starts[at] <= t;
+        const int k = 31 - __clz(__ballot_sync(kFullMask, on) | 1u);
+        base += k * step;
+        range = min(step, range - k * step);
+    }
+    return base;
+}
+
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    constexpr int kUnroll = 8;
+    __shared__ int4 where[kAppendThreads / 32][32];  // token, head, page (-1: nowhere) and slot in it
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long items = (long long)a.tokens * a.c.heads;
+    const long long first = ((long long)blockIdx.x * (kAppendThreads / 32) + warp) * a.per;
+    if (first >= items) return;
+    const int count = (int)min((long long)a.per, items - first);
+    const int t = (int)((first + lane) / a.c.heads), h = (int)(first + lane - (long long)t * a.c.heads);
+    where[warp][lane] = make_int4(t, h, -1, 0);
+    __syncwarp();
+    // An item's vectors, its key's and then its value's, take a power of two
+    // of places, so that no vector costs a division.
+    const int vecs = a.c.dim / 8, total = count << a.shift, mask = (1 << a.shift) - 1;
+    bool looked_up = false;
+    for (int i0 = lane; i0 - lane < total; i0 += 32 * kUnroll) {
+        int4 data[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + 32 * u, in = i & mask;
+            if (i < total && in < 2 * vecs) {
+                const int4 at = where[warp][i >> a.shift];
+                const bool v = in >= vecs;
+                const uint16_t* src = v ? a.v_new + at.x * a.vns[0] + at.y * a.vns[1] + (in - vecs) * 8
+                                        : a.k_new + at.x * a.kns[0] + at.y * a.kns[1] + in * 8;
+                data[u] = __ldcs(reinterpret_cast<const int4*>(src));
+            }
         }
-        b = lo;
-        i = t - a.starts[b];
-    }
-    const int slot = a.c.len(b) + i;
-    if (i < 0 || slot >= a.c.capacity()) return;
-    const int page = a.c.page_of(b, slot);
-    const int at = slot % a.c.page_size;
-    if (page >= 0) {
-        const bool v = lane >= 16;
-        const uint16_t* src = v ? a.v_new + t * a.vns[0] + h * a.vns[1] : a.k_new + t * a.kns[0] + h * a.kns[1];
-        uint16_t* dst = v ? a.c.v + page * a.c.vs[0] + at * a.c.vs[1] + h * a.c.vs[2]
-                          : a.c.k + page * a.c.ks[0] + at * a.c.ks[1] + h * a.c.ks[2];
-        for (int x = (lane & 15) * 8; x < a.c.dim; x += 128)
-            *reinterpret_cast<int4*>(dst + x) = *reinterpret_cast<const int4*>(src + x);
-    }
-    if (lane == 0) {
-        if (a.weight.data) a.weight.row(b, h)[slot] = 0.f;
-        if (a.pos.data) a.pos.row(b, h)[slot] = a.next_pos[b] + i;
+        if (!looked_up) {
+            looked_up = true;
+            int b = a.starts ? find_seq(a.starts, a.c.seqs, __shfl_sync(kFullMask, t, 0), lane) : t;
+            if (lane < count) {
+                int i = 0;
+                bool in = true;
+                if (a.starts) {
+                    int next = a.starts[b + 1];
+                    while (next <= t && b + 1 < a.c.seqs) next = a.starts[++b + 1];
+                    in = t < next;  // else past the last sequence's tokens
+                    i = t - a.starts[b];
+                }
+                const int slot = a.c.len(b) + i;
+                if (in && i >= 0 && slot < a.c.capacity()) {
+                    where[warp][lane].z = a.c.page_of(b, slot);
+                    where[warp][lane].w = slot % a.c.page_size;
+                    if (a.weight.data) a.weight.row(b, h)[slot] = 0.f;
+                    if (a.pos.data) a.pos.row(b, h)[slot] = a.next_pos[b] + i;
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + 32 * u, in = i & mask;
+            if (i < total && in < 2 * vecs) {
+                const int4 at = where[warp][i >> a.shift];
+                const bool v = in >= vecs;
+                uint16_t* dst = v ? a.c.v + at.z * a.c.vs[0] + at.w * a.c.vs[1] + at.y * a.c.vs[2] + (in - vecs) * 8
+                                  : a.c.k + at.z * a.c.ks[0] + at.w * a.c.ks[1] + at.y * a.c.ks[2] + in * 8;
+                if (at.z >= 0) *reinterpret_cast<int4*>(dst) = data[u];
+            }
+        }
     }
 }
 
@@ -60,11 +111,13 @@ cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k
                              const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
                              KvRows<float> weight, KvRows<int> pos, const int* next_pos) {
     AppendArgs a = {c, k_new, v_new, {k_stride[0], k_stride[1]}, {v_stride[0], v_stride[1]},
-                    tokens, starts, weight, pos, next_pos};
-    const long long warps = (long long)tokens * c.heads;
-    const long long blocks = (warps + 7) / 8;
+                    tokens, starts, weight, pos, next_pos, 1, 1};
+    while ((1 << a.shift) < c.dim / 4) ++a.shift;
+    const long long items = (long long)tokens * c.heads;
+    while (a.per < 32 && items / (2 * a.per) >= 152 * 16) a.per *= 2;  // 16 warps an SM at least, then longer ones
+    const long long warps = (items + a.per - 1) / a.per, blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    kv_append_kernel<<<(unsigned)blocks, 256, 0, s>>>(a);
+    kv_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -319,7 +319,7 @@ __device__ __forceinline__ void join_shares(const AttendArgs& p, int c0, int fir
                                          int heads, float2* row_ml, float (*factor)[GP], float2* joined, int bar,
                                          int me) {
     // A warp has every fourth head, a lane one share; all loads are in flight at once.
-    constexpr int kMine = GP < 4 ? 1 : GP / 4, kFly = 16;
+    constexpr int kMine = GP < 4 ? 1 : GP / 4, kFly = 8;
     const int lane = me & 31, quarter = me >> 5;
     float2 ml[kMine];
 #pragma unroll
@@ -343,39 +343,52 @@ __device__ __forceinline__ void join_shares(const AttendArgs& p, int c0, int fir
     }
     bar_sync(bar, kSoftmax);
     const int quads = heads * p.c.dim / 4;
-    const size_t share = (size_t)GP * p.c.dim / 4 * 2 * stride;  // from one share to the next
+    const int share = GP * p.c.dim / 4 * 2 * stride;  // from one share to the next
+    // Two quads of elements of eight shares at a time.
 #pragma unroll 1
-    for (int i = me; i < quads; i += kSoftmax) {
-        const int g = 4 * i / p.c.dim;
-        const float4* from = reinterpret_cast<const float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim) + i;
-        const float4* from0 = from + (first == c0 ? GP * p.c.dim / 4 : 0);  // the row's first block has its own place
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = me; i0 < quads; i0 += 2 * kSoftmax) {
+        float4 o[2] = {};
+        int g[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) g[q] = min(4 * (i0 + q * kSoftmax) / p.c.dim, GP - 1);
+        const float4* from = reinterpret_cast<const float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim) + i0;
+        const int own = first == c0 ? GP * p.c.dim / 4 : 0;  // the row's first block has a place of its own
 #pragma unroll 1
         for (int j0 = 0; j0 < n; j0 += kFly) {
-            float4 y[kFly];
+            float4 y[2][kFly];
 #pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j0 + j < n) y[j] = __ldcg(j0 + j == 0 ? from0 : from + (j0 + j) * share);
-            }
+            for (int j = 0; j < kFly; ++j)
 #pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                const float f = j0 + j < n ? factor[j0 + j][g] : 0.f;
-                o.x = fmaf(y[j].x, f, o.x);
-                o.y = fmaf(y[j].y, f, o.y);
-                o.z = fmaf(y[j].z, f, o.z);
-                o.w = fmaf(y[j].w, f, o.w);
-            }
+                for (int q = 0; q < 2; ++q) {
+                    y[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (j0 + j < n && i0 + q * kSoftmax < quads)
+                        y[q][j] = __ldcg(from + (j0 + j == 0 ? own : (j0 + j) * share) + q * kSoftmax);
+                }
+#pragma unroll
+            for (int j = 0; j < kFly; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float f = j0 + j < n ? factor[j0 + j][g[q]] : 0.f;
+                    o[q].x = fmaf(y[q][j].x, f, o[q].x);
+                    o[q].y = fmaf(y[q][j].y, f, o[q].y);
+                    o[q].z = fmaf(y[q][j].z, f, o[q].z);
+                    o[q].w = fmaf(y[q][j].w, f, o[q].w);
+                }
         }
-        if (final) {
-            const float sum = joined[g].y, r = sum == 0.f ? 0.f : __frcp_rn(sum);
-            if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-            uint2 word;
-            word.x = from_float(o.x * r, p.c.bf16) | (uint32_t)from_float(o.y * r, p.c.bf16) << 16;
-            word.y = from_float(o.z * r, p.c.bf16) | (uint32_t)from_float(o.w * r, p.c.bf16) << 16;
-            *reinterpret_cast<uint2*>(p.a.out + (size_t)q0 * p.c.dim + 4 * i) = word;
-        } else {
-            reinterpret_cast<float4*>(p.part_o + (size_t)(2 * first + (first == c0)) * GP * p.c.dim)[i] = o;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int i = i0 + q * kSoftmax;
+            if (i >= quads) break;
+            if (final) {
+                const float sum = joined[g[q]].y, r = sum == 0.f ? 0.f : __frcp_rn(sum);
+                if (sum == 0.f) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                uint2 word;
+                word.x = from_float(o[q].x * r, p.c.bf16) | (uint32_t)from_float(o[q].y * r, p.c.bf16) << 16;
+                word.y = from_float(o[q].z * r, p.c.bf16) | (uint32_t)from_float(o[q].w * r, p.c.bf16) << 16;
+                *reinterpret_cast<uint2*>(p.a.out + (size_t)q0 * p.c.dim + 4 * i) = word;
+            } else {
+                reinterpret_cast<float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim)[own + i] = o[q];
+            }
         }
     }
     if (me < heads) {

@@ -41,6 +41,7 @@ struct EvictArgs {
     int* movers;  // [seqs * heads][room]: the movers, in the row's last M places
     int room;     // moves a row's lists have room for
     int chunks;   // blocks of the second launch per row
+    int shift;    // log2 of the places that a move's vectors take: no vector costs a division
     int part;     // slots a block of the first has room for in shared memory
 };
 
@@ -322,16 +323,16 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
         __syncwarp();
         where[warp][lane] = at;
         __syncwarp();
-        const int total = min(32, moves - j0) * 2 * vecs;
+        const int total = min(32, moves - j0) << a.shift, mask = (1 << a.shift) - 1;
         for (int i0 = lane; i0 < total; i0 += 32 * kUnroll) {
             int4 data[kUnroll];
             uint16_t* dst[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u, m = i / (2 * vecs), in = i - m * 2 * vecs;
+                const int i = i0 + 32 * u, in = i & mask;
                 dst[u] = nullptr;
-                if (i < total) {
-                    const int4 q = where[warp][m];
+                if (i < total && in < 2 * vecs) {
+                    const int4 q = where[warp][i >> a.shift];
                     if (q.x >= 0) {
                         const bool second = in >= vecs;
                         const uint16_t* base = second ? v : k;
@@ -407,6 +408,8 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
         err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
     if (err != cudaSuccess) return err;
     ++*launches;
+    a.shift = 1;
+    while ((1 << a.shift) < c.dim / 4) ++a.shift;
     a.chunks = (a.room + kMoveThreads - 1) / kMoveThreads;
     const long long most = (1 << 20) / rows + 1;
     if (a.chunks > most) a.chunks = (int)most;
