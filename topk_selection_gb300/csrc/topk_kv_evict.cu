@@ -55,13 +55,25 @@ __device__ __forceinline__ unsigned evict_key(float w, int pos, int sink, int re
     return key;
 }
 
+// A barrier of the cluster that makes the blocks' shared memory visible to one
+// another.  One thread's fence does for all of its block, after the block's
+// barrier: a release by every thread takes several times as long.
+__device__ __forceinline__ void cluster_sync(int tid) {
+    __syncthreads();
+    if (tid == 0) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // kHeld: the block's keys fit its shared memory; otherwise they are made anew
 // from global memory (L2) in each pass.
 template <int THREADS, bool kHeld>
 __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;
     extern __shared__ __align__(16) unsigned keys[];
-    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ __align__(16) int hist[2][kBins];   // of this digit; of the one before, or cleared for the next
+    __shared__ int coarse[2][kWarps];              // the same by kPer * 32 bins, the highest first
+    __shared__ int far_coarse[kMostBlocks][32], far_bins[kMostBlocks][kPer][32];  // the cluster's
     __shared__ int scan[kWarps];
     __shared__ int found[2];                       // the bin, and how many of its keys are kept
     __shared__ int4 tally;                         // this block: above and at the edge; the same below the budget
@@ -76,7 +88,6 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     float* wo = a.e.weight_out.row(b, h);
     int* po = a.e.pos_out.row(b, h);
     const bool copy_w = wo != w, copy_p = po != pos;
-    launch_dependents();  // the moves wait for this launch's end
     if (tid == 0 && h == 0 && rank == 0) a.lens[b] = n;
     // This block's slots: multiples of the warps' rounds.
     const int part = ((n + blocks - 1) / blocks + 31) & ~31, lo = min(rank * part, n), hi = min(lo + part, n);
@@ -125,7 +136,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         }
     };
     fetch(lo);
-    for (int i = tid; i < 3 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 2 * kBins; i += THREADS) (&hist[0][0])[i] = 0;
     if (tid == 0) tally = make_int4(0, 0, 0, 0);
     __syncthreads();
     for (int base = lo; base < end; base += 4 * THREADS) {
@@ -164,44 +175,87 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (((key[j] ^ prefix) >> up) == 0)
-                        atomicAdd(&hist[pass][(key[j] >> kShift[pass]) & (kWidth[pass] - 1)], 1);
+                        atomicAdd(&hist[pass & 1][(key[j] >> kShift[pass]) & (kWidth[pass] - 1)], 1);
             }
         }
-        if (blocks > 1) cluster.sync(); else __syncthreads();
-        // Thread t sums bins from the top: kPer of them, t = 0 the highest.
-        using Vec = typename std::conditional<kPer == 2, int2, int4>::type;
-        const int low_bin = kBins - kPer * (tid + 1);
-        int own[kPer] = {}, sum = 0;
-#pragma unroll
-        for (int r = 0; r < kMostBlocks; ++r) {
-            if (r >= blocks) break;
-            const int* from = blocks == 1 ? &hist[pass][0] : cluster.map_shared_rank(&hist[pass][0], r);
-            const Vec v = *reinterpret_cast<const Vec*>(from + low_bin);
-            const int* x = reinterpret_cast<const int*>(&v);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) own[j] += x[kPer - 1 - j];
-        }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += own[j];
-        int x = sum;
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(kFullMask, x, d);
-            if (lane >= d) x += y;
-        }
-        if (lane == 31) scan[warp] = x;
         __syncthreads();
-        const int before_warp = __reduce_add_sync(kFullMask, lane < warp ? scan[lane] : 0);
-        int before = before_warp + x - sum;
-        if (before < need && need <= before + sum) {
+        // Thread t has kPer bins, t = 0 the highest.
+        using Vec = typename std::conditional<kPer == 2, int2, int4>::type;
+        int* mine = hist[pass & 1];
+        auto bins_of = [&](const int* from, int t, int (&own)[kPer]) {  // highest first
+            const Vec v = *reinterpret_cast<const Vec*>(from + kBins - kPer * (t + 1));
+            const int* x = reinterpret_cast<const int*>(&v);
+            int sum = 0;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                if (before < need && need <= before + own[j]) {
-                    found[0] = kBins - 1 - (tid * kPer + j);
-                    found[1] = need - before;
+                own[j] = x[kPer - 1 - j];
+                sum += own[j];
+            }
+            return sum;
+        };
+        auto scan_warp = [&](int x) {
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(kFullMask, x, d);
+                if (lane >= d) x += y;
+            }
+            return x;
+        };
+        // The bin of thread t's among which the need-th key lies, `before` of them above.
+        auto look = [&](int t, const int (&own)[kPer], int before, int sum) {
+            if (before < need && need <= before + sum) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (before < need && need <= before + own[j]) {
+                        found[0] = kBins - 1 - (t * kPer + j);
+                        found[1] = need - before;
+                    }
+                    before += own[j];
                 }
-                before += own[j];
+            }
+        };
+        int own[kPer];
+        const int sum = bins_of(mine, tid, own);
+        if (blocks == 1) {
+            const int x = scan_warp(sum);
+            if (lane == 31) scan[warp] = x;
+            __syncthreads();
+            look(tid, own, __reduce_add_sync(kFullMask, lane < warp ? scan[lane] : 0) + x - sum, sum);
+        } else {
+            // Over the cluster in two steps, so that little is read from other
+            // blocks: the warp's worth of bins, then the bin in it.  A warp
+            // reads one block.
+            const int all = __reduce_add_sync(kFullMask, sum);
+            if (lane == 0) coarse[pass & 1][warp] = all;
+            cluster_sync(tid);
+            if (warp < blocks && lane < kWarps)
+                far_coarse[warp][lane] = cluster.map_shared_rank(&coarse[pass & 1][0], warp)[lane];
+            __syncthreads();
+            int v = 0;
+            if (lane < kWarps)
+                for (int r = 0; r < blocks; ++r) v += far_coarse[r][lane];
+            const int x = scan_warp(v), at = __ffs(__ballot_sync(kFullMask, x >= need)) - 1;
+            const int before = __shfl_sync(kFullMask, x - v, at), t = at * 32 + lane;
+            if (warp < blocks) {
+                bins_of(cluster.map_shared_rank(mine, warp), t, own);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) far_bins[warp][j][lane] = own[j];
+            }
+            __syncthreads();
+            if (warp == 0) {
+                int some = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    own[j] = 0;
+                    for (int r = 0; r < blocks; ++r) own[j] += far_bins[r][j][lane];
+                    some += own[j];
+                }
+                look(t, own, before + scan_warp(some) - some, some);
             }
         }
+        // The digit before has been read by every block: cleared for the one after this.
+        if (pass == 1)
+            for (int i = tid; i < kBins; i += THREADS) hist[0][i] = 0;
         __syncthreads();
         prefix |= (unsigned)found[0] << kShift[pass];
         need = found[1];
@@ -248,7 +302,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         atomicAdd(&tally.z, above_low);
         atomicAdd(&tally.w, ties_low);
     }
-    if (blocks > 1) cluster.sync(); else __syncthreads();
+    if (blocks > 1) cluster_sync(tid); else __syncthreads();
     int4 t = make_int4(0, 0, 0, 0);
     if (lane < blocks) t = blocks == 1 ? tally : *cluster.map_shared_rank(&tally, lane);
     const int up_low = __reduce_add_sync(kFullMask, t.z), all_ties_low = __reduce_add_sync(kFullMask, t.w);
@@ -270,7 +324,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (base + j * 32 >= to) break;
-            const int i = base + j * 32 + lane;
+            const int i0 = base + j * 32, i = i0 + lane;
             bool kept = key[j] >= least && least != 0;
             if (some) {
                 const unsigned at = __ballot_sync(kFullMask, key[j] == edge);
@@ -279,7 +333,11 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
             }
             const unsigned all = __ballot_sync(kFullMask, kept);
             const int before = kept_before + __popc(all & lanemask_lt());
-            if (i < budget) {
+            if (i0 + 32 <= budget) {  // alike for the warp, in nearly every round
+                if (!kept) holes[i - before] = i;
+            } else if (i0 >= budget) {
+                if (kept) movers[before] = i;
+            } else if (i < budget) {
                 if (!kept) holes[i - before] = i;
             } else if (kept) {
                 movers[before] = i;
@@ -287,7 +345,8 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
             kept_before += __popc(all);
         }
     }
-    if (blocks > 1) cluster.sync();  // no block leaves while another reads its counts
+    launch_dependents();  // the moves, which wait for this launch's end
+    if (blocks > 1) cluster_sync(tid);  // no block leaves while another reads its counts
 }
 
 // A warp takes 32 moves: a lane looks up one move's pages, then all lanes
@@ -394,11 +453,12 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     a.holes = a.moves + rows;
     a.movers = a.holes + (size_t)rows * a.room;
     // Blocks per row: as many as keep the SMs busy twice over, and leave each
-    // block 1024 slots at least.
+    // block 1024 slots at least.  (Clusters of 16 were slower: 8 rows of
+    // 131072 slots 49 us instead of 43, since not all eight run at once.)
     constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
     int blocks = 1;
-    while (blocks < kMostBlocks && (rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024)) blocks *= 2;
-    while (blocks < kMostBlocks && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
+    while (blocks < 8 && rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024) blocks *= 2;
+    while (blocks < 8 && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
     a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
     const bool held = a.part <= kMostHeld;
     cudaError_t err;
