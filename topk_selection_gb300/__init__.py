@@ -1,7 +1,8 @@
 """TopK selection on one GB300 (sm_103a): thin Python binding of libtopk.so.
 
 Argument marshalling only -- every step of the selection runs in the CUDA
-kernels behind the C ABI declared in include/topk.h.  PyTorch supplies device
+kernels behind the C ABI declared in include/topk.h (the key-value cache
+operators' marshalling is compiled: csrc/kv_binding.cpp).  PyTorch supplies device
 memory and the current stream.  There is no CPU fallback: if the library has
 not been built, importing the binding raises.
 
@@ -18,8 +19,8 @@ The first two accept CUDA tensors (asynchronous on the current stream) or CPU te
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -376,106 +377,24 @@ def reduce(x: torch.Tensor, op: str, out: torch.Tensor | None = None, stream=Non
     return out
 
 
-_KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-
-# The C structures as packed bytes: a decoding step makes several of these
-# calls per token and layer, and packing costs a tenth of what filling
-# ctypes structures does.  _KvCache and _KvRows above spell out the fields.
-_kv_pack_cache = struct.Struct("@PPiiiii4xqqqqqqPqiiP").pack
-_kv_pack_rows = struct.Struct("@Pqqi4x").pack
-_kv_pack_strides = struct.Struct("@qq").pack
-
-
-def _kv_refuse(t, name, dtype, device, shape):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
+def _load_kv_binding():
+    """The compiled module that marshals the key-value cache operators' tensors."""
+    path = _build.BINDING_PATH
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+    spec = importlib.util.spec_from_file_location("kv_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (_lib.topk_kv_append, _lib.topk_kv_attend, _lib.topk_kv_evict)))
+    return module
 
 
-def _kv_ints(t, name, device, n):
-    """The address of a contiguous int32 vector of n elements; None stays None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.shape != (n,):
-        _kv_refuse(t, name, torch.int32, device, (n,))
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+_kv = _load_kv_binding()
 
 
-def _kv_strides(t, name, shape):
-    """t's strides but the last, which has to be 1.  A dimension of one
-    element may have any stride in torch: the library gets one that it
-    accepts, which nothing is multiplied by."""
-    strides = t.stride()
-    if strides[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if 1 in shape:
-        return [8 if n == 1 else x for n, x in zip(shape[:-1], strides)]
-    return strides[:-1]
-
-
-def _kv_cache(k_pages, v_pages, table, lens):
-    """(struct topk_kv_cache, device, dtype, sequences, heads, dim)."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _KV_DTYPES:
-        raise TypeError("k_pages must be a float16 or bfloat16 tensor")
-    if not k_pages.is_cuda:
-        raise ValueError("k_pages must be a CUDA tensor")
-    dev, dtype, shape = k_pages.device, k_pages.dtype, k_pages.shape
-    if len(shape) != 4:
-        _kv_refuse(k_pages, "k_pages", dtype, dev, (None,) * 4)
-    if not isinstance(v_pages, torch.Tensor) or v_pages.dtype != dtype or v_pages.device != dev or \
-            v_pages.shape != shape:
-        _kv_refuse(v_pages, "v_pages", dtype, dev, tuple(shape))
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.device != dev or table.dim() != 2:
-        _kv_refuse(table, "table", torch.int32, dev, (None, None))
-    seqs, width = table.shape
-    stride = table.stride()
-    if stride[1] != 1 and width > 1:
-        raise ValueError("the rows of table must be contiguous")
-    cache = _kv_pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _KV_DTYPES[dtype], *shape,
-                           *_kv_strides(k_pages, "k_pages", shape), *_kv_strides(v_pages, "v_pages", shape),
-                           table.data_ptr(), stride[0] if seqs > 1 else width, width, seqs,
-                           _kv_ints(lens, "lens", dev, seqs))
-    return cache, dev, dtype, seqs, shape[2], shape[3]
-
-
-def _kv_rows(t, name, dtype, device, seqs, heads):
-    """struct topk_kv_rows of a tensor [seqs, heads, slots], or None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.dim() != 3 or \
-            t.shape[:2] != (seqs, heads):
-        _kv_refuse(t, name, dtype, device, (seqs, heads, None))
-    a, b, c = t.stride()
-    slots = t.shape[2]
-    if c != 1 and slots > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _kv_pack_rows(t.data_ptr(), a, b, slots)
-
-
-# The current stream's handle by device index; torch.cuda.current_stream
-# builds a Stream object, which takes as long as a launch.
-_kv_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _kv_call(fn, name, device, stream, *args):
-    index = device.index
-    if stream is None and _kv_raw_stream is not None:
-        handle = _kv_raw_stream(index)
-    else:
-        handle = _stream_handle(stream, device)
-    if index == torch.cuda.current_device():
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle)
-    if rc != TOPK_OK:
-        raise TopKError(rc, name)
+def _kv_stream(stream):
+    return None if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -495,24 +414,9 @@ def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                       written at the new slots
 
     lens is not changed: add the tokens' numbers to it afterwards."""
-    cache, dev, dtype, seqs, heads, dim = _kv_cache(k_pages, v_pages, table, lens)
-    if not isinstance(k_new, torch.Tensor) or k_new.dtype != dtype or k_new.device != dev or k_new.dim() != 3 or \
-            k_new.shape[1:] != (heads, dim):
-        _kv_refuse(k_new, "k_new", dtype, dev, (None, heads, dim))
-    shape = k_new.shape
-    if not isinstance(v_new, torch.Tensor) or v_new.dtype != dtype or v_new.device != dev or v_new.shape != shape:
-        _kv_refuse(v_new, "v_new", dtype, dev, tuple(shape))
-    if (pos is None) != (next_pos is None):
-        raise ValueError("pos and next_pos come together")
-    starts = _kv_ints(starts, "starts", dev, seqs + 1)
-    next_pos = _kv_ints(next_pos, "next_pos", dev, seqs)
-    weight = _kv_rows(weight, "weight", torch.float32, dev, seqs, heads)
-    pos = _kv_rows(pos, "pos", torch.int32, dev, seqs, heads)
-    if shape[0] == 0:
-        return
-    _kv_call(_lib.topk_kv_append, "topk_kv_append", dev, stream, cache, k_new.data_ptr(),
-             _kv_pack_strides(*_kv_strides(k_new, "k_new", shape)), v_new.data_ptr(),
-             _kv_pack_strides(*_kv_strides(v_new, "v_new", shape)), shape[0], starts, weight, pos, next_pos)
+    rc = _kv.append(k_pages, v_pages, table, lens, k_new, v_new, starts, weight, pos, next_pos, _kv_stream(stream))
+    if rc != TOPK_OK:
+        raise TopKError(rc, "topk_kv_append")
 
 
 def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -527,30 +431,10 @@ def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, tab
     defaults to dim ** -0.5.  With weight (float32 [seqs, heads, slots]), the
     attention that each slot gets, summed over its query heads, is added to it
     and written to weight_out (default: weight itself)."""
-    cache, dev, dtype, seqs, heads, dim = _kv_cache(k_pages, v_pages, table, lens)
-    if not isinstance(q, torch.Tensor) or q.dtype != dtype or q.device != dev or q.dim() != 3 or \
-            q.shape[0] != seqs or q.shape[2] != dim:
-        _kv_refuse(q, "q", dtype, dev, (seqs, None, dim))
-    shape = q.shape
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    elif not isinstance(out, torch.Tensor) or out.dtype != dtype or out.device != dev or out.shape != shape:
-        _kv_refuse(out, "out", dtype, dev, tuple(shape))
-    if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    elif not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or \
-            lse.shape != shape[:2]:
-        _kv_refuse(lse, "lse", torch.float32, dev, tuple(shape[:2]))
-    if not out.is_contiguous() or not lse.is_contiguous():
-        raise ValueError("out and lse must be contiguous")
-    if weight is None and weight_out is not None:
-        raise ValueError("weight_out needs weight")
-    weight = _kv_rows(weight, "weight", torch.float32, dev, seqs, heads)
-    weight_out = weight if weight_out is None else _kv_rows(weight_out, "weight_out", torch.float32, dev, seqs, heads)
-    _kv_call(_lib.topk_kv_attend, "topk_kv_attend", dev, stream, cache, q.data_ptr(),
-             _kv_pack_strides(*_kv_strides(q, "q", shape)), shape[1], dim ** -0.5 if scale is None else float(scale),
-             out.data_ptr(), lse.data_ptr(), weight, weight_out)
-    return out, lse
+    got = _kv.attend(q, k_pages, v_pages, table, lens, scale, weight, weight_out, out, lse, _kv_stream(stream))
+    if type(got) is int:
+        raise TopKError(got, "topk_kv_attend")
+    return got
 
 
 def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -563,16 +447,13 @@ def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, 
     pos_out, lens_out), by default weight, pos and lens themselves, changed in
     place -- topk_kv_evict in include/topk.h.  Pages past the first
     ceil(budget / page_size) of a sequence can be reused afterwards."""
-    cache, dev, _, seqs, heads, _ = _kv_cache(k_pages, v_pages, table, lens)
     weight_out = weight if weight_out is None else weight_out
     pos_out = pos if pos_out is None else pos_out
     lens_out = lens if lens_out is None else lens_out
-    _kv_call(_lib.topk_kv_evict, "topk_kv_evict", dev, stream, cache,
-             _kv_rows(weight, "weight", torch.float32, dev, seqs, heads),
-             _kv_rows(pos, "pos", torch.int32, dev, seqs, heads), _kv_ints(next_pos, "next_pos", dev, seqs),
-             int(budget), int(sink), int(recent),
-             _kv_rows(weight_out, "weight_out", torch.float32, dev, seqs, heads),
-             _kv_rows(pos_out, "pos_out", torch.int32, dev, seqs, heads), _kv_ints(lens_out, "lens_out", dev, seqs))
+    rc = _kv.evict(k_pages, v_pages, table, lens, weight, pos, next_pos, budget, sink, recent, weight_out, pos_out,
+                   lens_out, _kv_stream(stream))
+    if rc != TOPK_OK:
+        raise TopKError(rc, "topk_kv_evict")
     return weight_out, pos_out, lens_out
 
 

@@ -2,21 +2,27 @@
 
 Each .cu file compiles in parallel to an object file under ``_lib/``; the
 objects link into ``_lib/libtopk.so`` (CUDA runtime linked statically).
-Nothing is rebuilt when the library is newer than every source.
+Beside it, g++ compiles the Python binding of the key-value cache operators
+(csrc/kv_binding.cpp) against the installed torch into ``_lib/kv_binding.so``.
+Nothing is rebuilt when both are newer than every source.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtopk.so")
+BINDING_SRC = os.path.join(CSRC, "kv_binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "kv_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
@@ -34,15 +40,27 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _binding_command(out: str):
+    """g++ on the binding, against the torch and Python that are running."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", out, BINDING_SRC,
+            *(f"-I{p}" for p in include), f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch",
+            "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -59,6 +77,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    binding = BINDING_PATH + f".tmp{os.getpid()}"
+    procs.append((BINDING_SRC, subprocess.Popen(_binding_command(binding), stdout=subprocess.PIPE,
+                                                stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -67,10 +88,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(os.path.basename(f) for f in failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(os.path.basename(f) for f in failed))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], check=True)
     os.replace(tmp, LIB_PATH)
+    os.replace(binding, BINDING_PATH)
     return LIB_PATH
 
 
