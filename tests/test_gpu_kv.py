@@ -452,3 +452,11 @@ def test_operators_together(tk):
                                             budget, sink, recent)
                     mirror[b][h] = [row[i] for i in src]
             assert lens.tolist() == [len(mirror[b][0]) for b in range(seqs)]
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 8, 16])
+def test_attend_many_rows_of_a_block(tk, dim, group):
+    """More tiles than there are SMs, in short rows of unequal lengths: a block goes through several rows."""
+    lens = [(i * 61) % 700 + (i % 5 == 0) for i in range(60)]
+    check_attend(tk, lens, 4, group, dim, 16, torch.bfloat16, "head", seed=21)

@@ -183,22 +183,28 @@ __device__ __forceinline__ Walk find_range(const AttendArgs& p, int* sh) {
 
 template <int DP, int GP>
 struct Shape {
-    static constexpr int kSub = DP / 64;                  // 128-byte columns of a row
-    static constexpr int kItem = kTile * DP * 2;          // bytes of a tile's keys or values
-    static constexpr int kRing = kRingBytes / kItem;
-    static constexpr int kQBytes = kSub * 16 * 128;       // 16 rows of a query block
+    // A tile's keys, and its values, are copied in parts of at most 128
+    // elements of dim.  Keys and values have rings of their own: each is
+    // filled by one warp and emptied by one thread, in order, which is what
+    // the parity of a barrier's phase can tell apart.
+    static constexpr int kParts = DP > 128 ? DP / 128 : 1;
+    static constexpr int kSub = DP / kParts / 64;         // 128-byte columns of a part's row
+    static constexpr int kItem = kTile * kSub * 128;      // bytes of a part
+    static constexpr int kRing = kRingBytes / 2 / kItem;
+    static constexpr int kQBytes = DP / 64 * 16 * 128;    // 16 rows of a query block
     static constexpr int kPCols = GP <= 8 ? 16 : 2 * GP;  // hi of every head, then lo; the rest is not looked at
     static constexpr int kPRow = kPCols * 2;              // bytes of a slot's row of P
     static constexpr int kPBytes = kPRow * kTile;
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
-    static constexpr int kOBlocks = DP / kM;
+    static constexpr int kOBlocks = kParts;
     // Tensor memory columns: two S buffers of 16, then O of each softmax
     // group for this row, and of both for the row before.
     static constexpr int kTmemS = 0, kTmemO = 32, kOCols = kOBlocks * kPCols;
     static constexpr int kTmemCols = 32 + 4 * kOCols <= 128 ? 128 : 256;
     static constexpr size_t kSmem = 1024 + kRingBytes + 2 * kQBytes + 2 * kPBytes;
     // Barriers, by their place in bars[].
-    static constexpr int kFull = 0, kEmpty = kRing, kSFull = 2 * kRing, kSFree = kSFull + 2, kPReady = kSFull + 4,
+    static constexpr int kFullK = 0, kFullV = kRing, kEmptyK = 2 * kRing, kEmptyV = 3 * kRing, kSFull = 4 * kRing,
+                         kSFree = kSFull + 2, kPReady = kSFull + 4,
                          kPFree = kSFull + 6, kQFull = kSFull + 8, kQFree = kSFull + 10, kDrain = kSFull + 12,
                          kTold = kSFull + 14, kBars = kSFull + 18;
 };
@@ -216,7 +222,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     return false;
 }
 
-// A place in the ring, moved on by n <= kRing items.
+// A place in a ring, moved on by n <= RING items.
 template <int RING>
 struct Place {
     int at;
@@ -500,12 +506,13 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
     };
 
     if (warp == kCopyK || warp == kCopyV) {
-        // Copies into the ring, in the order in which the products use them:
-        // K(0), K(1), V(0), K(2), V(1), ..., V(count - 1).  One warp has the
-        // keys, one the values: a copy takes its issuer some 50 clocks, and a
-        // tile of small pages is many copies.
+        // Copies into the rings.  One warp has the keys, one the values: a
+        // copy takes its issuer some 50 clocks, and a tile of small pages is
+        // many copies.
         const bool keys = warp == kCopyK;
         const CUtensorMap* map = keys ? &map_k : &map_v;
+        const int full0 = keys ? S::kFullK : S::kFullV, empty0 = keys ? S::kEmptyK : S::kEmptyV;
+        const uint32_t my_ring = keys ? ring : ring + kRingBytes / 2;
         const uint64_t policy = l2_evict_first_policy();
         // Lane i holds the page of the tile's i-th box, fetched a tile ahead
         // of its use: the load takes as long as a third of a tile's copy.  A
@@ -531,7 +538,6 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         };
         auto wait_warp = [&](int bar, uint32_t parity) { return __all_sync(kFullMask, wait(bar, parity)); };
         Place<S::kRing> put = {0, 0};
-        if (!keys) put.move(count == 1 ? 1 : 2);
         int items = 0, q_loads = 0;
         Walk x = w, y = w;  // the tile to copy, and the one after it
         bool enters = true;
@@ -548,42 +554,46 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 if (q_loads >= 2 && !wait_warp(S::kQFree + buf, ((q_loads - 2) >> 1) & 1)) break;
                 if (lane == 0) {
                     const uint32_t full = bar0 + (S::kQFull + buf) * 8;
-                    mbar_expect_at(full, S::kSub * GP * 128);
-                    for (int sub = 0; sub < S::kSub; ++sub)
+                    mbar_expect_at(full, DP / 64 * GP * 128);
+                    for (int sub = 0; sub < DP / 64; ++sub)
                         tma_load_3d(q_buf + buf * S::kQBytes + sub * 16 * 128, &map_q, sub * 64,
                                     x.h * p.group + x.part * GP, x.b, full);
                 }
                 ++q_loads;
                 __syncwarp();
             }
-            // The place was used before when its item number is kRing or more.
-            const int item = keys ? (it == 0 ? 0 : 2 * it - 1) : (it + 1 < count ? 2 * it + 2 : 2 * it + 1);
-            if (item >= S::kRing && !wait_warp(S::kEmpty + put.at, put.phase ^ 1)) break;
-            const uint32_t full = bar0 + (S::kFull + put.at) * 8, dst = ring + put.at * S::kItem;
             const int left = x.n - x.t * kTile, boxes = left >= kTile ? kTile / p.box : (left + p.box - 1) / p.box;
-            if (lane == 0) mbar_expect_at(full, boxes * S::kSub * p.box * 128);
             if ((unsigned)page >= (unsigned)p.c.pages) page = p.c.pages;  // outside the pool: reads as zeros
-#pragma unroll 1
-            for (int i0 = 0; i0 < boxes; i0 += 4) {
-                int pg[4], at[4];
+            bool ok = true;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pg[i] = __shfl_sync(kFullMask, page, i0 + i);
-                    at[i] = __shfl_sync(kFullMask, in_now, i0 + i);
-                }
-                if (lane == 0)
+            for (int part = 0; part < S::kParts; ++part) {
+                ok = ok && (items < S::kRing || wait_warp(empty0 + put.at, put.phase ^ 1));
+                if (!ok) break;
+                const uint32_t full = bar0 + (full0 + put.at) * 8, dst = my_ring + put.at * S::kItem;
+                if (lane == 0) mbar_expect_at(full, boxes * S::kSub * p.box * 128);
+#pragma unroll 1
+                for (int i0 = 0; i0 < boxes; i0 += 4) {
+                    int pg[4], at[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (i0 + i >= boxes) break;
-#pragma unroll
-                        for (int sub = 0; sub < S::kSub; ++sub)
-                            tma_load_4d(dst + sub * (kTile * 128) + (i0 + i) * p.box * 128, map, sub * 64, at[i], x.h,
-                                        pg[i], full, policy);
+                        pg[i] = __shfl_sync(kFullMask, page, i0 + i);
+                        at[i] = __shfl_sync(kFullMask, in_now, i0 + i);
                     }
-                __syncwarp();
+                    if (lane == 0)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (i0 + i >= boxes) break;
+#pragma unroll
+                            for (int sub = 0; sub < S::kSub; ++sub)
+                                tma_load_4d(dst + sub * (kTile * 128) + (i0 + i) * p.box * 128, map,
+                                            (part * S::kSub + sub) * 64, at[i], x.h, pg[i], full, policy);
+                        }
+                    __syncwarp();
+                }
+                ++items;
+                put.move(1);
             }
-            ++items;
-            put.move(keys ? (it == 0 ? 1 : 2) : (it + 2 == count ? 1 : 2));
+            if (!ok) break;
             x = y;
             enters = y.t == 0;
             page = page_next;
@@ -592,10 +602,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         __syncwarp();
         if (gave_up) {  // wait for this warp's copies in flight, so that none lands after the block's end
 #pragma unroll 1
-            for (int it = max(0, items - S::kRing); it < items; ++it) {
-                const int item = keys ? (it == 0 ? 0 : 2 * it - 1) : (it + 1 < count ? 2 * it + 2 : 2 * it + 1);
-                mbar_wait(&bars[S::kFull + item % S::kRing], (item / S::kRing) & 1);
-            }
+            for (int i = max(0, items - S::kRing); i < items; ++i)
+                mbar_wait(&bars[full0 + i % S::kRing], (i / S::kRing) & 1);
 #pragma unroll 1
             for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
         }
@@ -615,18 +623,24 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
 #pragma unroll 1
                 for (int k = 0; k < n; ++k, ++it) {
                     const int buf = it & 1;
-                    ok = wait(S::kFull + get.at, get.phase) &&
-                         (it < 2 || wait(S::kSFree + buf, ((it >> 1) & 1) ^ 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t a = k_lo + get.at * (S::kItem >> 4), b = q_lo + qb * (S::kQBytes >> 4);
+                    ok = it < 2 || wait(S::kSFree + buf, ((it >> 1) & 1) ^ 1);
 #pragma unroll
-                    for (int j = 0; j < DP / 16; ++j)
-                        mma_f16(tmem + S::kTmemS + buf * 16, a + (((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4), hi,
-                                b + (((j >> 2) * (16 * 128) + (j & 3) * 32) >> 4), hi, id, j > 0);
+                    for (int part = 0; part < S::kParts; ++part) {
+                        ok = ok && wait(S::kFullK + get.at, get.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = k_lo + get.at * (S::kItem >> 4);
+                        const uint32_t b = q_lo + ((qb * S::kQBytes + part * S::kSub * 16 * 128) >> 4);
+#pragma unroll
+                        for (int j = 0; j < S::kSub * 4; ++j)
+                            mma_f16(tmem + S::kTmemS + buf * 16,
+                                    a + (((j >> 2) * (kTile * 128) + (j & 3) * 32) >> 4), hi,
+                                    b + (((j >> 2) * (16 * 128) + (j & 3) * 32) >> 4), hi, id, part > 0 || j > 0);
+                        mma_commit(bar0 + (S::kEmptyK + get.at) * 8);
+                        get.move(1);
+                    }
+                    if (!ok) break;
                     mma_commit(bar0 + (S::kSFull + buf) * 8);
-                    mma_commit(bar0 + (S::kEmpty + get.at) * 8);
-                    get.move(it == 0 ? 1 : 2);  // K(t) is item 2t - 1, but K(0) is the first
                 }
                 mma_commit(bar0 + (S::kQFree + qb) * 8);
                 x.t += n - 1;
@@ -642,10 +656,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         if (lane == 0) {  // O += V^T P^T
             const uint32_t id = mma_idesc(p.c.bf16, S::kM, S::kPCols, true);
             constexpr uint32_t hi_v = smem_desc_hi(1024, 128), hi_p = smem_desc_hi(S::kPRow * 8, S::kPRow);
-            const uint32_t v_lo = smem_desc_lo(ring, kTile * 128), p_lo = smem_desc_lo(p_buf, 16);
-            // V(t) is item 2t + 2, but the last one follows V(t - 1).
+            const uint32_t v_lo = smem_desc_lo(ring + kRingBytes / 2, kTile * 128), p_lo = smem_desc_lo(p_buf, 16);
             Place<S::kRing> get = {0, 0};
-            get.move(count == 1 ? 1 : 2);
             Walk x = w;
             bool ok = true;
 #pragma unroll 1
@@ -656,21 +668,24 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 for (int k = 0; k < n; ++k, ++it) {
                     const int buf = it & 1, steps = k + 1 < n ? 8 : (last + 15) >> 4;
                     const uint32_t o = tmem + S::kTmemO + ((piece & 1) * 2 + buf) * S::kOCols;
-                    ok = wait(S::kFull + get.at, get.phase) && wait(S::kPReady + buf, (it >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t a = v_lo + get.at * (S::kItem >> 4), b = p_lo + buf * (S::kPBytes >> 4);
+                    ok = wait(S::kPReady + buf, (it >> 1) & 1);
 #pragma unroll
-                    for (int j = 0; j < kTile / 16; ++j) {
-                        if (j >= steps) break;
+                    for (int part = 0; part < S::kParts; ++part) {
+                        ok = ok && wait(S::kFullV + get.at, get.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = v_lo + get.at * (S::kItem >> 4), b = p_lo + buf * (S::kPBytes >> 4);
 #pragma unroll
-                        for (int m = 0; m < S::kOBlocks; ++m)
-                            mma_f16(o + m * S::kPCols, a + ((m * 2 * (kTile * 128) + j * 2048) >> 4),
-                                    hi_v, b + j * (S::kPRow * 16 >> 4), hi_p, id, k > 1 || j > 0);
+                        for (int j = 0; j < kTile / 16; ++j) {
+                            if (j >= steps) break;
+                            mma_f16(o + part * S::kPCols, a + (j * 2048 >> 4), hi_v, b + j * (S::kPRow * 16 >> 4), hi_p,
+                                    id, k > 1 || j > 0);
+                        }
+                        mma_commit(bar0 + (S::kEmptyV + get.at) * 8);
+                        get.move(1);
                     }
+                    if (!ok) break;
                     mma_commit(bar0 + (S::kPFree + buf) * 8);
-                    mma_commit(bar0 + (S::kEmpty + get.at) * 8);
-                    get.move(it + 2 == count ? 1 : 2);
                 }
                 x.t += n - 1;
                 x.next(p);
@@ -808,16 +823,23 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 }
                 if (valid & 15) {
                     // Rows past the sequence's end inside the last step of 16: zero times NaN is NaN.
-                    const int item = it + 1 < count ? 2 * it + 2 : 2 * count - 1, st = item % S::kRing;
-                    ok = ok && wait(S::kFull + st, (item / S::kRing) & 1);
                     const int pad = (16 - (valid & 15)) * S::kSub * 8;
+                    // The place's use before this one has to be over, or its phase could be taken for
+                    // this one's.  It is a use three places back, so at most the tile before the last
+                    // (whose product was waited for above) unless a tile takes two places.
+                    if (S::kParts > 1 && it > 0) ok = ok && wait(S::kPFree + (group ^ 1), ((it - 1) >> 1) & 1);
+#pragma unroll
+                    for (int part = 0; part < S::kParts; ++part) {
+                        const int item = it * S::kParts + part, st = item % S::kRing;
+                        ok = ok && wait(S::kFullV + st, (item / S::kRing) & 1);
 #pragma unroll 1
-                    for (int i = me; ok && i < pad; i += kSoftmax)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         ring + st * S::kItem + i / 8 % S::kSub * (kTile * 128) +
-                                         (valid + i / (S::kSub * 8)) * 128 + (i & 7) * 16),
-                                     "r"(0)
-                                     : "memory");
+                        for (int i = me; ok && i < pad; i += kSoftmax)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             ring + kRingBytes / 2 + st * S::kItem + i / 8 % S::kSub * (kTile * 128) +
+                                             (valid + i / (S::kSub * 8)) * 128 + (i & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive_at(bar0 + (S::kPReady + group) * 8);

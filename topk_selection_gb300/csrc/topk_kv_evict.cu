@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     __shared__ int coarse[2][kWarps];              // the same by kPer * 32 bins, the highest first
     __shared__ int far_coarse[kMostBlocks][32], far_bins[kMostBlocks][kPer][32];  // the cluster's
     __shared__ int scan[kWarps];
-    __shared__ int found[2];                       // the bin, and how many of its keys are kept
+    __shared__ int found[3];                       // the bin, how many of its keys are kept, and how many it has
     __shared__ int4 tally;                         // this block: above and at the edge; the same below the budget
     __shared__ int warp_above[kWarps], warp_ties[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -164,18 +164,18 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     }
     unsigned prefix = 0;
     int need = budget;
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        constexpr int kShift[3] = {21, 10, 0}, kWidth[3] = {kBins, kBins, kBins / 2};
+        const int up = pass == 0 ? 32 : pass == 1 ? 21 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const unsigned mask = (1u << (up - shift)) - 1;
         if (pass > 0) {
-            const int up = kShift[pass - 1];
             for (int base = lo; base < end; base += 4 * THREADS) {
                 unsigned key[4];
                 keys_at(base + 4 * tid, end, key);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (((key[j] ^ prefix) >> up) == 0)
-                        atomicAdd(&hist[pass & 1][(key[j] >> kShift[pass]) & (kWidth[pass] - 1)], 1);
+                        atomicAdd(&hist[pass & 1][(key[j] >> shift) & mask], 1);
             }
         }
         __syncthreads();
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
                     if (before < need && need <= before + own[j]) {
                         found[0] = kBins - 1 - (t * kPer + j);
                         found[1] = need - before;
+                        found[2] = own[j];
                     }
                     before += own[j];
                 }
@@ -257,8 +258,13 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
         if (pass == 1)
             for (int i = tid; i < kBins; i += THREADS) hist[0][i] = 0;
         __syncthreads();
-        prefix |= (unsigned)found[0] << kShift[pass];
+        prefix |= (unsigned)found[0] << shift;
         need = found[1];
+        if (need == found[2]) {  // all of the bin: no need to look into it
+            prefix -= 1;  // above any absent key's 0, and keys equal to it are not kept
+            need = 0;
+            break;
+        }
     }
     const unsigned edge = prefix;  // keys above it are kept, and the first `need` that equal it
 
