@@ -824,9 +824,9 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 if (valid & 15) {
                     // Rows past the sequence's end inside the last step of 16: zero times NaN is NaN.
                     const int pad = (16 - (valid & 15)) * S::kSub * 8;
-                    // The place's use before this one has to be over, or its phase could be taken for
-                    // this one's.  It is a use three places back, so at most the tile before the last
-                    // (whose product was waited for above) unless a tile takes two places.
+                    // The use of the place before this one has to be over, or its phase could be taken for
+                    // this one's.  It was three places back: the tile it - 3, whose product came before
+                    // the one waited for above, or with two places to a tile perhaps the last one's.
                     if (S::kParts > 1 && it > 0) ok = ok && wait(S::kPFree + (group ^ 1), ((it - 1) >> 1) & 1);
 #pragma unroll
                     for (int part = 0; part < S::kParts; ++part) {
@@ -972,7 +972,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
 
 // Adds the heads' shares to the weights: p * 2^(tile's reference - row's) /
 // sum.  Block c takes the tiles that block c of the first launch had, so its
-// p may still be in L2; a warp takes a tile, all its loads in flight at once.
+// p may still be in L2; a warp takes every kWarps-th of them, and all of a
+// tile's loads are in flight at once.
 template <int GP>
 __global__ void __launch_bounds__(kWeightThreads) kv_weight_kernel(const __grid_constant__ AttendArgs p) {
     constexpr int kWarps = kWeightThreads / 32;
@@ -981,57 +982,51 @@ __global__ void __launch_bounds__(kWeightThreads) kv_weight_kernel(const __grid_
     grid_dependency_wait();
     Walk w;
     w.load(p.walk + blockIdx.x * Walk::kWords);
+    int ahead = warp;  // tiles still to go to this warp's next
 #pragma unroll 1
-    for (int tile = w.s; tile < w.e;) {
-        const int count = min(w.tiles - w.t, w.e - tile);  // this block's tiles of the row
+    for (int tile = w.s; tile + ahead < w.e;) {
+        const int left = w.tiles - w.t;
+        if (ahead >= left) {  // on to the next row
+            ahead -= left;
+            tile += left;
+            w.t = w.tiles - 1;
+            w.next(p);
+            continue;
+        }
+        w.t += ahead;
+        tile += ahead;
+        ahead = kWarps;
         // Of a group in several parts, the block that has the first adds up all.
 #pragma unroll 1
         for (int pt = 0; w.part == 0 && pt < p.parts; ++pt) {
             const int heads = min(GP, p.group - pt * GP);
             const float* wi = pt == 0 ? p.a.weight.row(w.b, w.h) : p.a.weight_out.row(w.b, w.h);
             float* wo = p.a.weight_out.row(w.b, w.h);
+            const size_t x = tile + (size_t)pt * w.tiles;
+            const int slot0 = w.t * kTile + lane;
             float2 ml = make_float2(0.f, 0.f);
-            if (lane < heads) ml = p.row_ml[((size_t)w.row(p) + pt) * GP + lane];
-#pragma unroll 1
-            for (int k = warp; k < count; k += kWarps) {
-                const size_t x = tile + k + (size_t)pt * w.tiles;
-                const int slot0 = (w.t + k) * kTile + lane;
-                float y[4][GP], sum[4];
-                const float tm = lane < heads ? p.tile_m[x * GP + lane] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float* v = p.p + (x * kTile + i * 32 + lane) * GP;
-                    if constexpr (GP % 4 == 0) {
-#pragma unroll
-                        for (int g = 0; g < GP; g += 4) {
-                            const float4 q = *reinterpret_cast<const float4*>(v + g);
-                            y[i][g] = q.x;
-                            y[i][g + 1] = q.y;
-                            y[i][g + 2] = q.z;
-                            y[i][g + 3] = q.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < GP; ++g) y[i][g] = v[g];
-                    }
-                    sum[i] = slot0 + i * 32 < w.n ? wi[slot0 + i * 32] : 0.f;
-                }
-                const float f = ml.y == 0.f || tm == -INFINITY ? 0.f : exp2f(tm - ml.x) / ml.y;
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    const float fg = __shfl_sync(kFullMask, f, g);
-                    if (g >= heads) break;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[i] = fmaf(y[i][g], fg, sum[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (slot0 + i * 32 < w.n) wo[slot0 + i * 32] = sum[i];
+            float tm = 0.f, y[4][GP], sum[4];
+            if (lane < heads) {
+                ml = p.row_ml[((size_t)w.row(p) + pt) * GP + lane];
+                tm = p.tile_m[x * GP + lane];
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                load_row<GP>(p.p + (x * kTile + i * 32 + lane) * GP, y[i]);
+                sum[i] = slot0 + i * 32 < w.n ? wi[slot0 + i * 32] : 0.f;
+            }
+            const float f = ml.y == 0.f || tm == -INFINITY ? 0.f : exp2f(tm - ml.x) / ml.y;
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float fg = __shfl_sync(kFullMask, f, g);
+                if (g >= heads) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = fmaf(y[i][g], fg, sum[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (slot0 + i * 32 < w.n) wo[slot0 + i * 32] = sum[i];
         }
-        tile += count;
-        w.t += count - 1;
-        w.next(p);
     }
 }
 
