@@ -460,3 +460,92 @@ def test_attend_many_rows_of_a_block(tk, dim, group):
     """More tiles than there are SMs, in short rows of unequal lengths: a block goes through several rows."""
     lens = [(i * 61) % 700 + (i % 5 == 0) for i in range(60)]
     check_attend(tk, lens, 4, group, dim, 16, torch.bfloat16, "head", seed=21)
+
+
+def test_allocation_failure_is_a_status(tk):
+    """Scratch that cannot be had: nothing is written, and the same call works afterwards."""
+    cache = _kv.Cache([200], 2, 64, 16, torch.float16, "head", seed=23)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(1, 4, 64, device="cuda").half()
+    out = torch.full((1, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    tk.set_option(tk.OPT_FAULT_ALLOC, 1)
+    try:
+        with torch.cuda.stream(s), pytest.raises(tk.TopKError) as err:
+            tk.kv_attend(q, k, v, table, lens, out=out)
+        assert err.value.status == 3  # TOPK_ERR_NO_MEMORY
+    finally:
+        tk.set_option(tk.OPT_FAULT_ALLOC, 0)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0)
+    with torch.cuda.stream(s):
+        tk.kv_attend(q, k, v, table, lens, out=out)
+    s.synchronize()
+    eo, _, _, to, _, _ = _kv.attend(cache, q.cpu(), 0.125)
+    _kv.close(out, eo, to)
+
+
+def test_a_selection_after_them_waits(tk):
+    """A TopK behind a cache operator on the stream must not start before it ends: it may read what that wrote."""
+    lens = [1500]
+    cache = _kv.Cache(lens, 1, 64, 16, torch.float16, "head", seed=24)
+    k, v, table, lens_d = cache.dev()
+    q = torch.randn(1, 1, 64, device="cuda").half()
+    weight = torch.zeros(1, 1, cache.capacity, device="cuda")
+    for _ in range(20):
+        tk.topk_f32(weight.reshape(-1)[:1500], 8)
+        tk.kv_attend(q, k, v, table, lens_d, weight=weight)
+        best = tk.topk_f32(weight.reshape(-1)[:1500], 8)
+        assert not tk.last_launch_early()
+        assert torch.equal(best.cpu(), torch.sort(weight.cpu().reshape(-1)[:1500], descending=True).values[:8])
+
+
+def test_captured_in_a_graph(tk):
+    """The calls only enqueue, once a first one on the stream has made their scratch."""
+    cache = _kv.Cache([700, 300], 2, 64, 16, torch.bfloat16, "token", room=8, seed=25)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(2, 8, 64, device="cuda").to(torch.bfloat16)
+    new = torch.randn(2, 2, 64, device="cuda").to(torch.bfloat16)
+    weight = torch.zeros(2, 2, cache.capacity, device="cuda")
+    pos = torch.arange(cache.capacity, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    w_out, p_out, l_out = torch.zeros_like(weight), torch.zeros_like(pos), torch.zeros_like(lens)
+
+    def step():
+        tk.kv_append(k, v, table, lens, new, new, weight=weight)
+        out, _ = tk.kv_attend(q, k, v, table, lens, weight=weight, weight_out=w_out)
+        tk.kv_evict(k, v, table, lens, w_out, pos, lens, 256, weight_out=weight, pos_out=p_out, lens_out=l_out)
+        return out
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    k0, v0, w0 = k.clone(), v.clone(), weight.clone()
+    with torch.cuda.stream(s):
+        want = step().clone()
+        kept = k.clone()
+        for t, t0 in ((k, k0), (v, v0), (weight, w0)):
+            t.copy_(t0)
+        graph = torch.cuda.CUDAGraph()
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            out = step()
+        for _ in range(3):
+            for t, t0 in ((k, k0), (v, v0), (weight, w0)):
+                t.copy_(t0)
+            graph.replay()
+    s.synchronize()
+    assert torch.equal(bits(out), bits(want)) and torch.equal(bits(k), bits(kept))
+    assert l_out.tolist() == [256, 256]
+
+
+def test_example_runs():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "kv_decode.py"), "--seqs", "3", "--prompt", "150",
+                        "--steps", "120", "--limit", "200", "--budget", "96", "--recent", "16", "--dim", "64"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert "of 273 tokens held" in r.stdout

@@ -109,6 +109,7 @@ def test_attend_errors(tk):
     near = ctypes.byref(tk._KvRows(addr(8) + 64, 160, 80, 80))
     assert attend(tk, weight=rows(tk, 8), weight_out=near) == 1    # overlapping, and not the same
     assert attend(tk, c=cache(tk, seqs=60000), q_heads=400) == 2
+    assert attend(tk, c=cache(tk, seqs=1000, table_width=1 << 20, table_stride=1 << 20), q_heads=64) == 2  # tiles
 
 
 def test_evict_errors(tk):

@@ -146,6 +146,8 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
         if ((rc = check_rows(weight_out, c, c.capacity())) != TOPK_OK) return rc;
         if (!same_or_apart(weight, weight_out, c)) return TOPK_ERR_INVALID_ARG;
     }
+    // Tiles of 128 slots are numbered in 32 bits.
+    if ((int64_t)c.seqs * q_heads * ((c.capacity() + 127) / 128) > INT32_MAX) return TOPK_ERR_UNSUPPORTED;
     if ((int64_t)c.seqs * q_heads > (1 << 24)) return TOPK_ERR_UNSUPPORTED;
     rc = on_device({c.k, c.v, c.table, c.lens, q, out, lse, present(weight) ? weight->data : nullptr,
                     present(weight_out) ? weight_out->data : nullptr});

@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kMostBlocks = 8;  // of a cluster
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 64;
 
 struct EvictArgs {
     KvCache c;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
 // A warp takes 32 moves: a lane looks up one move's pages, then all lanes
 // copy the 32 moves' vectors, kUnroll of them in flight per lane.
 __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
-    constexpr int kUnroll = 8;
+    constexpr int kUnroll = 4;
     __shared__ int4 where[kMoveThreads / 32][32];  // source page and slot in it, target page and slot
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, b = row / a.c.heads, h = row % a.c.heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -460,7 +460,7 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     a.movers = a.holes + (size_t)rows * a.room;
     // Blocks per row: as many as keep the SMs busy twice over, and leave each
     // block 1024 slots at least.  (Clusters of 16 were slower: 8 rows of
-    // 131072 slots 49 us instead of 43, since not all eight run at once.)
+    // 131072 slots 53 us instead of 43, since not all eight run at once.)
     constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
     int blocks = 1;
     while (blocks < 8 && rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024) blocks *= 2;
