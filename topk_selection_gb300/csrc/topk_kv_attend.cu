@@ -334,6 +334,24 @@ __device__ __forceinline__ void join_shares(const AttendArgs& p, int c0, int fir
         ml[i] = make_float2(0.f, 0.f);
         if (lane < n && g < heads) ml[i] = __ldcg(&p.part_ml[(2 * c + (c == c0)) * GP + g]);
     }
+    // Two quads of elements of kFly shares at a time, the first of them under
+    // way while the factors are worked out.
+    const int quads = heads * p.c.dim / 4;
+    const int share = GP * p.c.dim / 4 * 2 * stride;      // from one share to the next
+    const int own = first == c0 ? GP * p.c.dim / 4 : 0;  // the row's first block has a place of its own
+    const float4* shares = reinterpret_cast<const float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim);
+    float4 y[2][kFly];
+    auto fetch = [&](int i0, int j0) {
+#pragma unroll
+        for (int j = 0; j < kFly; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                y[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < n && i0 + q * kSoftmax < quads)
+                    y[q][j] = __ldcg(shares + (j0 + j == 0 ? own : (j0 + j) * share) + i0 + q * kSoftmax);
+            }
+    };
+    fetch(me, 0);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int g = quarter + 4 * i;
@@ -348,28 +366,15 @@ __device__ __forceinline__ void join_shares(const AttendArgs& p, int c0, int fir
         }
     }
     bar_sync(bar, kSoftmax);
-    const int quads = heads * p.c.dim / 4;
-    const int share = GP * p.c.dim / 4 * 2 * stride;  // from one share to the next
-    // Two quads of elements of eight shares at a time.
 #pragma unroll 1
     for (int i0 = me; i0 < quads; i0 += 2 * kSoftmax) {
         float4 o[2] = {};
         int g[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) g[q] = min(4 * (i0 + q * kSoftmax) / p.c.dim, GP - 1);
-        const float4* from = reinterpret_cast<const float4*>(p.part_o + (size_t)2 * first * GP * p.c.dim) + i0;
-        const int own = first == c0 ? GP * p.c.dim / 4 : 0;  // the row's first block has a place of its own
 #pragma unroll 1
         for (int j0 = 0; j0 < n; j0 += kFly) {
-            float4 y[2][kFly];
-#pragma unroll
-            for (int j = 0; j < kFly; ++j)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    y[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j0 + j < n && i0 + q * kSoftmax < quads)
-                        y[q][j] = __ldcg(from + (j0 + j == 0 ? own : (j0 + j) * share) + q * kSoftmax);
-                }
+            if (i0 != me || j0 > 0) fetch(i0, j0);
 #pragma unroll
             for (int j = 0; j < kFly; ++j)
 #pragma unroll
