@@ -13,6 +13,7 @@
 
 #include "../../include/topk.h"
 #include "topk_internal.h"
+#include "topk_kv.cuh"
 
 static_assert(TOPK_MAX_K == topk::kBigKMax, "the header states the big-k form's limit");
 

@@ -214,17 +214,6 @@ cudaError_t sort_launch(cudaStream_t s, const uint32_t* keys, const uint32_t* va
 void note_cuda_error(int err);
 void note_launch();
 
-// The same for entry points that enqueue several, and their scratch: `bytes`
-// bytes of the stream's workspace (no contents to rely on) and its status
-// word; the call after them does not start early.  Returns a topk_status.
-void note_launches(int n);
-int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status);
-// `bytes` bytes that are zero before the first call on the stream, and a number
-// that counts the calls.
-int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch);
-// TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
-int device_pointer(const void* p);
-
 // Device address of topk_i32_noalloc's scratch on `device`, or null if that
 // entry point has not run there yet.
 void* noalloc_scratch_if_ready(int device);

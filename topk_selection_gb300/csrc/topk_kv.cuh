@@ -43,6 +43,18 @@ struct KvRows {
     __device__ T* row(int b, int h) const { return data + b * seq + h * head; }
 };
 
+// Of the C ABI layer (topk_api.cu): `bytes` bytes of the stream's scratch (no
+// contents to rely on) and its status word, with the record that the call
+// after this one must not start early.  Returns a topk_status.
+int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status);
+// `bytes` bytes that are zero before the first call on the stream, and a
+// number that counts the calls.
+int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch);
+// TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
+int device_pointer(const void* p);
+// Counts n kernel launches.
+void note_launches(int n);
+
 cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k_new, const long long* k_stride,
                              const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
                              KvRows<float> weight, KvRows<int> pos, const int* next_pos);
