@@ -25,7 +25,7 @@ struct AppendArgs {
     KvRows<int> pos;
     const int* next_pos;
     int per;    // items of a warp
-    int shift;  // log2 of the places that an item's vectors take
+    int shift;  // log2 of the lanes that a key takes
 };
 
 // The last sequence whose tokens start at or before t: 32 candidates a round.
@@ -42,7 +42,7 @@ __device__ __forceinline__ int find_seq(const int* starts, int seqs, int t, int 
 }
 
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-    constexpr int kUnroll = 8;
+    constexpr int kUnroll = 4;  // of keys and of values each
     __shared__ int4 where[kAppendThreads / 32][32];  // token, head, page (-1: nowhere) and slot in it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long items = (long long)a.tokens * a.c.heads;
@@ -52,21 +52,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const int t = (int)((first + lane) / a.c.heads), h = (int)(first + lane - (long long)t * a.c.heads);
     where[warp][lane] = make_int4(t, h, -1, 0);
     __syncwarp();
-    // An item's vectors, its key's and then its value's, take a power of two
-    // of places, so that no vector costs a division.
-    const int vecs = a.c.dim / 8, total = count << a.shift, mask = (1 << a.shift) - 1;
+    // A key's vectors take a power of two of lanes, and its value's the same
+    // ones: no vector costs a division, and strides are the warp's.
+    const int total = count << a.shift, x = (lane & ((1 << a.shift) - 1)) * 8;
+    const bool on = x < a.c.dim;
     bool looked_up = false;
     for (int i0 = lane; i0 - lane < total; i0 += 32 * kUnroll) {
-        int4 data[kUnroll];
+        int4 k[kUnroll], v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + 32 * u, in = i & mask;
-            if (i < total && in < 2 * vecs) {
+            const int i = i0 + 32 * u;
+            if (i < total && on) {
                 const int4 at = where[warp][i >> a.shift];
-                const bool v = in >= vecs;
-                const uint16_t* src = v ? a.v_new + at.x * a.vns[0] + at.y * a.vns[1] + (in - vecs) * 8
-                                        : a.k_new + at.x * a.kns[0] + at.y * a.kns[1] + in * 8;
-                data[u] = __ldcs(reinterpret_cast<const int4*>(src));
+                k[u] = __ldcs(reinterpret_cast<const int4*>(a.k_new + at.x * a.kns[0] + at.y * a.kns[1] + x));
+                v[u] = __ldcs(reinterpret_cast<const int4*>(a.v_new + at.x * a.vns[0] + at.y * a.vns[1] + x));
             }
         }
         if (!looked_up) {
@@ -93,13 +92,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + 32 * u, in = i & mask;
-            if (i < total && in < 2 * vecs) {
+            const int i = i0 + 32 * u;
+            if (i < total && on) {
                 const int4 at = where[warp][i >> a.shift];
-                const bool v = in >= vecs;
-                uint16_t* dst = v ? a.c.v + at.z * a.c.vs[0] + at.w * a.c.vs[1] + at.y * a.c.vs[2] + (in - vecs) * 8
-                                  : a.c.k + at.z * a.c.ks[0] + at.w * a.c.ks[1] + at.y * a.c.ks[2] + in * 8;
-                if (at.z >= 0) *reinterpret_cast<int4*>(dst) = data[u];
+                if (at.z < 0) continue;
+                *reinterpret_cast<int4*>(a.c.k + at.z * a.c.ks[0] + at.w * a.c.ks[1] + at.y * a.c.ks[2] + x) = k[u];
+                *reinterpret_cast<int4*>(a.c.v + at.z * a.c.vs[0] + at.w * a.c.vs[1] + at.y * a.c.vs[2] + x) = v[u];
             }
         }
     }
@@ -111,8 +109,8 @@ cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k
                              const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
                              KvRows<float> weight, KvRows<int> pos, const int* next_pos) {
     AppendArgs a = {c, k_new, v_new, {k_stride[0], k_stride[1]}, {v_stride[0], v_stride[1]},
-                    tokens, starts, weight, pos, next_pos, 1, 1};
-    while ((1 << a.shift) < c.dim / 4) ++a.shift;
+                    tokens, starts, weight, pos, next_pos, 1, 0};
+    while ((1 << a.shift) < c.dim / 8) ++a.shift;  // dim is at most 256: 32 lanes
     const long long items = (long long)tokens * c.heads;
     // 16 warps an SM at least, then longer ones (40942 tokens of 8 heads: 164 us
     // with one item a warp, 59 with 8 or 16, 62 with 32).

@@ -41,7 +41,7 @@ struct EvictArgs {
     int* movers;  // [seqs * heads][room]: the movers, in the row's last M places
     int room;     // moves a row's lists have room for
     int chunks;   // blocks of the second launch per row
-    int shift;    // log2 of the places that a move's vectors take: no vector costs a division
+    int shift;    // log2 of the lanes that a key takes
     int part;     // slots a block of the first has room for in shared memory
 };
 
@@ -358,12 +358,15 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
 // A warp takes 32 moves: a lane looks up one move's pages, then all lanes
 // copy the 32 moves' vectors, kUnroll of them in flight per lane.
 __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 2;  // of keys and of values each
     __shared__ int4 where[kMoveThreads / 32][32];  // source page and slot in it, target page and slot
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, b = row / a.c.heads, h = row % a.c.heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int vecs = a.c.dim / 8;  // 16-byte vectors of a key
-    const uint16_t *k = a.c.k + h * a.c.ks[2], *v = a.c.v + h * a.c.vs[2];
+    // A key's vectors take a power of two of lanes, and its value's the same
+    // ones: no vector costs a division, and strides are the warp's.
+    const int x = (lane & ((1 << a.shift) - 1)) * 8;
+    const bool on = x < a.c.dim;
+    uint16_t *const k = a.c.k + h * a.c.ks[2] + x, *const v = a.c.v + h * a.c.vs[2] + x;
     grid_dependency_wait();
     if (chunk == 0 && h == 0 && threadIdx.x == 0) {
         const int n = a.lens[b];
@@ -388,29 +391,29 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
         __syncwarp();
         where[warp][lane] = at;
         __syncwarp();
-        const int total = min(32, moves - j0) << a.shift, mask = (1 << a.shift) - 1;
+        const int total = min(32, moves - j0) << a.shift;
         for (int i0 = lane; i0 < total; i0 += 32 * kUnroll) {
-            int4 data[kUnroll];
-            uint16_t* dst[kUnroll];
+            int4 kv[kUnroll], vv[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u, in = i & mask;
-                dst[u] = nullptr;
-                if (i < total && in < 2 * vecs) {
+                const int i = i0 + 32 * u;
+                if (i < total && on) {
                     const int4 q = where[warp][i >> a.shift];
-                    if (q.x >= 0) {
-                        const bool second = in >= vecs;
-                        const uint16_t* base = second ? v : k;
-                        const long long page = second ? a.c.vs[0] : a.c.ks[0], slot = second ? a.c.vs[1] : a.c.ks[1];
-                        const int x = (second ? in - vecs : in) * 8;
-                        data[u] = *reinterpret_cast<const int4*>(base + q.x * page + q.y * slot + x);
-                        dst[u] = const_cast<uint16_t*>(base) + q.z * page + q.w * slot + x;
-                    }
+                    if (q.x < 0) continue;
+                    kv[u] = *reinterpret_cast<const int4*>(k + q.x * a.c.ks[0] + q.y * a.c.ks[1]);
+                    vv[u] = *reinterpret_cast<const int4*>(v + q.x * a.c.vs[0] + q.y * a.c.vs[1]);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (dst[u]) *reinterpret_cast<int4*>(dst[u]) = data[u];
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + 32 * u;
+                if (i < total && on) {
+                    const int4 q = where[warp][i >> a.shift];
+                    if (q.x < 0) continue;
+                    *reinterpret_cast<int4*>(k + q.z * a.c.ks[0] + q.w * a.c.ks[1]) = kv[u];
+                    *reinterpret_cast<int4*>(v + q.z * a.c.vs[0] + q.w * a.c.vs[1]) = vv[u];
+                }
+            }
         }
     }
 }
@@ -474,8 +477,8 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
         err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
     if (err != cudaSuccess) return err;
     ++*launches;
-    a.shift = 1;
-    while ((1 << a.shift) < c.dim / 4) ++a.shift;
+    a.shift = 0;
+    while ((1 << a.shift) < c.dim / 8) ++a.shift;
     a.chunks = (a.room + kMoveThreads - 1) / kMoveThreads;
     const long long most = (1 << 20) / rows + 1;
     if (a.chunks > most) a.chunks = (int)most;
