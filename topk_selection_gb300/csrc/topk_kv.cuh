@@ -88,6 +88,6 @@ struct KvEvict {
 };
 size_t kv_evict_scratch(const KvCache& c, const KvEvict& e);
 cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
-                            unsigned* status, int* launches);
+                            unsigned* counters, unsigned epoch, int* launches);
 
 }  // namespace topk

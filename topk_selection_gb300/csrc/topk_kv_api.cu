@@ -215,10 +215,12 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
     e.lens_out = lens_out;
     void* scratch = nullptr;
     unsigned* status = nullptr;
+    unsigned *counters = nullptr, epoch = 0;
     rc = topk::kv_scratch(device, s, topk::kv_evict_scratch(c, e), &scratch, &status);
+    if (rc == TOPK_OK) rc = topk::kv_counters(device, s, topk::kKvCounters * sizeof(unsigned), &counters, &epoch);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    err = topk::kv_evict_launch(device, s, c, e, scratch, status, &launches);
+    err = topk::kv_evict_launch(device, s, c, e, scratch, counters, epoch, &launches);
     topk::note_launches(launches);
     return err == cudaSuccess ? TOPK_OK : cuda_fail(err);
 }

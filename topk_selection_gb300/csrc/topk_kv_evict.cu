@@ -1,7 +1,11 @@
 // topk_kv_evict: keep the `budget` best slots of each (sequence, head).
 //
 // Bound by HBM: a weight and a position are read per slot, and a kept slot
-// above the budget is read and written once.  Two launches.
+// above the budget is read and written once.  Two launches, or one where few
+// slots move.  512 rows of 8192 slots, half of them kept (1.20 GB): 209 us,
+// 5.7 TB/s, 27 us of them for the selection; 8 rows of 131072 cut to an eighth
+// (128 MB): 41 us, 20 for the selection, whose three digits cost the cluster a
+// barrier and two reads of its neighbours each.
 //
 // The first selects.  A row belongs to a cluster of 1 to 8 blocks, each with
 // a contiguous part of its slots, whose 32-bit keys it reads once and keeps
@@ -31,6 +35,11 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kMostBlocks = 8;  // of a cluster
 constexpr int kMoveThreads = 64;
+// Rows with at most so many moves are moved by the blocks that selected: 32
+// rows of 1101 slots with a budget of 1024 take 9.1 us instead of 11.3, 256
+// of 1280 17.7 instead of 21.1; with 512 moves 32 rows take 12.5 instead of
+// 11.7, and with 1024 moves 256 rows 37.1 instead of 33.3.
+constexpr int kFused = 256;
 
 struct EvictArgs {
     KvCache c;
@@ -43,6 +52,8 @@ struct EvictArgs {
     int chunks;   // blocks of the second launch per row
     int shift;    // log2 of the lanes that a key takes
     int part;     // slots a block of the first has room for in shared memory
+    int fused;    // whether the first launch makes the moves too
+    unsigned* ticket;  // then: its blocks that are done, zero before and after
 };
 
 // Order-preserving key: protected above NaN above every number, -0 equal to
@@ -65,10 +76,73 @@ __device__ __forceinline__ void cluster_sync(int tid) {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// Moves j0 to j0 + count - 1 (at most 32) of a row, by one warp: a lane looks
+// up one move's pages, then all lanes copy the moves' vectors, kUnroll of
+// them in flight per lane.  `where`: the warp's 32 entries of shared memory.
+__device__ __forceinline__ void move_some(const EvictArgs& a, int b, int h, const int* holes, const int* movers, int j0,
+                                          int count, int4* where, int lane) {
+    constexpr int kUnroll = 2;  // of keys and of values each
+    // A key's vectors take a power of two of lanes, and its value's the same
+    // ones: no vector costs a division, and strides are the warp's.
+    const int x = (lane & ((1 << a.shift) - 1)) * 8;
+    const bool on = x < a.c.dim;
+    uint16_t *const k = a.c.k + h * a.c.ks[2] + x, *const v = a.c.v + h * a.c.vs[2] + x;
+    int4 at = make_int4(-1, 0, -1, 0);  // source page and slot in it, target page and slot
+    if (lane < count) {
+        const int from = movers[j0 + lane], to = holes[j0 + lane];
+        const int fi = from / a.c.page_size, ti = to / a.c.page_size;
+        const int* table = a.c.table + b * a.c.table_stride;
+        at = make_int4(table[fi], from - fi * a.c.page_size, table[ti], to - ti * a.c.page_size);
+        a.e.weight_out.row(b, h)[to] = a.e.weight.row(b, h)[from];
+        a.e.pos_out.row(b, h)[to] = a.e.pos.row(b, h)[from];
+        // A move from or to a page that the table does not name is dropped.
+        if ((unsigned)at.x >= (unsigned)a.c.pages || (unsigned)at.z >= (unsigned)a.c.pages) at.x = -1;
+    }
+    __syncwarp();
+    where[lane] = at;
+    __syncwarp();
+    const int total = count << a.shift;
+    for (int i0 = lane; i0 < total; i0 += 32 * kUnroll) {
+        int4 kv[kUnroll], vv[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + 32 * u;
+            if (i < total && on) {
+                const int4 q = where[i >> a.shift];
+                if (q.x < 0) continue;
+                kv[u] = *reinterpret_cast<const int4*>(k + q.x * a.c.ks[0] + q.y * a.c.ks[1]);
+                vv[u] = *reinterpret_cast<const int4*>(v + q.x * a.c.vs[0] + q.y * a.c.vs[1]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + 32 * u;
+            if (i < total && on) {
+                const int4 q = where[i >> a.shift];
+                if (q.x < 0) continue;
+                *reinterpret_cast<int4*>(k + q.z * a.c.ks[0] + q.w * a.c.ks[1]) = kv[u];
+                *reinterpret_cast<int4*>(v + q.z * a.c.vs[0] + q.w * a.c.vs[1]) = vv[u];
+            }
+        }
+    }
+}
+
+// The last block of a launch that makes the moves too writes the lengths: lens
+// may be lens_out, and by then every block has read it.  One warp calls it,
+// after a barrier of its block.
+__device__ __forceinline__ void write_lens(const EvictArgs& a, int lane) {
+    unsigned before = 0;
+    if (lane == 0)
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.ticket) : "memory");
+    if (__shfl_sync(kFullMask, before, 0) + 1 != gridDim.x) return;
+    for (int b = lane; b < a.c.seqs; b += 32) a.e.lens_out[b] = min(__ldcg(a.lens + b), a.e.budget);
+    if (lane == 0) *a.ticket = 0;
+}
+
 // kHeld: the block's keys fit its shared memory; otherwise they are made anew
 // from global memory (L2) in each pass.
 template <int THREADS, bool kHeld>
-__global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constant__ EvictArgs a) {
     constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;
     extern __shared__ __align__(16) unsigned keys[];
     __shared__ __align__(16) int hist[2][kBins];   // of this digit; of the one before, or cleared for the next
@@ -97,6 +171,10 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
             if (copy_p) po[i] = pos[i];
         }
         if (tid == 0 && rank == 0) a.moves[row] = 0;
+        if (a.fused) {
+            __syncthreads();
+            if (warp == 0) write_lens(a, lane);
+        }
         return;
     }
     const int sink = a.e.sink;
@@ -315,7 +393,8 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     const bool lower = lane < rank;
     int up_before = __reduce_add_sync(kFullMask, (lower ? t.x : 0) + (lane < warp ? warp_above[lane] : 0));
     int ties_before = __reduce_add_sync(kFullMask, (lower ? t.y : 0) + (lane < warp ? warp_ties[lane] : 0));
-    if (tid == 0 && rank == 0) a.moves[row] = budget - up_low - min(all_ties_low, need);
+    const int moves = budget - up_low - min(all_ties_low, need);
+    if (tid == 0 && rank == 0) a.moves[row] = moves;
     int* holes = a.holes + (size_t)row * a.room;
     int* movers = a.movers + (size_t)row * a.room + (a.room - budget);
     // Of the keys at the edge, all of this warp's are kept or none, but in the
@@ -353,20 +432,21 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const EvictArgs a) {
     }
     launch_dependents();  // the moves, which wait for this launch's end
     if (blocks > 1) cluster_sync(tid);  // no block leaves while another reads its counts
+    if (!a.fused) return;
+    if (blocks == 1) __syncthreads();
+    // The lists are complete.  The histograms' place takes the looked-up pages.
+    static_assert(sizeof(hist) >= kWarps * 32 * sizeof(int4), "look-ups fit");
+    int4* where = reinterpret_cast<int4*>(&hist[0][0]) + warp * 32;
+    const int warps = blocks * kWarps, batch = min(32, (moves + warps - 1) / warps);
+    for (int j0 = (rank * kWarps + warp) * batch; j0 < moves; j0 += warps * batch)
+        move_some(a, b, h, holes, movers + (budget - moves), j0, min(batch, moves - j0), where, lane);
+    if (warp == 0) write_lens(a, lane);
 }
 
-// A warp takes 32 moves: a lane looks up one move's pages, then all lanes
-// copy the 32 moves' vectors, kUnroll of them in flight per lane.
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a) {
-    constexpr int kUnroll = 2;  // of keys and of values each
-    __shared__ int4 where[kMoveThreads / 32][32];  // source page and slot in it, target page and slot
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_constant__ EvictArgs a) {
+    __shared__ int4 where[kMoveThreads / 32][32];
     const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, b = row / a.c.heads, h = row % a.c.heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // A key's vectors take a power of two of lanes, and its value's the same
-    // ones: no vector costs a division, and strides are the warp's.
-    const int x = (lane & ((1 << a.shift) - 1)) * 8;
-    const bool on = x < a.c.dim;
-    uint16_t *const k = a.c.k + h * a.c.ks[2] + x, *const v = a.c.v + h * a.c.vs[2] + x;
     grid_dependency_wait();
     if (chunk == 0 && h == 0 && threadIdx.x == 0) {
         const int n = a.lens[b];
@@ -375,47 +455,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictArgs a
     const int moves = a.moves[row];
     const int* holes = a.holes + (size_t)row * a.room;
     const int* movers = a.movers + (size_t)row * a.room + (a.room - moves);
-    for (int j0 = (chunk * (kMoveThreads / 32) + warp) * 32; j0 < moves; j0 += a.chunks * kMoveThreads) {
-        const int j = j0 + lane;
-        int4 at = make_int4(-1, 0, -1, 0);
-        if (j < moves) {
-            const int from = movers[j], to = holes[j];
-            const int fi = from / a.c.page_size, ti = to / a.c.page_size;
-            const int* table = a.c.table + b * a.c.table_stride;
-            at = make_int4(table[fi], from - fi * a.c.page_size, table[ti], to - ti * a.c.page_size);
-            a.e.weight_out.row(b, h)[to] = a.e.weight.row(b, h)[from];
-            a.e.pos_out.row(b, h)[to] = a.e.pos.row(b, h)[from];
-            // A move from or to a page that the table does not name is dropped.
-            if ((unsigned)at.x >= (unsigned)a.c.pages || (unsigned)at.z >= (unsigned)a.c.pages) at.x = -1;
-        }
-        __syncwarp();
-        where[warp][lane] = at;
-        __syncwarp();
-        const int total = min(32, moves - j0) << a.shift;
-        for (int i0 = lane; i0 < total; i0 += 32 * kUnroll) {
-            int4 kv[kUnroll], vv[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u;
-                if (i < total && on) {
-                    const int4 q = where[warp][i >> a.shift];
-                    if (q.x < 0) continue;
-                    kv[u] = *reinterpret_cast<const int4*>(k + q.x * a.c.ks[0] + q.y * a.c.ks[1]);
-                    vv[u] = *reinterpret_cast<const int4*>(v + q.x * a.c.vs[0] + q.y * a.c.vs[1]);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u;
-                if (i < total && on) {
-                    const int4 q = where[warp][i >> a.shift];
-                    if (q.x < 0) continue;
-                    *reinterpret_cast<int4*>(k + q.z * a.c.ks[0] + q.w * a.c.ks[1]) = kv[u];
-                    *reinterpret_cast<int4*>(v + q.z * a.c.vs[0] + q.w * a.c.vs[1]) = vv[u];
-                }
-            }
-        }
-    }
+    for (int j0 = (chunk * (kMoveThreads / 32) + warp) * 32; j0 < moves; j0 += a.chunks * kMoveThreads)
+        move_some(a, b, h, holes, movers, j0, min(32, moves - j0), where[warp], lane);
 }
 
 int room_of(const KvCache& c, const KvEvict& e) {
@@ -452,8 +493,8 @@ size_t kv_evict_scratch(const KvCache& c, const KvEvict& e) {
     return 4 * (c.seqs + rows + 2 * rows * room_of(c, e));
 }
 
-cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch, unsigned*,
-                            int* launches) {
+cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
+                            unsigned* counters, unsigned epoch, int* launches) {
     const int rows = c.seqs * c.heads;
     EvictArgs a = {c, e};
     a.room = room_of(c, e);
@@ -461,6 +502,10 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     a.moves = a.lens + c.seqs;
     a.holes = a.moves + rows;
     a.movers = a.holes + (size_t)rows * a.room;
+    a.ticket = counters + (epoch & 1) * (kKvCounters / 2);
+    a.fused = a.room <= kFused;
+    a.shift = 0;
+    while ((1 << a.shift) < c.dim / 8) ++a.shift;
     // Blocks per row: as many as keep the SMs busy twice over, and leave each
     // block 1024 slots at least.  (Clusters of 16 were slower: 8 rows of
     // 131072 slots 53 us instead of 43, since not all eight run at once.)
@@ -477,8 +522,7 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
         err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
     if (err != cudaSuccess) return err;
     ++*launches;
-    a.shift = 0;
-    while ((1 << a.shift) < c.dim / 8) ++a.shift;
+    if (a.fused) return cudaSuccess;
     a.chunks = (a.room + kMoveThreads - 1) / kMoveThreads;
     const long long most = (1 << 20) / rows + 1;
     if (a.chunks > most) a.chunks = (int)most;
