@@ -260,8 +260,10 @@ int topk_reduce_f32(const float* in, size_t n, int op, double* out, struct CUstr
  * (b, h, s) lies at b * seq_stride + h * head_stride + s.
  *
  * All pointers are device memory (TOPK_ERR_INVALID_ARG for host memory) and
- * the calls only enqueue.  Nothing here uses atomics on results: equal inputs
- * give equal outputs, bit for bit, on the same device.
+ * the calls only enqueue.  They may be captured in a graph once a call as
+ * large has run on the stream (the first one allocates).  Nothing here uses
+ * atomics on results: equal inputs give equal outputs, bit for bit, on the
+ * same device.
  */
 enum topk_kv_dtype { TOPK_KV_F16 = 0, TOPK_KV_BF16 = 1 };
 
@@ -332,7 +334,12 @@ int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const i
  *               float32 rows with at least a sequence's capacity of slots,
  *               both or neither; the same array, or not overlapping.
  *
- * Products, sums and softmax statistics are float32.
+ * Products, sums and softmax statistics are float32; a share of attention
+ * enters the product with the values to 16 bits (bfloat16) or 22 (float16).
+ * One launch, and a second one with weights.  Scratch: with weights 512 bytes
+ * per query head (their number per head rounded up to 1, 4, 8 or a multiple of
+ * 16, of 8 for dim > 128) and 128 slots of every sequence's capacity, and a
+ * few MB besides.
  */
 int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64_t* q_stride, int q_heads, float scale,
                    void* out, float* lse, const struct topk_kv_rows* weight, const struct topk_kv_rows* weight_out,
@@ -359,6 +366,9 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
  *   weight_out, pos_out  rows of at least min(budget, capacity) slots: the
  *                        same arrays as weight and pos, or not overlapping.
  *   lens_out             int32[seqs]: min(lens, budget); may be lens itself.
+ *
+ * One launch where at most 256 slots of a row can move, else two.  Scratch: 8
+ * bytes per row and slot that can move, min(budget, capacity - budget).
  */
 int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* weight,
                   const struct topk_kv_rows* pos, const int32_t* next_pos, int budget, int sink, int recent,

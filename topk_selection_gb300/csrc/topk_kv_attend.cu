@@ -25,7 +25,25 @@
 // [c * T / n, (c + 1) * T / n) of them.  A row that lies in one block is
 // finished there; the shares of a row that several blocks have are joined by
 // the last of them to finish (no block waits for another).  With weights, the
-// p are stored, and a second launch adds them up once the sums are known.
+// p are stored (float32, the group's heads of a slot side by side), and a
+// second launch adds them up once the sums are known: storing and reading
+// them costs 8 bytes a slot and head in L2, where a group of eight reads 512
+// of keys and values (dim 128) from HBM.
+//
+// A block has an SM to itself: 192 KB of its shared memory are the rings that
+// keep HBM busy.  Its warps: one copies keys and one values (a tile of small
+// pages is up to 32 copies), one thread issues each product, and two groups
+// of four do the softmax of every other tile, so that their latencies (some
+// 1500 clocks a tile for 8 heads, against 2800 in which HBM delivers a tile of
+// dim 128) overlap.
+//
+// Measured: 64 sequences of 4096 to 16384 slots, 64 query heads on 8, dim 128
+// (2.69 GB): 393 us, 6.84 TB/s, the rate of a copy.  One sequence of 131071
+// with weights (545 MB): 99 us, of which the first launch streams for 78 at
+// the copy's rate; 2.5 us pass before the first copy, 5 to 7 between the last
+// tile and the last join, and 6 in the second launch.  24 sequences of 501 to
+// 2001 with a key-value head for each query head, dim 64 (123 MB): 35 us, the
+// same ends around 21 us of streaming.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
