@@ -169,7 +169,9 @@ __device__ __forceinline__ Walk find_range(const AttendArgs& p, int* sh) {
     const int before = __reduce_add_sync(kFullMask, lane < warp ? v : 0) + x - mine;
     Walk k;
     k.total = __reduce_add_sync(kFullMask, v);
-    k.blocks = min((int)gridDim.x, k.total);
+    // One block to a row where one short sequence is all there is: a join costs
+    // as much as four tiles (300 slots of 2 heads, dim 64: 8.6 us a call instead of 10.4).
+    k.blocks = min((int)gridDim.x, seqs == 1 && k.total <= 4 * p.rows ? p.rows : k.total);
     k.s = k.e = k.b = k.h = k.part = k.t = k.n = k.tiles = 0;
     if ((int)blockIdx.x < k.blocks) {  // uniform over the block
         k.s = share_start(blockIdx.x, k.blocks, k.total);

@@ -402,32 +402,57 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     const bool some = ties_before < need && need < ties_before + ties;
     const unsigned least = ties_before + ties <= need ? edge : edge + 1;  // edge + 1 == 0 has no key at it
     int kept_before = up_before + min(ties_before, need);
-    for (int base = from; base < to; base += 128) {
-        unsigned key[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) key[j] = base + j * 32 < to ? key_at(base + j * 32 + lane) : 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (base + j * 32 >= to) break;
-            const int i0 = base + j * 32, i = i0 + lane;
-            bool kept = key[j] >= least && least != 0;
-            if (some) {
-                const unsigned at = __ballot_sync(kFullMask, key[j] == edge);
-                kept = key[j] > edge || (key[j] == edge && ties_before + __popc(at & lanemask_lt()) < need);
-                ties_before += __popc(at);
-            }
+    auto list = [&](int i, bool kept, int before) {  // slot i, with `before` kept ones below it
+        if (i < budget) {
+            if (!kept) holes[i - before] = i;
+        } else if (kept) {
+            movers[before] = i;
+        }
+    };
+    if (some) {
+        for (int i = from + lane; i - lane < to; i += 32) {
+            const unsigned key = key_at(i);
+            const unsigned at = __ballot_sync(kFullMask, key == edge);
+            const bool kept = key > edge || (key == edge && ties_before + __popc(at & lanemask_lt()) < need);
             const unsigned all = __ballot_sync(kFullMask, kept);
-            const int before = kept_before + __popc(all & lanemask_lt());
-            if (i0 + 32 <= budget) {  // alike for the warp, in nearly every round
-                if (!kept) holes[i - before] = i;
-            } else if (i0 >= budget) {
-                if (kept) movers[before] = i;
-            } else if (i < budget) {
-                if (!kept) holes[i - before] = i;
-            } else if (kept) {
-                movers[before] = i;
-            }
+            ties_before += __popc(at);
+            list(i, kept, kept_before + __popc(all & lanemask_lt()));
             kept_before += __popc(all);
+        }
+    } else {
+        // A lane has four slots in a row; their number of kept ones is added
+        // up over the lanes below by the bits of it.
+        const unsigned lower_lanes = lanemask_lt();
+        for (int base = from; base < to; base += 128) {
+            const int i = base + 4 * lane;
+            unsigned key[4];
+            keys_at(i, to, key);
+            bool kept[4];
+            int mine = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                kept[j] = key[j] >= least && least != 0;
+                mine += kept[j];
+            }
+            const unsigned b0 = __ballot_sync(kFullMask, mine & 1), b1 = __ballot_sync(kFullMask, mine & 2),
+                           b2 = __ballot_sync(kFullMask, mine & 4);
+            int before = kept_before + __popc(b0 & lower_lanes) + 2 * __popc(b1 & lower_lanes) +
+                         4 * __popc(b2 & lower_lanes);
+            kept_before += __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
+            if (i >= to) continue;
+            if (base + 128 <= budget) {  // alike for the warp, nearly always
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!kept[j]) holes[i + j - before] = i + j;
+                    before += kept[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    list(i + j, kept[j], before);
+                    before += kept[j];
+                }
+            }
         }
     }
     launch_dependents();  // the moves, which wait for this launch's end
