@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "topk_internal.h"
@@ -34,6 +35,17 @@ struct KvCache {
         return (unsigned)p < (unsigned)pages ? p : -1;
     }
 };
+
+// Allows a kernel `bytes` of dynamic shared memory on a device; asked once
+// per device, of which `done` keeps a bit.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, int device, std::atomic<unsigned long long>& done) {
+    const unsigned long long bit = 1ull << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // A per-slot side array, [seqs, heads, slots].
 template <typename T>

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const long long items = (long long)a.tokens * a.c.heads;
     const long long first = ((long long)blockIdx.x * (kAppendThreads / 32) + warp) * a.per;
     if (first >= items) return;
+    grid_dependency_wait();  // launched early (launch_pdl): the previous kernel's writes first
     const int count = (int)min((long long)a.per, items - first);
     const int t = (int)((first + lane) / a.c.heads), h = (int)(first + lane - (long long)t * a.c.heads);
     where[warp][lane] = make_int4(t, h, -1, 0);
@@ -121,8 +122,7 @@ cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k
     while (a.per < 16 && items / (2 * a.per) >= 152 * 16) a.per *= 2;
     const long long warps = (items + a.per - 1) / a.per, blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    kv_append_kernel<<<(unsigned)blocks, kAppendThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(kv_append_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, s, a);
 }
 
 }  // namespace topk

@@ -1148,10 +1148,11 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
 }
 
 template <int DP, int GP>
-cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, int* launches) {
+cudaError_t launch(const Plan& plan, int device, cudaStream_t s, const CUtensorMap* maps, int* launches) {
     using Sh = Shape<DP, GP>;
     auto kernel = kv_attend_kernel<DP, GP>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    static std::atomic<unsigned long long> allowed{0}, allowed_weights{0};
+    cudaError_t e = allow_smem(kernel, (int)Sh::kSmem, device, allowed);
     if (e != cudaSuccess) return e;
     // Started early, it sets up its barriers and waits for the launch before it.
     e = launch_pdl(kernel, dim3(plan.blocks), dim3(kThreads), Sh::kSmem, s, plan.args, maps[0], maps[1], maps[2]);
@@ -1162,7 +1163,7 @@ cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, in
     // by one: the shared memory, which it does not use, keeps two of them from
     // sharing the SM that is free first (131072 slots: 10.2 us of it without, 5.6 with).
     constexpr int kAlone = 120 * 1024;
-    e = cudaFuncSetAttribute(kv_weight_kernel<GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
+    e = allow_smem(kv_weight_kernel<GP>, kAlone, device, allowed_weights);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kv_weight_kernel<GP>, dim3(plan.blocks), dim3(kWeightThreads), kAlone, s, plan.args);
     if (e == cudaSuccess) ++*launches;
@@ -1170,14 +1171,14 @@ cudaError_t launch(const Plan& plan, cudaStream_t s, const CUtensorMap* maps, in
 }
 
 template <int DP>
-cudaError_t launch_dim(const Plan& plan, int gp, cudaStream_t s, const CUtensorMap* maps, int* launches) {
+cudaError_t launch_dim(const Plan& plan, int gp, int device, cudaStream_t s, const CUtensorMap* maps, int* launches) {
     switch (gp) {
-        case 1: return launch<DP, 1>(plan, s, maps, launches);
-        case 4: return launch<DP, 4>(plan, s, maps, launches);
-        case 8: return launch<DP, 8>(plan, s, maps, launches);
+        case 1: return launch<DP, 1>(plan, device, s, maps, launches);
+        case 4: return launch<DP, 4>(plan, device, s, maps, launches);
+        case 8: return launch<DP, 8>(plan, device, s, maps, launches);
         default: break;
     }
-    if constexpr (DP <= 128) return launch<DP, 16>(plan, s, maps, launches);
+    if constexpr (DP <= 128) return launch<DP, 16>(plan, device, s, maps, launches);
     return cudaErrorInvalidValue;
 }
 
@@ -1204,9 +1205,9 @@ cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const
     if (e == cudaSuccess) e = make_map(&maps[1], c.v, c.bf16, 4, pool, vs, pool_box);
     if (e == cudaSuccess) e = make_map(&maps[2], a.q, c.bf16, 3, queries, qs, query_box);
     if (e != cudaSuccess) return e;
-    if (c.dim <= 64) return launch_dim<64>(plan, gp, s, maps, launches);
-    if (c.dim <= 128) return launch_dim<128>(plan, gp, s, maps, launches);
-    return launch_dim<256>(plan, gp, s, maps, launches);
+    if (c.dim <= 64) return launch_dim<64>(plan, gp, device, s, maps, launches);
+    if (c.dim <= 128) return launch_dim<128>(plan, gp, device, s, maps, launches);
+    return launch_dim<256>(plan, gp, device, s, maps, launches);
 }
 
 }  // namespace topk

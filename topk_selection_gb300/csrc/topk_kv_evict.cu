@@ -35,6 +35,7 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kMostBlocks = 8;  // of a cluster
 constexpr int kMoveThreads = 64;
+constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
 // Rows with at most so many moves are moved by the blocks that selected: 32
 // rows of 1101 slots with a budget of 1024 take 9.1 us instead of 11.3, 256
 // of 1280 17.7 instead of 21.1; with 512 moves 32 rows take 12.5 instead of
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = blockIdx.x / blocks, b = row / a.c.heads, h = row % a.c.heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
     const int n = a.c.len(b), budget = a.e.budget;
     const float* w = a.e.weight.row(b, h);
     const int* pos = a.e.pos.row(b, h);
@@ -259,15 +261,19 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
         __syncthreads();
         // Thread t has kPer bins, t = 0 the highest.
         using Vec = typename std::conditional<kPer == 2, int2, int4>::type;
+        constexpr int kWide = sizeof(Vec) / 4;
         int* mine = hist[pass & 1];
         auto bins_of = [&](const int* from, int t, int (&own)[kPer]) {  // highest first
-            const Vec v = *reinterpret_cast<const Vec*>(from + kBins - kPer * (t + 1));
-            const int* x = reinterpret_cast<const int*>(&v);
             int sum = 0;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                own[j] = x[kPer - 1 - j];
-                sum += own[j];
+            for (int i = 0; i < kPer; i += kWide) {
+                const Vec v = *reinterpret_cast<const Vec*>(from + kBins - kPer * (t + 1) + i);
+                const int* x = reinterpret_cast<const int*>(&v);
+#pragma unroll
+                for (int j = 0; j < kWide; ++j) {
+                    own[kPer - 1 - i - j] = x[j];
+                    sum += x[j];
+                }
             }
             return sum;
         };
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     if (!a.fused) return;
     if (blocks == 1) __syncthreads();
     // The lists are complete.  The histograms' place takes the looked-up pages.
-    static_assert(sizeof(hist) >= kWarps * 32 * sizeof(int4), "look-ups fit");
+    static_assert(kWarps <= 32 && sizeof(hist) >= kWarps * 32 * sizeof(int4), "look-ups fit");
     int4* where = reinterpret_cast<int4*>(&hist[0][0]) + warp * 32;
     const int warps = blocks * kWarps, batch = min(32, (moves + warps - 1) / warps);
     for (int j0 = (rank * kWarps + warp) * batch; j0 < moves; j0 += warps * batch)
@@ -490,24 +496,26 @@ int room_of(const KvCache& c, const KvEvict& e) {
 }
 
 template <int THREADS, bool kHeld>
-cudaError_t select(const EvictArgs& a, int rows, int blocks, cudaStream_t s) {
+cudaError_t select(const EvictArgs& a, int rows, int blocks, int device, cudaStream_t s) {
     auto kernel = kv_select_kernel<THREADS, kHeld>;
     const size_t smem = kHeld ? (size_t)a.part * 4 : 0;
-    if (smem > 16 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr int kMostSmem = kMostHeld * 4;
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = kHeld ? allow_smem(kernel, kMostSmem, device, allowed) : cudaSuccess;
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * blocks));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it waits before it reads anything
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -518,7 +526,7 @@ size_t kv_evict_scratch(const KvCache& c, const KvEvict& e) {
     return 4 * (c.seqs + rows + 2 * rows * room_of(c, e));
 }
 
-cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
+cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
                             unsigned* counters, unsigned epoch, int* launches) {
     const int rows = c.seqs * c.heads;
     EvictArgs a = {c, e};
@@ -534,17 +542,21 @@ cudaError_t kv_evict_launch(int, cudaStream_t s, const KvCache& c, const KvEvict
     // Blocks per row: as many as keep the SMs busy twice over, and leave each
     // block 1024 slots at least.  (Clusters of 16 were slower: 8 rows of
     // 131072 slots 53 us instead of 43, since not all eight run at once.)
-    constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
     int blocks = 1;
     while (blocks < 8 && rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024) blocks *= 2;
     while (blocks < 8 && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
     a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
     const bool held = a.part <= kMostHeld;
     cudaError_t err;
-    if (rows * blocks <= 152)
-        err = held ? select<1024, true>(a, rows, blocks, s) : select<1024, false>(a, rows, blocks, s);
+    // Short rows spend their time at barriers, which cost less in small blocks
+    // (32 rows of 1101 slots: 8.0 us with 256 threads, 9.0 with 1024); few long
+    // ones need all the threads that an SM takes (8 of 131072: 42 us with 1024, 45 with 512).
+    if (rows * blocks <= 152 && blocks == 1 && c.capacity() <= 2048)
+        err = select<256, true>(a, rows, blocks, device, s);
+    else if (rows * blocks <= 152)
+        err = held ? select<1024, true>(a, rows, blocks, device, s) : select<1024, false>(a, rows, blocks, device, s);
     else
-        err = held ? select<512, true>(a, rows, blocks, s) : select<512, false>(a, rows, blocks, s);
+        err = held ? select<512, true>(a, rows, blocks, device, s) : select<512, false>(a, rows, blocks, device, s);
     if (err != cudaSuccess) return err;
     ++*launches;
     if (a.fused) return cudaSuccess;
