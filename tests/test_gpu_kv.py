@@ -378,6 +378,15 @@ def test_evict_long_rows(tk):
 
 def test_evict_rows_beyond_shared_memory(tk):
     check_evict(tk, [900001], 1, 8, 1024, 100000, 4, 1000, rand_weight)
+    check_evict(tk, [400300], 1, 8, 1024, 400200, 4, 1000, few_values, in_place=True)  # few moves
+
+
+@pytest.mark.parametrize("lens,budget,heads", [([1040, 1025, 1024], 1024, 8), ([2100] * 70, 2048, 4), ([33], 32, 1),
+                                               ([5000, 4990, 4800], 4900, 1)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_a_few(tk, lens, budget, heads, in_place):
+    """What a decoder evicts that stays at its budget: few slots of each row, moved by the launch that selects."""
+    check_evict(tk, lens, heads, 64, 16, budget, 2, 20, rand_weight, in_place=in_place, dtype=torch.bfloat16)
 
 
 def test_evict_pages_of_none(tk):

@@ -1098,10 +1098,13 @@ int group_part(const KvCache& c, const KvAttend& a) {
 }
 
 int sm_count(int device) {
-    static int counts[64];
-    if (device < 0 || device >= 64) return 152;
-    if (!counts[device]) cudaDeviceGetAttribute(&counts[device], cudaDevAttrMultiProcessorCount, device);
-    return counts[device];
+    static std::atomic<int> counts[64];
+    int n = device >= 0 && device < 64 ? counts[device].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 1;
+        if (device >= 0 && device < 64) counts[device].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 // The plan of a call, and its scratch when `scratch` is given.
