@@ -40,7 +40,7 @@
 //
 // Measured: 64 sequences of 4096 to 16384 slots, 64 query heads on 8, dim 128
 // (2.69 GB): 393 us, 6.84 TB/s, the rate of a copy.  One sequence of 131071
-// with weights (545 MB): 99 us, of which the first launch streams for 78 at
+// with weights (545 MB): 97 us, of which the first launch streams for 78 at
 // the copy's rate; 2.5 us pass before the first copy, 5 to 7 between the last
 // tile and the last join, and 6 in the second launch.  24 sequences of 501 to
 // 2001 with a key-value head for each query head, dim 64 (123 MB): 35 us, the

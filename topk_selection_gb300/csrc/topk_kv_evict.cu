@@ -2,9 +2,9 @@
 //
 // Bound by HBM: a weight and a position are read per slot, and a kept slot
 // above the budget is read and written once.  Two launches, or one where few
-// slots move.  512 rows of 8192 slots, half of them kept (1.20 GB): 209 us,
-// 5.7 TB/s, 27 us of them for the selection; 8 rows of 131072 cut to an eighth
-// (128 MB): 41 us, 20 for the selection, whose three digits cost the cluster a
+// slots move.  512 rows of 8192 slots, half of them kept (1.20 GB): 205 us,
+// 5.8 TB/s, 25 us of them for the selection; 8 rows of 131072 cut to an eighth
+// (128 MB): 40 us, 20 for the selection, whose three digits cost the cluster a
 // barrier and two reads of its neighbours each.
 //
 // The first selects.  A row belongs to a cluster of 1 to 8 blocks, each with
