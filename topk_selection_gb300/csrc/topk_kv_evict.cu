@@ -549,9 +549,11 @@ cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const 
     const bool held = a.part <= kMostHeld;
     cudaError_t err;
     // Short rows spend their time at barriers, which cost less in small blocks
-    // (32 rows of 1101 slots: 8.0 us with 256 threads, 9.0 with 1024); few long
-    // ones need all the threads that an SM takes (8 of 131072: 42 us with 1024, 45 with 512).
-    if (rows * blocks <= 152 && blocks == 1 && c.capacity() <= 2048)
+    // (32 rows of 1101 slots: 8.0 us with 256 threads, 9.0 with 1024; 160 of
+    // 1500 10.9, with 512 11.2), and more than two of which share an SM (512 of
+    // 1100: 14.5 and 18.9, of 4500 115 and 118, but of 8192 211 and 205).  Few
+    // long ones need all the threads that an SM takes (8 of 131072: 42 us with 1024, 45 with 512).
+    if (blocks == 1 && c.capacity() <= (rows <= 304 ? 2048 : 5120))
         err = select<256, true>(a, rows, blocks, device, s);
     else if (rows * blocks <= 152)
         err = held ? select<1024, true>(a, rows, blocks, device, s) : select<1024, false>(a, rows, blocks, device, s);
