@@ -36,10 +36,11 @@ constexpr int kBins = 2048;
 constexpr int kMostBlocks = 8;  // of a cluster
 constexpr int kMoveThreads = 64;
 constexpr int kMostHeld = 48 * 1024;  // keys that fit beside the histograms
-// Rows with at most so many moves are moved by the blocks that selected: 32
-// rows of 1101 slots with a budget of 1024 take 9.1 us instead of 11.3, 256
-// of 1280 17.7 instead of 21.1; with 512 moves 32 rows take 12.5 instead of
-// 11.7, and with 1024 moves 256 rows 37.1 instead of 33.3.
+// Rows with at most so many moves are moved by the blocks that selected.  With
+// a budget of 1024: 32 rows of 1101 slots 8.7 us instead of 10.5, 256 of them
+// 10.3 instead of 12.1; with 256 moves 32 rows 11.5 instead of 10.8, but 256
+// rows 14.4 instead of 15.1 and 512 27.6 instead of 28.7; with 512 moves 32
+// rows 16.3 instead of 11.2, and 256 27.6 instead of 21.7.
 constexpr int kFused = 256;
 
 struct EvictArgs {
