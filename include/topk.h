@@ -335,7 +335,8 @@ int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const i
  *               both or neither; the same array, or not overlapping.
  *
  * Products, sums and softmax statistics are float32; a share of attention
- * enters the product with the values to 16 bits (bfloat16) or 22 (float16).
+ * enters the product with the values to 24 bits (bfloat16) or 22 (float16);
+ * to 16 for bfloat16 heads in groups above 8 with dim <= 128.
  * One launch, and a second one with weights.  Scratch: with weights 512 bytes
  * per query head (their number per head rounded up to 1, 4, 8 or a multiple of
  * 16, of 8 for dim > 128) and 128 slots of every sequence's capacity, and a

@@ -15,10 +15,13 @@
 // Softmax is one pass.  p = 2^(s * scale * log2(e) - m + kBias), where m is a
 // reference that moves only when some score passes it by kSlack (a factor
 // 2^kSlack, far from float32's range), so that O is hardly ever rescaled.  P
-// enters the second product as two 16-bit numbers, hi + lo, which the
-// product adds up in columns of their own: 16 columns are the least that
-// this shape of the instruction takes, and a group of 8 fills them with hi
-// and lo, so P keeps 16 bits or more at no cost.
+// enters the second product as a sum of 16-bit numbers, each what the ones
+// before it left, which the product adds up in columns of their own: two
+// numbers of float16 (22 bits), three of bfloat16 (24: all of float32's).
+// The product is far from its rate, so further columns cost what it takes to
+// split and store P.  Only 9 to 16 bfloat16 heads at once stay at two
+// numbers, 16 bits: their 48 columns would take P's buffers from 16 to 32 KB,
+// and the rings fill the shared memory.
 //
 // Work is split evenly whatever the lengths are: all (sequence, head) rows'
 // tiles of 128 slots are numbered in order, and block c takes the range
@@ -213,7 +216,9 @@ struct Shape {
     static constexpr int kItem = kTile * kSub * 128;      // bytes of a part
     static constexpr int kRing = kRingBytes / 2 / kItem;
     static constexpr int kQBytes = DP / 64 * 16 * 128;    // 16 rows of a query block
-    static constexpr int kPCols = GP <= 8 ? 16 : 2 * GP;  // hi of every head, then lo; the rest is not looked at
+    static constexpr int kTerms = GP <= 8 ? 3 : 2;        // numbers that P is split into at most
+    // The first number of every head, then the second, ...; the rest is not looked at.
+    static constexpr int kPCols = GP <= 4 ? 16 : 32;
     static constexpr int kPRow = kPCols * 2;              // bytes of a slot's row of P
     static constexpr int kPBytes = kPRow * kTile;
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
@@ -221,7 +226,7 @@ struct Shape {
     // Tensor memory columns: two S buffers of 16, then O of each softmax
     // group for this row, and of both for the row before.
     static constexpr int kTmemS = 0, kTmemO = 32, kOCols = kOBlocks * kPCols;
-    static constexpr int kTmemCols = 32 + 4 * kOCols <= 128 ? 128 : 256;
+    static constexpr int kTmemCols = 32 + 4 * kOCols <= 128 ? 128 : 32 + 4 * kOCols <= 256 ? 256 : 512;
     static constexpr size_t kSmem = 1024 + kRingBytes + 2 * kQBytes + 2 * kPBytes;
     // Barriers, by their place in bars[].
     static constexpr int kFullK = 0, kFullV = kRing, kEmptyK = 2 * kRing, kEmptyV = 3 * kRing, kSFull = 4 * kRing,
@@ -280,24 +285,29 @@ __device__ __forceinline__ float warp_sums(float (&v)[GP], int lane) {
 template <int GP>
 __device__ __forceinline__ int warp_head(int lane) { return lane / (32 / GP); }
 
-// N numbers as 16-bit elements hi and lo = p - hi, all hi and then all lo.
-template <bool BF16, int N>
+// N numbers as sums of TERMS 16-bit elements (of two for float16), each the
+// rounded rest of the ones before it: the first of all numbers, then the second, ...
+template <bool BF16, int TERMS, int N>
 __device__ __forceinline__ void split(const float (&p)[N], uint32_t* words) {
-    uint16_t e[2 * N];
+    uint16_t e[TERMS * N + 1] = {};
 #pragma unroll
     for (int g = 0; g < N; ++g) {
-        if constexpr (BF16) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(p[g]);
-            e[g] = __bfloat16_as_ushort(hi);
-            e[N + g] = __bfloat16_as_ushort(__float2bfloat16_rn(p[g] - __bfloat162float(hi)));
-        } else {
-            const __half hi = __float2half_rn(p[g]);
-            e[g] = __half_as_ushort(hi);
-            e[N + g] = __half_as_ushort(__float2half_rn(p[g] - __half2float(hi)));
+        float rest = p[g];
+#pragma unroll
+        for (int t = 0; t < (BF16 ? TERMS : 2); ++t) {
+            if constexpr (BF16) {
+                const __nv_bfloat16 x = __float2bfloat16_rn(rest);
+                e[t * N + g] = __bfloat16_as_ushort(x);
+                rest -= __bfloat162float(x);
+            } else {
+                const __half x = __float2half_rn(rest);
+                e[t * N + g] = __half_as_ushort(x);
+                rest -= __half2float(x);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) words[i] = (uint32_t)e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
+    for (int i = 0; i < (TERMS * N + 1) / 2; ++i) words[i] = (uint32_t)e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
 }
 
 // N consecutive floats, as wide as they come.
@@ -474,7 +484,6 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
     __shared__ float red[2][4][GP];                        // of each softmax group and its warps
     __shared__ __align__(16) float each[2][2][kRow];       // two numbers of each head for the group's threads
     __shared__ float told_m[4][GP], told_l[4][4][GP];      // what one group tells the other at a row's end
-    __shared__ float factor[2][kJoin][GP];
     __shared__ float2 joined[2][GP];
     __shared__ unsigned arrived[2];
     __shared__ volatile int gave_up;
@@ -794,11 +803,11 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                         ok = wait(S::kPFree + group, ((it >> 1) & 1) ^ 1);  // the group's tile before is in O
                         __syncwarp();
                         tc_fence_after();
-                        constexpr int kStep = 2 * GP < 8 ? 2 * GP : 8;
+                        constexpr int kStep = GP < 8 ? 4 : 8;
 #pragma unroll
                         for (int o = 0; o < S::kOBlocks; ++o) {
 #pragma unroll
-                            for (int j = 0; j < 2 * GP; j += kStep) {
+                            for (int j = 0; j < S::kTerms * GP; j += kStep) {
                                 float v[kStep];
                                 const uint32_t at = my_o + o * S::kPCols + j;
                                 tmem_ld<kStep>(at, v);
@@ -826,14 +835,17 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                         if (g < heads) to[g * kTile] = e[g];
                     if (me < GP) p.tile_m[(size_t)(tile0 + k) * GP + me] = my_m;
                 }
-                uint32_t word[GP];
-                if (p.c.bf16) split<true, GP>(e, word); else split<false, GP>(e, word);
+                uint32_t word[(S::kTerms * GP + 1) / 2];
+                if (p.c.bf16) split<true, S::kTerms, GP>(e, word); else split<false, S::kTerms, GP>(e, word);
                 if (it >= 2) ok = ok && wait(S::kPFree + group, ((it >> 1) & 1) ^ 1);
-                if constexpr (GP == 1) {
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(my_p + (turn << 4)), "r"(word[0]) : "memory");
-                } else {
+                if constexpr (GP <= 4) {
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(my_p + ((GP == 4 ? 1 ^ turn : turn) << 4)),
+                                 "r"(word[GP == 4 ? 4 : 0]), "r"(word[GP == 4 ? 5 : 1])
+                                 : "memory");
+                }
+                if constexpr (GP > 1) {
 #pragma unroll
-                    for (int i = 0; i < GP / 4; ++i)
+                    for (int i = 0; i < S::kTerms * GP / 8; ++i)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(my_p + ((i ^ turn) << 4)),
                                      "r"(word[4 * i]), "r"(word[4 * i + 1]), "r"(word[4 * i + 2]), "r"(word[4 * i + 3])
                                      : "memory");
@@ -930,24 +942,28 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 constexpr int kStep = GP < 8 ? GP : 8;
 #pragma unroll
                 for (int j = 0; j < GP; j += kStep) {
-                    // hi and lo columns of this group's O, then of the other's
-                    float v[4][kStep], fa[kStep], fb[kStep];
+                    // The columns of P's numbers in this group's O, then in the other's.
+                    float v[2 * S::kTerms][kStep], fa[kStep], fb[kStep];
                     const uint32_t at = my_o + o * S::kPCols + j;
                     const uint32_t other = group == 0 ? at + S::kOCols : at - S::kOCols;
-                    tmem_ld<kStep>(at, v[0]);
-                    tmem_ld<kStep>(at + GP, v[1]);
-                    if (n > 1) {
-                        tmem_ld<kStep>(other, v[2]);
-                        tmem_ld<kStep>(other + GP, v[3]);
-                    }
+#pragma unroll
+                    for (int t = 0; t < S::kTerms; ++t) tmem_ld<kStep>(at + t * GP, v[t]);
+                    if (n > 1)
+#pragma unroll
+                        for (int t = 0; t < S::kTerms; ++t) tmem_ld<kStep>(other + t * GP, v[S::kTerms + t]);
                     load_row<kStep>(first_of + j, fa);
                     load_row<kStep>(second_of + j, fb);
                     tmem_wait_ld();
+                    auto sum_of = [&](int t, int i) {
+                        float x = v[t][i] + v[t + 1][i];
+                        if (S::kTerms == 3 && p.c.bf16) x += v[t + S::kTerms - 1][i];  // float16 has two
+                        return x;
+                    };
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
                         // A head with no sum has a factor of 0, also where its products are not numbers.
-                        v[0][i] = fa[i] == 0.f ? 0.f : (v[0][i] + v[1][i]) * fa[i];
-                        if (n > 1 && fb[i] != 0.f) v[0][i] += (v[2][i] + v[3][i]) * fb[i];
+                        v[0][i] = fa[i] == 0.f ? 0.f : sum_of(0, i) * fa[i];
+                        if (n > 1 && fb[i] != 0.f) v[0][i] += sum_of(S::kTerms, i) * fb[i];
                     }
                     if (whole) {
                         uint16_t* to = p.a.out + (size_t)(q0 + j) * p.c.dim + d;
@@ -963,9 +979,13 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 }
             }
             tc_fence_before();
-            if (!whole)
-                join_row<GP>(p, x.total, x.blocks, row_start, x.tiles, q0, heads, row_ml, factor[group], joined[group],
+            if (!whole) {
+                // The group's P is free: its products are over, and it writes the next one behind a barrier.
+                static_assert(S::kPBytes >= kJoin * GP * sizeof(float), "a join's factors fit where P was");
+                auto* factor = reinterpret_cast<float(*)[GP]>(smem_raw + (p_buf + group * S::kPBytes - smem_addr(smem_raw)));
+                join_row<GP>(p, x.total, x.blocks, row_start, x.tiles, q0, heads, row_ml, factor, joined[group],
                              &arrived[group], 1 + group, me);
+            }
             x.t += n - 1;
             x.next(p);
         }

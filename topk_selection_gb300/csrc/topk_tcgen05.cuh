@@ -91,9 +91,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float* r) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const float* r) {
-    static_assert(N == 2 || N == 8, "columns");
-    if constexpr (N == 2)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"f"(r[0]), "f"(r[1]), "r"(addr)
+    static_assert(N == 4 || N == 8, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]),
+                     "f"(r[3]), "r"(addr)
                      : "memory");
     if constexpr (N == 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "r"(addr)
