@@ -261,7 +261,11 @@ int topk_reduce_f32(const float* in, size_t n, int op, double* out, struct CUstr
  *
  * All pointers are device memory (TOPK_ERR_INVALID_ARG for host memory) and
  * the calls only enqueue.  They may be captured in a graph once a call as
- * large has run on the stream (the first one allocates).  Nothing here uses
+ * large has run on the stream (the first one allocates).  The scratch that a
+ * captured call was given lives until topk_release_workspace(), whatever
+ * larger calls follow on the stream.  It is the stream's all the same: graphs
+ * captured on one stream, and calls on that stream, have to run one after
+ * another, on whichever stream the graphs are launched.  Nothing here uses
  * atomics on results: equal inputs give equal outputs, bit for bit, on the
  * same device.
  */

@@ -64,3 +64,92 @@ def test_shares_enter_the_product_with_float32s_bits(tk, dim, group, dtype):
         p = np.exp(kk[:, 0]) / np.exp(kk[:, 0]).sum()
         tol[b] = _kv.UNIT[dtype] * np.abs(want[b]) + 2.0 ** -25 + 2.0 ** -20 * (p @ np.abs(vv))
     _kv.close(out, want, tol)
+
+
+def decoder(seqs, n, heads, group, dim, dtype=torch.float16, seed=42):
+    """A cache of `n` slots in each sequence, weights to attend with, and what to evict to."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    page = 16
+    width = n // page + 1
+    k, v = (torch.randn(seqs * width, heads, page, dim, device="cuda", generator=g).to(dtype).transpose(1, 2)
+            for _ in range(2))
+    table = torch.randperm(seqs * width, device="cuda", generator=g).to(torch.int32).reshape(seqs, width)
+    lens = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    q = torch.randn(seqs, heads * group, dim, device="cuda", generator=g).to(dtype)
+    weight = torch.rand(seqs, heads, width * page, device="cuda", generator=g)
+    pos = torch.arange(width * page, dtype=torch.int32, device="cuda").repeat(seqs, heads, 1)
+    return dict(k=k, v=v, table=table, lens=lens, q=q, weight=weight, pos=pos)
+
+
+def attend_and_evict(tk, c, k, v):
+    """A step on copies of the pools: (out, lse, weights, evicted weights, positions)."""
+    w_out = torch.full_like(c["weight"], -1.0)
+    out, lse = tk.kv_attend(c["q"], k, v, c["table"], c["lens"], weight=c["weight"], weight_out=w_out)
+    n = c["weight"].shape[2]
+    w, p, _ = tk.kv_evict(k, v, c["table"], c["lens"], w_out, c["pos"], c["lens"], n // 2, sink=2, recent=8,
+                          weight_out=torch.full_like(w_out, -1.0), pos_out=torch.full_like(c["pos"], -1),
+                          lens_out=torch.zeros_like(c["lens"]))
+    return out, lse, w_out, w, p
+
+
+def test_graphs_outlive_larger_calls(tk):
+    """One graph per batch size, captured on one stream from small to large: each goes on working, and no replay writes
+    into what was allocated since."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(s):
+        for seqs, n in ((1, 700), (3, 2100), (8, 6000), (8, 6100), (24, 9000)):
+            c = decoder(seqs, n, 2, 4, 64)
+            k, v = c["k"].clone(), c["v"].clone()
+            want = [t.clone() for t in attend_and_evict(tk, c, k, v)]
+            k.copy_(c["k"])
+            v.copy_(c["v"])
+            s.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                got = attend_and_evict(tk, c, k, v)
+            graphs.append((graph, c, k, v, want, got))
+        big = decoder(40, 16000, 4, 8, 64)
+        attend_and_evict(tk, big, big["k"].clone(), big["v"].clone())
+        s.synchronize()
+        del big
+        torch.cuda.empty_cache()
+        patterns = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+                    for size in [2 ** 20] * 8 + [2 ** 21] * 8 + [2 ** 23] * 4 + [2 ** 25] * 4 + [2 ** 28]]
+        for _ in range(2):
+            for graph, c, k, v, want, got in graphs:
+                k.copy_(c["k"])
+                v.copy_(c["v"])
+                for t in got:
+                    t.zero_()
+                graph.replay()
+                for a, b in zip(got, want):
+                    assert torch.equal(a, b)
+        assert all(bool((p == 0x5A).all()) for p in patterns)
+    s.synchronize()
+
+
+def test_a_capture_that_would_allocate_is_refused(tk):
+    """The status comes back, the capture goes on, and the same call works on the stream afterwards."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c = decoder(2, 300, 2, 2, 64)
+    big = decoder(20, 3000, 4, 8, 64)
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.stream(s):
+        attend_and_evict(tk, c, c["k"].clone(), c["v"].clone())
+        s.synchronize()
+        w_out = torch.zeros_like(big["weight"])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            with pytest.raises(tk.TopKError) as err:
+                tk.kv_attend(big["q"], big["k"], big["v"], big["table"], big["lens"], weight=big["weight"],
+                             weight_out=w_out)
+            x += 1
+        assert err.value.status == 3  # TOPK_ERR_NO_MEMORY
+        graph.replay()
+        assert x.tolist() == [1, 1, 1, 1]
+        tk.kv_attend(big["q"], big["k"], big["v"], big["table"], big["lens"], weight=big["weight"], weight_out=w_out)
+    s.synchronize()
+    tk.check_stream(s)

@@ -10,6 +10,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "../../include/topk.h"
 #include "topk_internal.h"
@@ -75,9 +76,10 @@ struct Workspace {
     unsigned sort_epoch = 0;    // tags the sort's look-back words, one per call
     void* kv = nullptr;         // key-value cache operators' scratch
     size_t kv_bytes = 0;
-    void* kv_count = nullptr;   // their counters (zero between calls), and the calls so far
-    size_t kv_count_bytes = 0;
-    unsigned kv_epoch = 0;
+    bool kv_in_graph = false;   // whether a captured call holds its address
+    std::vector<void*> kv_kept; // outgrown scratch that captured calls hold
+    void* kv_state = nullptr;   // their status word and counters (zero between calls); never moves
+    unsigned kv_epoch = 0;      // calls so far
 };
 
 std::mutex g_ws_mutex;
@@ -130,6 +132,50 @@ int workspace(cudaStream_t s, int device, size_t ctrl_cand, size_t in_bytes, siz
     return TOPK_OK;
 }
 
+// At least `need` bytes of scratch for the key-value cache operators, and
+// their status and counters, on s.  A graph holds the addresses that its calls
+// were captured with and may be replayed at any time: nothing is allocated in
+// a capture, and scratch that a captured call was given is kept when it is
+// outgrown (until the workspace is released).  What replaces it is twice as
+// large where that can be had, so that all that is kept stays below the last
+// one's size.
+int grow_kv(Workspace& w, cudaStream_t s, size_t need) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &status) != cudaSuccess) cudaGetLastError();
+    if (status != cudaStreamCaptureStatusNone) {
+        if (!w.kv_state || w.kv_bytes < need) {
+            t_last_cuda_error = (int)cudaErrorStreamCaptureUnsupported;
+            return TOPK_ERR_NO_MEMORY;
+        }
+        w.kv_in_graph = true;
+        return TOPK_OK;
+    }
+    if (!w.kv_state) {
+        void* state = nullptr;
+        size_t bytes = 0;
+        const int rc = grow(&state, &bytes, topk::kKvStateWords * sizeof(unsigned));
+        if (rc != TOPK_OK) return rc;
+        const cudaError_t e = cudaMemsetAsync(state, 0, bytes, s);
+        if (e != cudaSuccess) {
+            cudaFree(state);
+            return cuda_fail(e);
+        }
+        w.kv_state = state;
+    }
+    if (w.kv_bytes >= need) return TOPK_OK;
+    if (!w.kv_in_graph) return grow(&w.kv, &w.kv_bytes, need);
+    void* larger = nullptr;
+    size_t bytes = 0;
+    int rc = grow(&larger, &bytes, need > 2 * w.kv_bytes ? need : 2 * w.kv_bytes);
+    if (rc != TOPK_OK && need < 2 * w.kv_bytes) rc = grow(&larger, &bytes, need);
+    if (rc != TOPK_OK) return rc;
+    w.kv_kept.push_back(w.kv);
+    w.kv = larger;
+    w.kv_bytes = bytes;
+    w.kv_in_graph = false;
+    return TOPK_OK;
+}
+
 // True when p is host memory (pageable or pinned) rather than device or
 // managed memory.
 int is_host_pointer(const void* p, bool* host) {
@@ -173,13 +219,16 @@ bool early_start(Workspace* w, const void* in, size_t in_bytes, const void* a, s
 
 // Record that the last launch on w's stream does not release its successor
 // early: the next launch there must not start early, whatever it reads.
-void mark_not_released(Workspace* w) {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
+void mark_not_released_locked(Workspace* w) {
     w->stream_out[0] = nullptr;
     w->stream_out_bytes[0] = SIZE_MAX;
     w->stream_out[1] = nullptr;
     w->stream_out_bytes[1] = 0;
     t_last_early = 0;
+}
+void mark_not_released(Workspace* w) {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    mark_not_released_locked(w);
 }
 
 }  // namespace
@@ -194,31 +243,16 @@ int sort_withhold_option() { return g_sort_withhold.load(std::memory_order_relax
 void note_cuda_error(int err) { t_last_cuda_error = err; }
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
-int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status) {
-    Workspace* w = nullptr;
-    int rc = workspace(s, device, kI32CandOffset, 0, 0, &w);
-    if (rc != TOPK_OK) return rc;
-    {
-        std::lock_guard<std::mutex> lock(g_ws_mutex);
-        rc = grow(&w->kv, &w->kv_bytes, bytes);
-    }
-    if (rc != TOPK_OK) return rc;
-    mark_not_released(w);
-    *scratch = w->kv;
-    *status = reinterpret_cast<unsigned*>(static_cast<char*>(w->ctrl_cand) + kI32StatusOffset);
-    return TOPK_OK;
-}
-int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch) {
+int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* out) {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     Workspace& w = g_ws[{device, reinterpret_cast<uintptr_t>(s)}];
-    if (w.kv_count_bytes < bytes) {
-        const int rc = grow(&w.kv_count, &w.kv_count_bytes, bytes);
-        if (rc != TOPK_OK) return rc;
-        const cudaError_t e = cudaMemsetAsync(w.kv_count, 0, bytes, s);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
-    *counters = static_cast<unsigned*>(w.kv_count);
-    *epoch = w.kv_epoch++;
+    const int rc = grow_kv(w, s, scratch_bytes);
+    if (rc != TOPK_OK) return rc;
+    mark_not_released_locked(&w);
+    out->scratch = w.kv;
+    out->status = static_cast<unsigned*>(w.kv_state);
+    out->counters = out->status + kKvStatusWords;
+    out->epoch = w.kv_epoch++;
     return TOPK_OK;
 }
 int device_pointer(const void* p) {
@@ -578,12 +612,13 @@ int topk_check_stream(struct CUstream_st* stream) {
     if (e != cudaSuccess) return cuda_fail(e);
     e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e);
-    void* words[2] = {nullptr, nullptr};
+    void* words[3] = {nullptr, nullptr, nullptr};
     {
         std::lock_guard<std::mutex> lock(g_ws_mutex);
         auto it = g_ws.find({device, reinterpret_cast<uintptr_t>(s)});
         if (it != g_ws.end() && it->second.ctrl_cand)
             words[0] = static_cast<char*>(it->second.ctrl_cand) + topk::kI32StatusOffset;
+        if (it != g_ws.end()) words[2] = it->second.kv_state;
     }
     if (void* na = topk::noalloc_scratch_if_ready(device)) words[1] = static_cast<char*>(na) + topk::kI32StatusOffset;
     int rc = TOPK_OK;
@@ -664,8 +699,10 @@ int topk_release_workspace(void) {
     for (auto& kv : g_ws) {
         Workspace& w = kv.second;
         cudaSetDevice(kv.first.first);
-        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk, w.kv, w.kv_count})
+        for (void* p : {w.ctrl_cand, w.stage_in, w.stage_out, w.items, w.sort, w.bigk, w.kv, w.kv_state})
             if (p && cudaFree(p) != cudaSuccess) rc = TOPK_ERR_CUDA;
+        for (void* p : w.kv_kept)
+            if (cudaFree(p) != cudaSuccess) rc = TOPK_ERR_CUDA;
     }
     g_ws.clear();
     if (prev >= 0) cudaSetDevice(prev);

@@ -55,13 +55,22 @@ struct KvRows {
     __device__ T* row(int b, int h) const { return data + b * seq + h * head; }
 };
 
-// Of the C ABI layer (topk_api.cu): `bytes` bytes of the stream's scratch (no
-// contents to rely on) and its status word, with the record that the call
-// after this one must not start early.  Returns a topk_status.
-int kv_scratch(int device, cudaStream_t s, size_t bytes, void** scratch, unsigned** status);
-// `bytes` bytes that are zero before the first call on the stream, and a
-// number that counts the calls.
-int kv_counters(int device, cudaStream_t s, size_t bytes, unsigned** counters, unsigned* epoch);
+// counters: kKvCounters words, in two halves that calls use in turn by their
+// epoch; a call finds its half zero and leaves it zero.
+constexpr int kKvCounters = 1536;  // three for each of at most 256 blocks
+constexpr int kKvStatusWords = 32;
+constexpr int kKvStateWords = kKvStatusWords + kKvCounters;
+
+// What a call has of its stream (topk_api.cu).
+struct KvState {
+    void* scratch;       // no contents to rely on
+    unsigned* status;    // sticky; topk_check_stream reads it
+    unsigned* counters;
+    unsigned epoch;      // counts the calls
+};
+// At least scratch_bytes of it, 256-byte aligned, with the record that the
+// call after this one must not start early.  Returns a topk_status.
+int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* state);
 // TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
 int device_pointer(const void* p);
 // Counts n kernel launches.
@@ -71,7 +80,6 @@ cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k
                              const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
                              KvRows<float> weight, KvRows<int> pos, const int* next_pos);
 
-// scratch: kv_attend_scratch(...) bytes, 256-byte aligned, no contents needed.
 struct KvAttend {
     const uint16_t* q;
     long long qs[2];  // elements between sequences, query heads
@@ -83,11 +91,8 @@ struct KvAttend {
     KvRows<float> weight_out;
 };
 size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a);
-// counters: kKvCounters words, in two halves that calls use in turn by their
-// epoch; a call finds its half zero and leaves it zero.
-constexpr int kKvCounters = 1536;  // three for each of at most 256 blocks
-cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, void* scratch,
-                             unsigned* counters, unsigned epoch, unsigned* status, int* launches);
+cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, const KvState& state,
+                             int* launches);
 
 struct KvEvict {
     KvRows<const float> weight;
@@ -99,7 +104,7 @@ struct KvEvict {
     int* lens_out;
 };
 size_t kv_evict_scratch(const KvCache& c, const KvEvict& e);
-cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
-                            unsigned* counters, unsigned epoch, int* launches);
+cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, const KvState& state,
+                            int* launches);
 
 }  // namespace topk

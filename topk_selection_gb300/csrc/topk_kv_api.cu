@@ -166,14 +166,11 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
     a.lse = lse;
     a.weight = rows_of<const float>(weight);
     a.weight_out = rows_of<float>(weight_out);
-    void* scratch = nullptr;
-    unsigned* status = nullptr;
-    unsigned *counters = nullptr, epoch = 0;
-    rc = topk::kv_scratch(device, s, topk::kv_attend_scratch(device, c, a), &scratch, &status);
-    if (rc == TOPK_OK) rc = topk::kv_counters(device, s, topk::kKvCounters * sizeof(unsigned), &counters, &epoch);
+    topk::KvState state;
+    rc = topk::kv_state(device, s, topk::kv_attend_scratch(device, c, a), &state);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    e = topk::kv_attend_launch(device, s, c, a, scratch, counters, epoch, status, &launches);
+    e = topk::kv_attend_launch(device, s, c, a, state, &launches);
     topk::note_launches(launches);
     return e == cudaSuccess ? TOPK_OK : cuda_fail(e);
 }
@@ -213,14 +210,11 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
     e.weight_out = rows_of<float>(weight_out);
     e.pos_out = rows_of<int>(pos_out);
     e.lens_out = lens_out;
-    void* scratch = nullptr;
-    unsigned* status = nullptr;
-    unsigned *counters = nullptr, epoch = 0;
-    rc = topk::kv_scratch(device, s, topk::kv_evict_scratch(c, e), &scratch, &status);
-    if (rc == TOPK_OK) rc = topk::kv_counters(device, s, topk::kKvCounters * sizeof(unsigned), &counters, &epoch);
+    topk::KvState state;
+    rc = topk::kv_state(device, s, topk::kv_evict_scratch(c, e), &state);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    err = topk::kv_evict_launch(device, s, c, e, scratch, counters, epoch, &launches);
+    err = topk::kv_evict_launch(device, s, c, e, state, &launches);
     topk::note_launches(launches);
     return err == cudaSuccess ? TOPK_OK : cuda_fail(err);
 }

@@ -1207,12 +1207,12 @@ size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a) {
     return make_plan(device, c, a, nullptr).bytes;
 }
 
-cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, void* scratch,
-                             unsigned* counters, unsigned epoch, unsigned* status, int* launches) {
-    Plan plan = make_plan(device, c, a, scratch);
-    plan.args.status = status;
-    plan.args.done = counters + (epoch & 1) * (kKvCounters / 2);
-    plan.args.clear = counters + (~epoch & 1) * (kKvCounters / 2);
+cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, const KvState& state,
+                             int* launches) {
+    Plan plan = make_plan(device, c, a, state.scratch);
+    plan.args.status = state.status;
+    plan.args.done = state.counters + (state.epoch & 1) * (kKvCounters / 2);
+    plan.args.clear = state.counters + (~state.epoch & 1) * (kKvCounters / 2);
     const int gp = group_part(c, a);
     CUtensorMap maps[3];
     const cuuint64_t pool[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};

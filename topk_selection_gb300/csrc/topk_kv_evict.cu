@@ -527,16 +527,16 @@ size_t kv_evict_scratch(const KvCache& c, const KvEvict& e) {
     return 4 * (c.seqs + rows + 2 * rows * room_of(c, e));
 }
 
-cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, void* scratch,
-                            unsigned* counters, unsigned epoch, int* launches) {
+cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, const KvState& state,
+                            int* launches) {
     const int rows = c.seqs * c.heads;
     EvictArgs a = {c, e};
     a.room = room_of(c, e);
-    a.lens = static_cast<int*>(scratch);
+    a.lens = static_cast<int*>(state.scratch);
     a.moves = a.lens + c.seqs;
     a.holes = a.moves + rows;
     a.movers = a.holes + (size_t)rows * a.room;
-    a.ticket = counters + (epoch & 1) * (kKvCounters / 2);
+    a.ticket = state.counters + (state.epoch & 1) * (kKvCounters / 2);
     a.fused = a.room <= kFused;
     a.shift = 0;
     while ((1 << a.shift) < c.dim / 8) ++a.shift;
