@@ -265,7 +265,9 @@ int topk_reduce_f32(const float* in, size_t n, int op, double* out, struct CUstr
  * captured call was given lives until topk_release_workspace(), whatever
  * larger calls follow on the stream.  It is the stream's all the same: graphs
  * captured on one stream, and calls on that stream, have to run one after
- * another, on whichever stream the graphs are launched.  Nothing here uses
+ * another, on whichever stream the graphs are launched.  Host threads may
+ * call them on one stream at the same time: one call's launches are not
+ * parted by another's.  Nothing here uses
  * atomics on results: equal inputs give equal outputs, bit for bit, on the
  * same device.
  */

@@ -153,3 +153,36 @@ def test_a_capture_that_would_allocate_is_refused(tk):
         tk.kv_attend(big["q"], big["k"], big["v"], big["table"], big["lens"], weight=big["weight"], weight_out=w_out)
     s.synchronize()
     tk.check_stream(s)
+
+
+def test_host_threads_on_one_stream(tk):
+    """Two threads whose calls meet on one stream, one with small and growing caches: each gets its own results."""
+    import threading
+
+    s = torch.cuda.Stream()
+    cases = [[decoder(2, 500, 2, 4, 64, seed=50), decoder(3, 900, 2, 4, 64, seed=51), decoder(6, 4000, 2, 4, 64, seed=52)],
+             [decoder(4, 1500, 4, 2, 128, seed=53)]]
+    want = [[[t.clone() for t in attend_and_evict(tk, c, c["k"].clone(), c["v"].clone())] for c in cs] for cs in cases]
+    torch.cuda.synchronize()
+    failures = []
+
+    def work(which):
+        try:
+            with torch.cuda.stream(s):
+                for round_ in range(40):
+                    at = round_ * len(cases[which]) // 40
+                    c = cases[which][at]
+                    got = attend_and_evict(tk, c, c["k"].clone(), c["v"].clone())
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[which][at])):
+                        failures.append((which, round_))
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            failures.append((which, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    s.synchronize()
+    tk.check_stream(s)
+    assert failures == []

@@ -80,6 +80,7 @@ struct Workspace {
     std::vector<void*> kv_kept; // outgrown scratch that captured calls hold
     void* kv_state = nullptr;   // their status word and counters (zero between calls); never moves
     unsigned kv_epoch = 0;      // calls so far
+    std::mutex kv_turn;         // held from a call's look at the above to its last launch
 };
 
 std::mutex g_ws_mutex;
@@ -219,16 +220,13 @@ bool early_start(Workspace* w, const void* in, size_t in_bytes, const void* a, s
 
 // Record that the last launch on w's stream does not release its successor
 // early: the next launch there must not start early, whatever it reads.
-void mark_not_released_locked(Workspace* w) {
+void mark_not_released(Workspace* w) {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
     w->stream_out[0] = nullptr;
     w->stream_out_bytes[0] = SIZE_MAX;
     w->stream_out[1] = nullptr;
     w->stream_out_bytes[1] = 0;
     t_last_early = 0;
-}
-void mark_not_released(Workspace* w) {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    mark_not_released_locked(w);
 }
 
 }  // namespace
@@ -244,15 +242,19 @@ void note_cuda_error(int err) { t_last_cuda_error = err; }
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
 int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* out) {
+    Workspace* w = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_ws_mutex);
+        w = &g_ws[{device, reinterpret_cast<uintptr_t>(s)}];
+    }
+    out->turn = std::unique_lock<std::mutex>(w->kv_turn);  // before the lock below: launches are not made under that one
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace& w = g_ws[{device, reinterpret_cast<uintptr_t>(s)}];
-    const int rc = grow_kv(w, s, scratch_bytes);
+    const int rc = grow_kv(*w, s, scratch_bytes);
     if (rc != TOPK_OK) return rc;
-    mark_not_released_locked(&w);
-    out->scratch = w.kv;
-    out->status = static_cast<unsigned*>(w.kv_state);
+    out->scratch = w->kv;
+    out->status = static_cast<unsigned*>(w->kv_state);
     out->counters = out->status + kKvStatusWords;
-    out->epoch = w.kv_epoch++;
+    out->epoch = w->kv_epoch++;
     return TOPK_OK;
 }
 int device_pointer(const void* p) {

@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "topk_internal.h"
 
@@ -67,9 +68,12 @@ struct KvState {
     unsigned* status;    // sticky; topk_check_stream reads it
     unsigned* counters;
     unsigned epoch;      // counts the calls
+    // Other host threads' calls on the stream wait until this one has made its
+    // launches: they share the scratch, which another's launch between two of
+    // one call's would overwrite.
+    std::unique_lock<std::mutex> turn;
 };
-// At least scratch_bytes of it, 256-byte aligned, with the record that the
-// call after this one must not start early.  Returns a topk_status.
+// At least scratch_bytes of it, 256-byte aligned.  Returns a topk_status.
 int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* state);
 // TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
 int device_pointer(const void* p);

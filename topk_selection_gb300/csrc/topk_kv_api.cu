@@ -122,10 +122,10 @@ int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const i
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return cuda_fail(e);
-    topk::note_unreleased_launch(device, s);
     const long long ks[2] = {k_new_stride[0], k_new_stride[1]}, vs[2] = {v_new_stride[0], v_new_stride[1]};
     e = topk::kv_append_launch(s, c, static_cast<const uint16_t*>(k_new), ks, static_cast<const uint16_t*>(v_new), vs,
                                tokens, starts, rows_of<float>(weight), rows_of<int>(pos), next_pos);
+    topk::note_unreleased_launch(device, s);  // behind the launch: another thread's may have come between
     if (e != cudaSuccess) return cuda_fail(e);
     topk::note_launch();
     return TOPK_OK;
@@ -171,6 +171,7 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
     if (rc != TOPK_OK) return rc;
     int launches = 0;
     e = topk::kv_attend_launch(device, s, c, a, state, &launches);
+    topk::note_unreleased_launch(device, s);
     topk::note_launches(launches);
     return e == cudaSuccess ? TOPK_OK : cuda_fail(e);
 }
@@ -215,6 +216,7 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
     if (rc != TOPK_OK) return rc;
     int launches = 0;
     err = topk::kv_evict_launch(device, s, c, e, state, &launches);
+    topk::note_unreleased_launch(device, s);
     topk::note_launches(launches);
     return err == cudaSuccess ? TOPK_OK : cuda_fail(err);
 }
