@@ -186,3 +186,37 @@ def test_host_threads_on_one_stream(tk):
     s.synchronize()
     tk.check_stream(s)
     assert failures == []
+
+
+def test_outputs_belong_to_the_stream_of_the_call(tk):
+    """What kv_attend allocates is its stream's memory, however the stream is given, so that the allocator hands it on
+    only behind the call."""
+    c = decoder(2, 300, 2, 2, 64)
+
+    def owner(t):
+        for segment in torch.cuda.memory_snapshot():
+            if segment["address"] <= t.data_ptr() < segment["address"] + segment["total_size"]:
+                return segment["stream"]
+        raise AssertionError("not the allocator's")
+
+    args = c["q"], c["k"], c["v"], c["table"], c["lens"]
+    torch.cuda.synchronize()
+    want, want_lse = tk.kv_attend(*args)
+    assert owner(want) == torch.cuda.current_stream().cuda_stream
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for given in (s, s.cuda_stream):
+        before = torch.cuda.current_stream()
+        out, lse = tk.kv_attend(*args, stream=given)
+        assert torch.cuda.current_stream() == before
+        assert owner(out) == s.cuda_stream and owner(lse) == s.cuda_stream
+        s.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    with torch.cuda.stream(s):
+        out, _ = tk.kv_attend(*args, stream=0)
+        assert owner(out) == 0
+        other, _ = tk.kv_attend(*args, stream=1)  # the legacy stream's other handle
+        assert owner(other) == 0
+        assert torch.cuda.current_stream() == s
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(other, want)

@@ -430,7 +430,8 @@ def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, tab
     q is [seqs, q_heads, dim], q_heads a multiple of the cache's heads; scale
     defaults to dim ** -0.5.  With weight (float32 [seqs, heads, slots]), the
     attention that each slot gets, summed over its query heads, is added to it
-    and written to weight_out (default: weight itself)."""
+    and written to weight_out (default: weight itself).  out and lse belong to
+    the stream of the call, as if made with it as the current one."""
     got = _kv.attend(q, k_pages, v_pages, table, lens, scale, weight, weight_out, out, lse, _kv_stream(stream))
     if type(got) is int:
         raise TopKError(got, "topk_kv_attend")

@@ -13,6 +13,7 @@
 
 #include <exception>
 #include <initializer_list>
+#include <optional>
 #include <sstream>
 
 #include "../../include/topk.h"
@@ -133,13 +134,27 @@ int integer(PyObject* o) {
     return v > INT32_MAX ? INT32_MAX : v < INT32_MIN ? INT32_MIN : (int)v;
 }
 
-// The stream of a call: a handle, or None for the current one.
-CUstream_st* stream_of(PyObject* o, const Cache& c) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(c.device.index()).stream();
-    void* s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw Raised();
-    return static_cast<CUstream_st*>(s);
-}
+// The stream of a call: a handle, or None for the current one.  It is the
+// current one while this lives, so that memory is allocated for the stream
+// that uses it.
+struct Stream {
+    CUstream_st* handle;
+    std::optional<c10::cuda::CUDAStreamGuard> on;
+
+    Stream(PyObject* o, const Cache& c) {
+        const c10::DeviceIndex device = c.device.index();
+        if (o == Py_None) {
+            handle = c10::cuda::getCurrentCUDAStream(device).stream();
+            return;
+        }
+        handle = static_cast<CUstream_st*>(PyLong_AsVoidPtr(o));
+        if (!handle && PyErr_Occurred()) throw Raised();
+        // torch counts the legacy stream, by either of its handles, as its default one.
+        const bool legacy = !handle || handle == cudaStreamLegacy;
+        on.emplace(legacy ? c10::cuda::getDefaultCUDAStream(device)
+                          : c10::cuda::getStreamFromExternal(handle, device));
+    }
+};
 
 // Runs f with every exception turned into a Python one, after a check of the
 // number of arguments.
@@ -179,11 +194,11 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* starts = ints(a[6], "starts", c, (int64_t)c.c.seqs + 1);
         const topk_kv_rows weight = rows(a[7], "weight", at::kFloat, c), pos = rows(a[8], "pos", at::kInt, c);
         const int32_t* next_pos = ints(a[9], "next_pos", c, c.c.seqs);
-        CUstream_st* s = stream_of(a[10], c);
+        const Stream s(a[10], c);
         if (k.size(0) == 0) return PyLong_FromLong(TOPK_OK);
         return PyLong_FromLong(call(c, [&] {
             return g_append(&c.c, k.const_data_ptr(), ks, v.const_data_ptr(), vs, (int)k.size(0), starts, &weight,
-                            &pos, next_pos, s);
+                            &pos, next_pos, s.handle);
         }));
     });
 }
@@ -205,6 +220,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (a[6] == Py_None && a[7] != Py_None) raise(PyExc_ValueError, "weight_out needs weight");
         const topk_kv_rows weight = rows(a[6], "weight", at::kFloat, c);
         const topk_kv_rows weight_out = a[7] == Py_None ? weight : rows(a[7], "weight_out", at::kFloat, c);
+        const Stream s(a[10], c);
         const at::Tensor out = a[8] != Py_None
                                    ? tensor(a[8], "out", c.type, c.device, {c.c.seqs, q_heads, c.c.dim})
                                    : at::Tensor(at::detail::empty_cuda({c.c.seqs, q_heads, c.c.dim}, c.type, c.device,
@@ -214,10 +230,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                                                    c.device, std::nullopt));
         if (!out.is_contiguous() || !lse.is_contiguous())
             raise(PyExc_ValueError, "out and lse must be contiguous");
-        CUstream_st* s = stream_of(a[10], c);
         const int rc = call(c, [&] {
             return g_attend(&c.c, q.const_data_ptr(), qs, (int)q_heads, (float)scale, out.data_ptr(),
-                            static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s);
+                            static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s.handle);
         });
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
         PyObject* pair = PyTuple_New(2);
@@ -239,9 +254,9 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const topk_kv_rows weight_out = rows(a[10], "weight_out", at::kFloat, c),
                            pos_out = rows(a[11], "pos_out", at::kInt, c);
         int32_t* lens_out = const_cast<int32_t*>(ints(a[12], "lens_out", c, c.c.seqs));
-        CUstream_st* s = stream_of(a[13], c);
+        const Stream s(a[13], c);
         return PyLong_FromLong(call(c, [&] {
-            return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out, s);
+            return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out, s.handle);
         }));
     });
 }
