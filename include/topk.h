@@ -482,7 +482,19 @@ enum topk_option {
      * up, and topk_check_stream reports TOPK_ERR_DEVICE_TIMEOUT; the output
      * is then wrong but every write stays inside it.  Only to exercise that
      * report, with TOPK_OPT_SORT_SPINS lowered so that the wait is short. */
-    TOPK_OPT_SORT_WITHHOLD = 8
+    TOPK_OPT_SORT_WITHHOLD = 8,
+    /* Tries of one wait before a block of topk_kv_attend gives up (0 restores
+     * the default, 2^22).  A block that gives up leaves its rows' out, lse
+     * and weights wrong (it writes nothing outside them), and
+     * topk_check_stream then reports TOPK_ERR_DEVICE_TIMEOUT.  Lower it only
+     * to exercise that report. */
+    TOPK_OPT_KV_SPINS = 9,
+    /* What the first block of topk_kv_attend withholds, so that waits on it
+     * run out: 1 the keys that it copies, 2 the values, 3 the word that its
+     * first two products with values are done (0 restores the default).  Only to
+     * exercise that report, with TOPK_OPT_KV_SPINS lowered so that the waits
+     * are short. */
+    TOPK_OPT_KV_WITHHOLD = 10
 };
 
 /* Set a process-wide option; takes effect for calls made afterwards.

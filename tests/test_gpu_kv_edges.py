@@ -220,3 +220,55 @@ def test_outputs_belong_to_the_stream_of_the_call(tk):
         assert torch.cuda.current_stream() == s
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(other, want)
+
+
+@pytest.fixture
+def withhold(tk):
+    """Makes the first block of kv_attend keep something back, with short waits; cleared afterwards."""
+    def put(what):
+        tk.set_option(tk.OPT_KV_SPINS, 200 if what else 0)
+        tk.set_option(tk.OPT_KV_WITHHOLD, what)
+
+    yield put
+    put(0)
+
+
+SHORT, RAGGED, LONG = (1, 300, 2, 4, 64), (20, 700, 4, 8, 128), (2, 40000, 2, 12, 64)
+WIDE = (3, 900, 2, 8, 256)
+
+
+@pytest.mark.parametrize("what", [1, 2, 3])
+@pytest.mark.parametrize("shape", [SHORT, RAGGED, LONG, WIDE])
+def test_waits_of_attend_run_out(tk, withhold, shape, what):
+    """Nothing hangs, the status says so, and nothing is written outside the outputs."""
+    c = decoder(*shape)
+    k0, v0 = c["k"].clone(), c["v"].clone()
+    args = c["q"], c["k"], c["v"], c["table"], c["lens"]
+    seqs, heads, cap = c["weight"].shape
+    want = tk.kv_attend(*args, weight=c["weight"], weight_out=torch.zeros_like(c["weight"]))
+    tk.check_stream()
+    rows, dim = c["q"].shape[0] * c["q"].shape[1], c["q"].shape[2]
+    s = torch.cuda.Stream()
+    out, lse = torch.full((rows + 16, dim), 7.0, dtype=c["q"].dtype, device="cuda"), torch.full((rows + 16,), 7.0).cuda()
+    w = torch.full((seqs, heads, cap + 64), 7.0, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    withhold(what)
+    with torch.cuda.stream(s):
+        tk.kv_attend(*args, weight=c["weight"], weight_out=w[:, :, :cap], out=out[:rows].view_as(c["q"]),
+                     lse=lse[:rows].view(c["q"].shape[:2]))
+    with pytest.raises(tk.TopKError) as err:
+        tk.check_stream(s)
+    assert err.value.status == 5  # TOPK_ERR_DEVICE_TIMEOUT
+    tk.check_stream(s)  # told once
+    withhold(0)
+    assert torch.all(out[rows:] == 7.0) and torch.all(lse[rows:] == 7.0) and torch.all(w[:, :, cap:] == 7.0)
+    assert torch.equal(c["k"], k0) and torch.equal(c["v"], v0)
+    assert torch.equal(c["weight"], decoder(*shape)["weight"])
+    got = tk.kv_attend(*args, weight=c["weight"], weight_out=torch.zeros_like(c["weight"]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_options_of_the_waits(tk):
+    for option, bad in ((tk.OPT_KV_SPINS, -1), (tk.OPT_KV_WITHHOLD, 4), (tk.OPT_KV_WITHHOLD, -1)):
+        with pytest.raises(tk.TopKError):
+            tk.set_option(option, bad)

@@ -145,6 +145,8 @@ OPT_NO_EARLY_START = 5
 OPT_FAULT_ALLOC = 6
 OPT_SORT_SPINS = 7
 OPT_SORT_WITHHOLD = 8
+OPT_KV_SPINS = 9
+OPT_KV_WITHHOLD = 10
 
 
 def set_option(option: int, value: int) -> None:

@@ -28,6 +28,8 @@ std::atomic<int> g_stream_static{0};
 std::atomic<int> g_no_early{0};
 std::atomic<int> g_sort_spins{0};
 std::atomic<int> g_sort_withhold{0};
+std::atomic<int> g_kv_spins{0};
+std::atomic<int> g_kv_withhold{0};
 std::atomic<int> g_fault_alloc{-1};  // -1: not read yet from TOPK_FAULT_ALLOC
 
 // Fault injection on the host: when set (environment TOPK_FAULT_ALLOC=1 at
@@ -238,6 +240,8 @@ int radix_sample_rank_option() { return g_radix_sample_rank.load(std::memory_ord
 int stream_static_option() { return g_stream_static.load(std::memory_order_relaxed); }
 int sort_spins_option() { return g_sort_spins.load(std::memory_order_relaxed); }
 int sort_withhold_option() { return g_sort_withhold.load(std::memory_order_relaxed); }
+int kv_spins_option() { return g_kv_spins.load(std::memory_order_relaxed); }
+int kv_withhold_option() { return g_kv_withhold.load(std::memory_order_relaxed); }
 void note_cuda_error(int err) { t_last_cuda_error = err; }
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
@@ -663,6 +667,14 @@ int topk_set_option(int option, int value) {
         case TOPK_OPT_SORT_WITHHOLD:
             if (value != 0 && value != 1) return TOPK_ERR_INVALID_ARG;
             g_sort_withhold.store(value, std::memory_order_relaxed);
+            return TOPK_OK;
+        case TOPK_OPT_KV_SPINS:
+            if (value < 0) return TOPK_ERR_INVALID_ARG;
+            g_kv_spins.store(value, std::memory_order_relaxed);
+            return TOPK_OK;
+        case TOPK_OPT_KV_WITHHOLD:
+            if (value < 0 || value > 3) return TOPK_ERR_INVALID_ARG;
+            g_kv_withhold.store(value, std::memory_order_relaxed);
             return TOPK_OK;
         case TOPK_OPT_FAULT_ALLOC:
             if (value != 0 && value != 1) return TOPK_ERR_INVALID_ARG;

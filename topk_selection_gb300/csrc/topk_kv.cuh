@@ -75,6 +75,9 @@ struct KvState {
 };
 // At least scratch_bytes of it, 256-byte aligned.  Returns a topk_status.
 int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* state);
+// Test options TOPK_OPT_KV_SPINS and TOPK_OPT_KV_WITHHOLD (topk_api.cu).
+int kv_spins_option();
+int kv_withhold_option();
 // TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
 int device_pointer(const void* p);
 // Counts n kernel launches.

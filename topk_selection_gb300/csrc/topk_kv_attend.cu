@@ -91,7 +91,10 @@ struct AttendArgs {
     float* p;         // [tile][GP][slot]: whole sectors from a warp
     float* tile_m;    // [tile][GP]: the reference of each tile's p
     unsigned* status;
+    int spins;        // tries of a wait before it gives up, 0 for kWaitSpins (TOPK_OPT_KV_SPINS)
+    int withhold;     // what the first block withholds (TOPK_OPT_KV_WITHHOLD)
 };
+enum Withhold { kKeys = 1, kValues = 2, kProducts = 3 };
 
 // The code of a launch is fetched anew when the cache it streams has pushed
 // it out of L2, and most of it runs once a row or once a launch: that part is
@@ -236,12 +239,16 @@ struct Shape {
 };
 
 // The bounded wait's slow side: gives up after kWaitSpins tries, or once
-// another wait of the block has.
+// another wait of the block has and *gave_up is 1.  Fewer tries, for tests, are
+// in *gave_up as a negative number: as an argument they cost 3% of a case whose
+// softmax just keeps up (12 heads on one, 32.9 us instead of 31.8).
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, unsigned* status) {
 #pragma unroll 1
     for (int i = 0; i < kWaitSpins; ++i) {
         if (mbar_try(bar, parity)) return true;
-        if (*gave_up) return false;
+        const int g = *gave_up;
+        if (g > 0) return false;
+        if (g < 0 && i >= -g) break;
     }
     *gave_up = 1;
     atomicOr(status, kStatusWaitTimeout);
@@ -486,6 +493,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
     __shared__ float told_m[4][GP], told_l[4][4][GP];      // what one group tells the other at a row's end
     __shared__ float2 joined[2][GP];
     __shared__ unsigned arrived[2];
+    __shared__ int issued[3];  // parts of keys and of values that were asked for, and queries
     __shared__ volatile int gave_up;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -497,7 +505,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
             mbar_init(&bars[i], by_threads ? kSoftmax : 1);
         }
         mbar_init_fence();
-        gave_up = 0;
+        gave_up = -p.spins;
     }
     if (warp == kCopyK && lane == 0) {
         prefetch_map(&map_k);
@@ -528,6 +536,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         return n;
     };
 
+    auto withholds = [&](int what) { return p.withhold == what && blockIdx.x == 0; };
     if (warp == kCopyK || warp == kCopyV) {
         // Copies into the rings.  One warp has the keys, one the values: a
         // copy takes its issuer some 50 clocks, and a tile of small pages is
@@ -567,7 +576,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         page = count > 0 ? fetch(y, true) : 0;
         int in_now = in;
 #pragma unroll 1
-        for (int it = 0; it < count; ++it) {
+        for (int it = 0; it < count && !withholds(keys ? kKeys : kValues); ++it) {
             if (it + 1 < count) {
                 y.next(p);
                 page_next = fetch(y, y.t == 0);
@@ -622,13 +631,9 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
             page = page_next;
             in_now = in;
         }
-        __syncwarp();
-        if (gave_up) {  // wait for this warp's copies in flight, so that none lands after the block's end
-#pragma unroll 1
-            for (int i = max(0, items - S::kRing); i < items; ++i)
-                mbar_wait(&bars[full0 + i % S::kRing], (i / S::kRing) & 1);
-#pragma unroll 1
-            for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
+        if (lane == 0) {
+            issued[keys ? 0 : 1] = items;
+            if (keys) issued[2] = q_loads;
         }
     } else if (warp == kMmaS) {
         if (lane == 0) {  // S = K Q^T
@@ -669,12 +674,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 x.t += n - 1;
                 x.next(p);
             }
-            if (gave_up) {  // wait for the products in flight
-                mma_commit(bar0 + S::kDrain * 8);
-                mbar_wait(&bars[S::kDrain], 0);
-            }
         }
-        __syncwarp();
     } else if (warp == kMmaO) {
         if (lane == 0) {  // O += V^T P^T
             const uint32_t id = mma_idesc(p.c.bf16, S::kM, S::kPCols, true);
@@ -708,17 +708,12 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                         get.move(1);
                     }
                     if (!ok) break;
-                    mma_commit(bar0 + (S::kPFree + buf) * 8);
+                    if (it >= 2 || !withholds(kProducts)) mma_commit(bar0 + (S::kPFree + buf) * 8);
                 }
                 x.t += n - 1;
                 x.next(p);
             }
-            if (gave_up) {
-                mma_commit(bar0 + (S::kDrain + 1) * 8);
-                mbar_wait(&bars[S::kDrain + 1], 0);
-            }
         }
-        __syncwarp();
     } else {
         // Softmax.  The two groups of 128 threads take the tiles in turn, each
         // with its own buffers of S and P, reference, sum and O, so that one
@@ -990,7 +985,27 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
             x.next(p);
         }
     }
+    __syncwarp();
     __syncthreads();
+    if (gave_up > 0) {
+        // Every wait is over, so all warps see the same.  Copies and products
+        // in flight end before the block does and tensor memory is freed.
+        if (warp == kCopyK || warp == kCopyV) {
+            const bool keys = warp == kCopyK;
+            const int full0 = keys ? S::kFullK : S::kFullV, items = issued[keys ? 0 : 1], q_loads = keys ? issued[2] : 0;
+#pragma unroll 1
+            for (int i = max(0, items - S::kRing); i < items; ++i)
+                mbar_wait(&bars[full0 + i % S::kRing], (i / S::kRing) & 1);
+#pragma unroll 1
+            for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait(&bars[S::kQFull + (i & 1)], (i >> 1) & 1);
+        } else if ((warp == kMmaS || warp == kMmaO) && lane == 0) {
+            const int drain = S::kDrain + (warp == kMmaO);
+            mma_commit(bar0 + drain * 8);
+            mbar_wait(&bars[drain], 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == kMmaS) tmem_dealloc(tmem, S::kTmemCols);
     // What sequences without slots give.
@@ -1211,6 +1226,8 @@ cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const
                              int* launches) {
     Plan plan = make_plan(device, c, a, state.scratch);
     plan.args.status = state.status;
+    plan.args.spins = kv_spins_option();
+    plan.args.withhold = kv_withhold_option();
     plan.args.done = state.counters + (state.epoch & 1) * (kKvCounters / 2);
     plan.args.clear = state.counters + (~state.epoch & 1) * (kKvCounters / 2);
     const int gp = group_part(c, a);
