@@ -18,6 +18,19 @@ def tk():
     topk_selection_gb300.check_stream()
 
 
+@pytest.fixture(scope="module")
+def side():
+    """side(): a stream beside the current one, behind what that has been given; the same one throughout."""
+    s = torch.cuda.Stream()
+
+    def behind():
+        s.wait_stream(torch.cuda.current_stream())
+        return s
+
+    yield behind
+    s.synchronize()
+
+
 def fill(cache, b, slot, pool, head, value):
     """pool's vector of a slot that sequence b holds."""
     pool[cache.table[b, slot // cache.page], slot % cache.page, head] = value
@@ -92,11 +105,10 @@ def attend_and_evict(tk, c, k, v):
     return out, lse, w_out, w, p
 
 
-def test_graphs_outlive_larger_calls(tk):
+def test_graphs_outlive_larger_calls(tk, side):
     """One graph per batch size, captured on one stream from small to large: each goes on working, and no replay writes
     into what was allocated since."""
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
+    s = side()
     graphs = []
     with torch.cuda.stream(s):
         for seqs, n in ((1, 700), (3, 2100), (8, 6000), (8, 6100), (24, 9000)):
@@ -130,10 +142,11 @@ def test_graphs_outlive_larger_calls(tk):
     s.synchronize()
 
 
-def test_a_capture_that_would_allocate_is_refused(tk):
+def test_a_capture_that_would_allocate_is_refused(tk, side):
     """The status comes back, the capture goes on, and the same call works on the stream afterwards."""
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    tk.release_workspace()  # other tests' scratch would be large enough
+    s = side()
     c = decoder(2, 300, 2, 2, 64)
     big = decoder(20, 3000, 4, 8, 64)
     x = torch.zeros(4, device="cuda")
@@ -155,15 +168,14 @@ def test_a_capture_that_would_allocate_is_refused(tk):
     tk.check_stream(s)
 
 
-def test_host_threads_on_one_stream(tk):
+def test_host_threads_on_one_stream(tk, side):
     """Two threads whose calls meet on one stream, one with small and growing caches: each gets its own results."""
     import threading
 
-    s = torch.cuda.Stream()
     cases = [[decoder(2, 500, 2, 4, 64, seed=50), decoder(3, 900, 2, 4, 64, seed=51), decoder(6, 4000, 2, 4, 64, seed=52)],
              [decoder(4, 1500, 4, 2, 128, seed=53)]]
     want = [[[t.clone() for t in attend_and_evict(tk, c, c["k"].clone(), c["v"].clone())] for c in cs] for cs in cases]
-    torch.cuda.synchronize()
+    s = side()
     failures = []
 
     def work(which):
@@ -188,7 +200,7 @@ def test_host_threads_on_one_stream(tk):
     assert failures == []
 
 
-def test_outputs_belong_to_the_stream_of_the_call(tk):
+def test_outputs_belong_to_the_stream_of_the_call(tk, side):
     """What kv_attend allocates is its stream's memory, however the stream is given, so that the allocator hands it on
     only behind the call."""
     c = decoder(2, 300, 2, 2, 64)
@@ -203,8 +215,7 @@ def test_outputs_belong_to_the_stream_of_the_call(tk):
     torch.cuda.synchronize()
     want, want_lse = tk.kv_attend(*args)
     assert owner(want) == torch.cuda.current_stream().cuda_stream
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
+    s = side()
     for given in (s, s.cuda_stream):
         before = torch.cuda.current_stream()
         out, lse = tk.kv_attend(*args, stream=given)
@@ -239,7 +250,7 @@ WIDE = (3, 900, 2, 8, 256)
 
 @pytest.mark.parametrize("what", [1, 2, 3])
 @pytest.mark.parametrize("shape", [SHORT, RAGGED, LONG, WIDE])
-def test_waits_of_attend_run_out(tk, withhold, shape, what):
+def test_waits_of_attend_run_out(tk, side, withhold, shape, what):
     """Nothing hangs, the status says so, and nothing is written outside the outputs."""
     c = decoder(*shape)
     k0, v0 = c["k"].clone(), c["v"].clone()
@@ -248,10 +259,9 @@ def test_waits_of_attend_run_out(tk, withhold, shape, what):
     want = tk.kv_attend(*args, weight=c["weight"], weight_out=torch.zeros_like(c["weight"]))
     tk.check_stream()
     rows, dim = c["q"].shape[0] * c["q"].shape[1], c["q"].shape[2]
-    s = torch.cuda.Stream()
     out, lse = torch.full((rows + 16, dim), 7.0, dtype=c["q"].dtype, device="cuda"), torch.full((rows + 16,), 7.0).cuda()
     w = torch.full((seqs, heads, cap + 64), 7.0, device="cuda")
-    s.wait_stream(torch.cuda.current_stream())
+    s = side()
     withhold(what)
     with torch.cuda.stream(s):
         tk.kv_attend(*args, weight=c["weight"], weight_out=w[:, :, :cap], out=out[:rows].view_as(c["q"]),
@@ -272,3 +282,67 @@ def test_options_of_the_waits(tk):
     for option, bad in ((tk.OPT_KV_SPINS, -1), (tk.OPT_KV_WITHHOLD, 4), (tk.OPT_KV_WITHHOLD, -1)):
         with pytest.raises(tk.TopKError):
             tk.set_option(option, bad)
+
+
+def cut_short(tk, withhold, c, what=2):
+    withhold(what)
+    tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"], weight=c["weight"],
+                 weight_out=torch.zeros_like(c["weight"]))
+    withhold(0)
+
+
+@pytest.mark.parametrize("what", [1, 2, 3])
+@pytest.mark.parametrize("checked", [False, True])
+@pytest.mark.parametrize("order", ["l", "el", "sl", "ssl", "seel", "e", "se", "lel"])
+def test_calls_after_one_cut_short(tk, side, withhold, order, checked, what):
+    """Evictions (e), small attentions (s) and large ones (l) that come next on the stream are right, whether the
+    status was asked for or not."""
+    small, large = decoder(*SHORT, seed=60), decoder(*LONG, seed=61)
+    args = {kind: (c["q"], c["k"], c["v"], c["table"], c["lens"]) for kind, c in (("s", small), ("l", large))}
+
+    def run(kind):
+        if kind != "e":
+            return tk.kv_attend(*args[kind])
+        return tk.kv_evict(small["k"].clone(), small["v"].clone(), small["table"], small["lens"], small["weight"],
+                           small["pos"], small["lens"], 150, weight_out=torch.zeros_like(small["weight"]),
+                           pos_out=torch.zeros_like(small["pos"]), lens_out=torch.zeros_like(small["lens"]))
+
+    want = {kind: [t.clone() for t in run(kind)] for kind in "sle"}
+    s = side()
+    with torch.cuda.stream(s):
+        cut_short(tk, withhold, large, what)
+        if checked:
+            with pytest.raises(tk.TopKError):
+                tk.check_stream(s)
+        for kind in order:
+            assert all(torch.equal(a, b) for a, b in zip(run(kind), want[kind])), kind
+    if not checked:
+        with pytest.raises(tk.TopKError):
+            tk.check_stream(s)
+    tk.check_stream(s)
+
+
+@pytest.mark.parametrize("before", [0, 1])
+def test_graphs_after_a_call_cut_short(tk, side, withhold, before):
+    """A graph's call always has the same counters: once the status was asked for, its replays are right."""
+    c = decoder(*LONG)
+    want = [t.clone() for t in tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"])]
+    s = side()
+    with torch.cuda.stream(s):
+        tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"], weight=c["weight"].clone())
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"])
+        for _ in range(before):
+            tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"])
+        cut_short(tk, withhold, c)
+        with pytest.raises(tk.TopKError):
+            tk.check_stream(s)
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    s.synchronize()
+    tk.check_stream(s)

@@ -257,8 +257,10 @@ int kv_state(int device, cudaStream_t s, size_t scratch_bytes, KvState* out) {
     if (rc != TOPK_OK) return rc;
     out->scratch = w->kv;
     out->status = static_cast<unsigned*>(w->kv_state);
-    out->counters = out->status + kKvStatusWords;
-    out->epoch = w->kv_epoch++;
+    const unsigned half = w->kv_epoch++ & 1;
+    unsigned* counters = out->status + kKvStatusWords;
+    out->mine = counters + half * kKvHalf;
+    out->other = counters + (half ^ 1) * kKvHalf;
     return TOPK_OK;
 }
 int device_pointer(const void* p) {
@@ -635,7 +637,11 @@ int topk_check_stream(struct CUstream_st* stream) {
         if (e != cudaSuccess) return cuda_fail(e);
         if (v != 0) {
             rc = TOPK_ERR_DEVICE_TIMEOUT;
-            e = cudaMemset(w, 0, sizeof(v));
+            // With the key-value cache operators' word go the counters that a
+            // call cut short leaves, in stream order.
+            e = w == words[2] ? cudaMemsetAsync(w, 0, topk::kKvStateWords * sizeof(unsigned), s)
+                              : cudaMemset(w, 0, sizeof(v));
+            if (e == cudaSuccess && w == words[2]) e = cudaStreamSynchronize(s);
             if (e != cudaSuccess) return cuda_fail(e);
         }
     }

@@ -56,18 +56,26 @@ struct KvRows {
     __device__ T* row(int b, int h) const { return data + b * seq + h * head; }
 };
 
-// counters: kKvCounters words, in two halves that calls use in turn by their
-// epoch; a call finds its half zero and leaves it zero.
-constexpr int kKvCounters = 1536;  // three for each of at most 256 blocks
+// Counters, in two halves that calls use in turn by their epoch.  A call finds
+// its half zero and leaves it zero, and clears the other one, which a call
+// before it may have left otherwise if its waits gave up.  A graph's calls
+// always have the same half: topk_check_stream clears both when it reports.
+constexpr int kKvBlocks = 256;               // of an attend at most
+constexpr int kKvTicket = 3 * kKvBlocks;     // an evict's word, behind three of each block of an attend
+constexpr int kKvHalf = 3 * kKvBlocks + 32;
 constexpr int kKvStatusWords = 32;
-constexpr int kKvStateWords = kKvStatusWords + kKvCounters;
+constexpr int kKvStateWords = kKvStatusWords + 2 * kKvHalf;
+// The whole grid calls it.
+__device__ __forceinline__ void clear_half(unsigned* half) {
+    for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < kKvHalf; i += gridDim.x * blockDim.x) half[i] = 0;
+}
 
 // What a call has of its stream (topk_api.cu).
 struct KvState {
     void* scratch;       // no contents to rely on
     unsigned* status;    // sticky; topk_check_stream reads it
-    unsigned* counters;
-    unsigned epoch;      // counts the calls
+    unsigned* mine;      // the call's half of the counters
+    unsigned* other;
     // Other host threads' calls on the stream wait until this one has made its
     // launches: they share the scratch, which another's launch between two of
     // one call's would overwrite.

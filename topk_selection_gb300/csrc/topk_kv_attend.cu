@@ -73,7 +73,7 @@ __device__ __forceinline__ uint16_t from_float(float x, int bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
 }
 
-static_assert(kKvCounters / 6 <= kJoin * kJoin, "a row's pieces are joined in two steps");
+static_assert(kKvBlocks <= kJoin * kJoin, "a row's pieces are joined in two steps");
 
 struct AttendArgs {
     KvCache c;
@@ -86,7 +86,7 @@ struct AttendArgs {
     float2* part_ml;  // [2 * blocks][GP]: its reference and sum
     float2* row_ml;   // [seqs * rows][GP]: the same of finished rows
     unsigned* done;   // [3 * blocks]: shares that have arrived, zero before and after
-    unsigned* clear;  // the next call's, cleared here in case a call before was cut short
+    unsigned* clear;  // the other half of the counters
     int* walk;        // [blocks][Walk::kWords]: where each block begins, when weights are wanted
     float* p;         // [tile][GP][slot]: whole sectors from a warp
     float* tile_m;    // [tile][GP]: the reference of each tile's p
@@ -513,7 +513,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
     }
     if (warp == kCopyV && lane == 0) prefetch_map(&map_v);
     grid_dependency_wait();
-    if (tid < 3) p.clear[blockIdx.x * 3 + tid] = 0;
+    clear_half(p.clear);
     if (warp == kMmaS) tmem_alloc(&tmem_at, S::kTmemCols);
     launch_dependents();  // the weights' launch waits for this one's end before it reads anything of it
     Walk w = find_range<kThreads>(p, scan);
@@ -1158,7 +1158,7 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
     const size_t rows = (size_t)c.seqs * p.rows, tiles = rows * ((c.capacity() + kTile - 1) / kTile);
     plan.blocks = sm_count(device);
     if ((size_t)plan.blocks > tiles) plan.blocks = (int)tiles;
-    if (plan.blocks > kKvCounters / 6) plan.blocks = kKvCounters / 6;
+    if (plan.blocks > kKvBlocks) plan.blocks = kKvBlocks;
     char* at = static_cast<char*>(scratch);
     size_t bytes = 0;
     auto take = [&](size_t n) {
@@ -1228,8 +1228,8 @@ cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const
     plan.args.status = state.status;
     plan.args.spins = kv_spins_option();
     plan.args.withhold = kv_withhold_option();
-    plan.args.done = state.counters + (state.epoch & 1) * (kKvCounters / 2);
-    plan.args.clear = state.counters + (~state.epoch & 1) * (kKvCounters / 2);
+    plan.args.done = state.mine;
+    plan.args.clear = state.other;
     const int gp = group_part(c, a);
     CUtensorMap maps[3];
     const cuuint64_t pool[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};

@@ -56,6 +56,7 @@ struct EvictArgs {
     int part;     // slots a block of the first has room for in shared memory
     int fused;    // whether the first launch makes the moves too
     unsigned* ticket;  // then: its blocks that are done, zero before and after
+    unsigned* clear;   // the other half of the counters
 };
 
 // Order-preserving key: protected above NaN above every number, -0 equal to
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     const int row = blockIdx.x / blocks, b = row / a.c.heads, h = row % a.c.heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
+    clear_half(a.clear);
     const int n = a.c.len(b), budget = a.e.budget;
     const float* w = a.e.weight.row(b, h);
     const int* pos = a.e.pos.row(b, h);
@@ -536,7 +538,8 @@ cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const 
     a.moves = a.lens + c.seqs;
     a.holes = a.moves + rows;
     a.movers = a.holes + (size_t)rows * a.room;
-    a.ticket = state.counters + (state.epoch & 1) * (kKvCounters / 2);
+    a.ticket = state.mine + kKvTicket;
+    a.clear = state.other;
     a.fused = a.room <= kFused;
     a.shift = 0;
     while ((1 << a.shift) < c.dim / 8) ++a.shift;
