@@ -36,6 +36,19 @@ def fill(cache, b, slot, pool, head, value):
     pool[cache.table[b, slot // cache.page], slot % cache.page, head] = value
 
 
+def scores_cache(scores, dim, dtype, heads=1, page=16, seed=30):
+    """One sequence whose slots' scores are `scores` for a query of ones at
+    element 0 and scale 1: keys hold them there, and zeros elsewhere."""
+    cache = _kv.Cache([len(scores)], heads, dim, page, dtype, "head", seed=seed)
+    for i, s in enumerate(scores):
+        key = torch.zeros(dim, dtype=dtype)
+        key[0] = s
+        fill(cache, 0, i, cache.k, 0, key)
+    q = torch.zeros(1, heads, dim, dtype=dtype)
+    q[:, :, 0] = 1
+    return cache, q
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("group", [1, 3, 8])
 @pytest.mark.parametrize("dim", [64, 128, 256])
@@ -77,6 +90,19 @@ def test_shares_enter_the_product_with_float32s_bits(tk, dim, group, dtype):
         p = np.exp(kk[:, 0]) / np.exp(kk[:, 0]).sum()
         tol[b] = _kv.UNIT[dtype] * np.abs(want[b]) + 2.0 ** -25 + 2.0 ** -20 * (p @ np.abs(vv))
     _kv.close(out, want, tol)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_score_that_is_not_a_number_reaches_every_weight_of_its_head(tk, value):
+    """Also those in tiles that hold only -inf besides."""
+    scores = [0.0] * 128 + [float("-inf")] * 128 + [0.5] * 44
+    scores[3] = value
+    cache, q = scores_cache(scores, 64, torch.float16)
+    k, v, table, lens = cache.dev()
+    weight = torch.ones(1, 1, cache.capacity, device="cuda")
+    out, lse = tk.kv_attend(q.cuda(), k, v, table, lens, scale=1.0, weight=weight)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    assert torch.isnan(weight[0, 0, :300]).all() and torch.all(weight[0, 0, 300:] == 1)
 
 
 def decoder(seqs, n, heads, group, dim, dtype=torch.float16, seed=42):

@@ -1071,7 +1071,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) kv_weight_kernel(const __gr
                 if (g < heads) y[g] = from[g * (kTile / 4)];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[i] = slot0 + i < w.n ? wi[slot0 + i] : 0.f;
-            const float f = ml.y == 0.f || tm == -INFINITY ? 0.f : exp2f(tm - ml.x) / ml.y;
+            const float f = ml.y == 0.f ? 0.f : exp2f(tm - ml.x) / ml.y;  // a NaN sum reaches every tile
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const float fg = __shfl_sync(kFullMask, f, g);
