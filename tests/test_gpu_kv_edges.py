@@ -105,6 +105,25 @@ def test_a_score_that_is_not_a_number_reaches_every_weight_of_its_head(tk, value
     assert torch.isnan(weight[0, 0, :300]).all() and torch.all(weight[0, 0, 300:] == 1)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("low", [-200.0, float("-inf")])
+@pytest.mark.parametrize("n,first,last,bad", [(300, 128, 256, 130), (40000, 5000, 20000, 12345)])
+def test_a_value_that_is_not_finite_shows_however_small_its_share(tk, n, first, last, bad, low, value):
+    """Its element of the output is not finite, the others are as they would be without it."""
+    scores = torch.zeros(n)
+    scores[first:last] = low
+    cache, q = scores_cache(scores.tolist(), 64, torch.bfloat16)
+    want, lse, _, tol, lse_tol, _ = _kv.attend(cache, q, 1.0)
+    cache.v[cache.table[0, bad // 16], bad % 16, 0, 5] = value
+    k, v, table, lens = cache.dev()
+    out, got = tk.kv_attend(q.cuda(), k, v, table, lens, scale=1.0)
+    assert not torch.isfinite(out[0, 0, 5])
+    out[0, 0, 5] = want[0, 0, 5]
+    if low > float("-inf"):  # else the bound of _kv.attend is not finite
+        _kv.close(out, want, tol)
+        _kv.close(got, lse, lse_tol)
+
+
 def decoder(seqs, n, heads, group, dim, dtype=torch.float16, seed=42):
     """A cache of `n` slots in each sequence, weights to attend with, and what to evict to."""
     g = torch.Generator("cuda").manual_seed(seed)

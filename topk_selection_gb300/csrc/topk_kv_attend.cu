@@ -921,7 +921,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 }
                 if (whole) {
                     const float r = ml.y == 0.f ? 0.f : __frcp_rn(ml.y);
-                    fa *= r;
+                    fa = ml.y == 0.f ? -1.f : fa * r;  // below 0: the head has no sum, and gives 0
                     fb *= r;
                 }
                 first_of[me] = fa;
@@ -956,9 +956,10 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                     };
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
-                        // A head with no sum has a factor of 0, also where its products are not numbers.
-                        v[0][i] = fa[i] == 0.f ? 0.f : sum_of(0, i) * fa[i];
-                        if (n > 1 && fb[i] != 0.f) v[0][i] += sum_of(S::kTerms, i) * fb[i];
+                        // A factor that has come down to 0 still lets a value that is not finite through.
+                        float x = sum_of(0, i) * fa[i];
+                        if (n > 1) x += sum_of(S::kTerms, i) * fb[i];
+                        v[0][i] = fa[i] < 0.f ? 0.f : x;
                     }
                     if (whole) {
                         uint16_t* to = p.a.out + (size_t)(q0 + j) * p.c.dim + d;
