@@ -124,6 +124,27 @@ def test_a_value_that_is_not_finite_shows_however_small_its_share(tk, n, first, 
         _kv.close(got, lse, lse_tol)
 
 
+@pytest.mark.parametrize("start", [-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 5, -2 ** 30, -2 ** 30 - 7, -2 ** 31 + 2 ** 30])
+def test_append_of_tokens_far_past_the_capacity(tk, start):
+    """A token's number in its sequence and its slot may pass 2^31: it is dropped, not wrapped to a slot below 0.
+    (Starts below 0 stand for that many tokens before the ones that k_new holds.)"""
+    cache = _kv.Cache([20, 5], 2, 64, 16, torch.float16, "head", room=12, seed=43)
+    k, v, table, lens = cache.dev()
+    before = k.clone(), v.clone()
+    new = torch.randn(40, 2, 64, device="cuda").half()
+    starts = torch.tensor([start, 38, 40], dtype=torch.int32, device="cuda")
+    weight = torch.full((2, 2, cache.capacity), 5.0, device="cuda")
+    pos = torch.full((2, 2, cache.capacity), -7, dtype=torch.int32, device="cuda")
+    tk.kv_append(k, v, table, lens, new, new, starts=starts, weight=weight, pos=pos, next_pos=lens)
+    at = cache.table[1, 0]
+    for pool, was in zip((k, v), before):
+        assert torch.equal(pool[at, 5:7], new[38:])
+        was[at, 5:7] = new[38:]
+        assert torch.equal(pool.view(torch.int16), was.view(torch.int16))
+    assert pos[1, 0].tolist() == [-7] * 5 + [5, 6] + [-7] * (cache.capacity - 7)
+    assert torch.all(pos[0] == -7) and torch.all(weight[0] == 5.0)
+
+
 def decoder(seqs, n, heads, group, dim, dtype=torch.float16, seed=42):
     """A cache of `n` slots in each sequence, weights to attend with, and what to evict to."""
     g = torch.Generator("cuda").manual_seed(seed)

@@ -77,20 +77,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
             looked_up = true;
             int b = a.starts ? find_seq(a.starts, a.c.seqs, __shfl_sync(kFullMask, t, 0), lane) : t;
             if (lane < count) {
-                int i = 0;
+                long long i = 0;  // starts are the caller's: neither this nor the slot may wrap
                 bool in = true;
                 if (a.starts) {
                     int next = a.starts[b + 1];
                     while (next <= t && b + 1 < a.c.seqs) next = a.starts[++b + 1];
                     in = t < next;  // else past the last sequence's tokens
-                    i = t - a.starts[b];
+                    i = (long long)t - a.starts[b];
                 }
-                const int slot = a.c.len(b) + i;
-                if (in && i >= 0 && slot < a.c.capacity()) {
+                const long long at = a.c.len(b) + i;
+                if (in && i >= 0 && at < a.c.capacity()) {
+                    const int slot = (int)at;
                     where[warp][lane].z = a.c.page_of(b, slot);
                     where[warp][lane].w = slot % a.c.page_size;
                     if (a.weight.data) a.weight.row(b, h)[slot] = 0.f;
-                    if (a.pos.data) a.pos.row(b, h)[slot] = a.next_pos[b] + i;
+                    if (a.pos.data) a.pos.row(b, h)[slot] = a.next_pos[b] + (int)i;
                 }
             }
             __syncwarp();
