@@ -357,9 +357,12 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
  * largest weight, and move them below slot `budget`.  Sequences with at most
  * `budget` slots keep everything.
  *
- * Order: protected slots first, then by weight descending (topk_rows_f32's
- * order: NaN above +inf, -0 equal to +0), the lower slot among equals.  A
- * slot is protected when pos < sink or pos >= next_pos[b] - recent.
+ * Order: protected slots first, all of them equal whatever they weigh; then
+ * the others by weight descending (topk_rows_f32's order: NaN above +inf, -0
+ * equal to +0); the lower slot among equals.  A slot is protected when
+ * pos < sink or pos >= next_pos[b] - recent.  Distinct positions below
+ * next_pos[b] protect at most sink + recent slots; where others protect more
+ * than `budget`, the lowest of them stay.
  * A kept slot below `budget` stays where it is; the kept slots at or above
  * it, in ascending order, fill the slots below it that were not kept, in
  * ascending order.  Keys, values, weights and positions move alike; slots at

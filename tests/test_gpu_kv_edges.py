@@ -145,6 +145,32 @@ def test_append_of_tokens_far_past_the_capacity(tk, start):
     assert torch.all(pos[0] == -7) and torch.all(weight[0] == 5.0)
 
 
+@pytest.mark.parametrize("rising", [False, True])
+def test_protected_slots_are_equal_whatever_they_weigh(tk, rising):
+    """Positions at or past next_pos protect more slots than are kept: the lowest of them stay, the heaviest of the
+    others do not; where fewer are protected, weights decide among the others alone."""
+    n, budget = 300, 64
+    c = decoder(1, n, 1, 1, 64)
+    weight = torch.arange(1, n + 1, dtype=torch.float32, device="cuda") if rising else \
+        torch.arange(n, 0, -1, dtype=torch.float32, device="cuda")
+    weight[7] = float("nan")
+    for protected in (range(100, 300, 2), range(200, 230)):
+        pos = torch.zeros_like(c["pos"])
+        pos[0, 0, list(protected)] = 1000
+        w = torch.zeros_like(c["weight"])
+        w[0, 0, :n] = weight
+        p_out = torch.arange(pos.shape[2], dtype=torch.int32, device="cuda").reshape(1, 1, -1)
+        p_in = pos.clone()
+        p_in[0, 0, :n] += torch.arange(n, device="cuda", dtype=torch.int32)  # tells the slots apart
+        kept = list(protected)[:budget]
+        rest = sorted(set(range(n)) - set(protected), key=lambda i: (i != 7, -float(weight[i]), i))
+        kept = sorted(kept + rest[:budget - len(kept)])
+        tk.kv_evict(c["k"].clone(), c["v"].clone(), c["table"], c["lens"], w, p_in,
+                    torch.tensor([1000], dtype=torch.int32, device="cuda"), budget, weight_out=torch.zeros_like(w),
+                    pos_out=p_out, lens_out=torch.zeros_like(c["lens"]))
+        assert sorted(p % 1000 for p in p_out[0, 0, :budget].tolist()) == kept
+
+
 def decoder(seqs, n, heads, group, dim, dtype=torch.float16, seed=42):
     """A cache of `n` slots in each sequence, weights to attend with, and what to evict to."""
     g = torch.Generator("cuda").manual_seed(seed)

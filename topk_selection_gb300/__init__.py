@@ -446,8 +446,9 @@ def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, 
              lens_out: torch.Tensor | None = None, stream=None):
     """Keep, per sequence and head, the `budget` slots with the largest weight
     (and those with pos < sink or pos >= next_pos - recent), moving the kept
-    ones from above the budget into the places freed below it: (weight_out,
-    pos_out, lens_out), by default weight, pos and lens themselves, changed in
+    ones from above the budget into the places freed below it; among equal
+    weights, and among protected slots whatever they weigh, the lower slot
+    goes first: (weight_out, pos_out, lens_out), by default weight, pos and lens themselves, changed in
     place -- topk_kv_evict in include/topk.h.  Pages past the first
     ceil(budget / page_size) of a sequence can be reused afterwards."""
     weight_out = weight if weight_out is None else weight_out
