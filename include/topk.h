@@ -257,7 +257,9 @@ int topk_reduce_f32(const float* in, size_t n, int op, double* out, struct CUstr
  *             capacity as the capacity.
  *
  * topk_kv_rows is a per-slot side array [seqs, heads, slots]: element
- * (b, h, s) lies at b * seq_stride + h * head_stride + s.
+ * (b, h, s) lies at b * seq_stride + h * head_stride + s.  Its rows do not
+ * overlap one another.  The rows of an array that is written may lie between
+ * those of the one that is read if both have the same strides.
  *
  * All pointers are device memory (TOPK_ERR_INVALID_ARG for host memory) and
  * the calls only enqueue.  They may be captured in a graph once a call as

@@ -438,3 +438,34 @@ def test_graphs_after_a_call_cut_short(tk, side, withhold, before):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     s.synchronize()
     tk.check_stream(s)
+
+
+def test_side_arrays_that_lie_between_one_another(tk):
+    """Rows of weight and weight_out alternate in one array: they do not overlap.  Dimensions of one element may have
+    any stride."""
+    cache = _kv.Cache([200, 90], 2, 64, 16, torch.float16, "head", seed=36)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(2, 4, 64, device="cuda").half()
+    weight = torch.rand(2, 2, cache.capacity, generator=torch.Generator().manual_seed(37))
+    both = torch.zeros(2, 2, 2, cache.capacity, device="cuda")
+    both[:, :, 0] = weight.cuda()
+    tk.kv_attend(q, k, v, table, lens, weight=both[:, :, 0], weight_out=both[:, :, 1])
+    plain = weight.cuda()
+    tk.kv_attend(q, k, v, table, lens, weight=plain)
+    for b, n in enumerate(cache.lens):
+        assert torch.equal(both[b, :, 1, :n], plain[b, :, :n])
+    assert torch.equal(both[:, :, 0].cpu(), weight)
+    pos = torch.arange(cache.capacity, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    pair = torch.zeros(2, 2, 2, cache.capacity, dtype=torch.int32, device="cuda")
+    pair[:, :, 0] = pos
+    w_out, p_out, l_out = tk.kv_evict(k, v, table, lens, both[:, :, 1], pair[:, :, 0], lens, 64,
+                                      weight_out=both[:, :, 0], pos_out=pair[:, :, 1], lens_out=lens.clone())
+    assert l_out.tolist() == [64, 64] and torch.equal(lens.cpu(), torch.tensor([200, 90], dtype=torch.int32))
+    for b in range(2):
+        for h in range(2):
+            src = _kv.evict_sources(plain[b, h].cpu().numpy(), np.arange(cache.capacity), cache.lens[b],
+                                    cache.lens[b], 64, 0, 0)
+            assert p_out[b, h, :64].tolist() == src.tolist()
+    one = plain[:1]
+    same = torch.as_strided(one, one.shape, (7 * one.stride(0), one.stride(1), 1), one.storage_offset())
+    tk.kv_attend(q[:1], k, v, table[:1], lens[:1].clone(), weight=one, weight_out=same)

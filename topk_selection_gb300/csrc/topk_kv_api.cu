@@ -58,13 +58,49 @@ int check_cache(const topk_kv_cache* c, topk::KvCache* out) {
     return TOPK_OK;
 }
 
+// Strides of a side array; that of a dimension with one element is no matter.
+struct Steps {
+    int64_t seq, head;
+    Steps(const topk_kv_rows* r, const topk::KvCache& c)
+        : seq(c.seqs > 1 ? r->seq_stride : 0), head(c.heads > 1 ? r->head_stride : 0) {}
+    bool operator==(const Steps& o) const { return seq == o.seq && head == o.head; }
+};
+
+// Whether some row of an array of `slots` slots meets a row of another one,
+// `apart` elements behind it, of `others` slots and the same strides; with
+// apart == 0, a row of its own other than itself.  Two rows that are ds
+// sequences and dh heads apart are apart + ds * seq + dh * head elements apart:
+// for each dh, the least ds that takes this above -others decides.
+bool rows_meet(const Steps& at, const topk::KvCache& c, int64_t slots, int64_t others, int64_t apart) {
+    const int64_t most = at.seq > 0 ? c.seqs - 1 : 0;
+    auto meet = [&](int64_t from, int64_t first, int64_t last) {  // some ds in [first, last]
+        if (first > last) return false;
+        int64_t ds = first;
+        if (at.seq > 0 && from + first * at.seq <= -others) ds = first + (-others - from - first * at.seq) / at.seq + 1;
+        return ds <= last && from + ds * at.seq > -others && from + ds * at.seq < slots;
+    };
+    const int heads = at.head > 0 ? c.heads - 1 : 0;
+    for (int dh = -heads; dh <= heads; ++dh) {
+        const int64_t from = apart + dh * at.head;
+        if (apart == 0 && dh == 0) {  // all but itself
+            if (meet(from, -most, -1) || meet(from, 1, most)) return true;
+        } else if (meet(from, -most, most)) {
+            return true;
+        }
+    }
+    return false;
+}
+
 // A side array with at least `slots` slots whose rows do not lie in one another.
 int check_rows(const topk_kv_rows* r, const topk::KvCache& c, int slots) {
+    constexpr int64_t kMost = int64_t(1) << 44;  // elements that addresses have room for
     if (misaligned(r->data, 4) || r->slots < slots) return TOPK_ERR_INVALID_ARG;
-    if ((c.heads > 1 && r->head_stride < r->slots) || (c.seqs > 1 && r->seq_stride < r->slots))
-        return TOPK_ERR_INVALID_ARG;
-    if (r->head_stride < 0 || r->seq_stride < 0) return TOPK_ERR_INVALID_ARG;
-    return TOPK_OK;
+    const Steps at(r, c);
+    if ((c.heads > 1 && at.head < r->slots) || (c.seqs > 1 && at.seq < r->slots)) return TOPK_ERR_INVALID_ARG;
+    if (r->head_stride < 0 || r->seq_stride < 0 || at.seq > kMost || at.head > kMost) return TOPK_ERR_INVALID_ARG;
+    const bool nested = c.seqs == 1 || c.heads == 1 || at.seq >= (c.heads - 1) * at.head + r->slots ||
+                        at.head >= (c.seqs - 1) * at.seq + r->slots;
+    return nested || !rows_meet(at, c, r->slots, r->slots, 0) ? TOPK_OK : TOPK_ERR_INVALID_ARG;
 }
 
 template <typename T>
@@ -75,16 +111,22 @@ topk::KvRows<T> rows_of(const topk_kv_rows* r) {
 
 bool present(const topk_kv_rows* r) { return r && r->data; }
 
-// The bytes that a side array spans.
-size_t span(const topk_kv_rows* r, const topk::KvCache& c) {
-    return 4 * ((size_t)(c.seqs - 1) * r->seq_stride + (size_t)(c.heads - 1) * r->head_stride + r->slots);
+// The elements that a side array spans.
+int64_t span(const topk_kv_rows* r, const topk::KvCache& c) {
+    const Steps at(r, c);
+    return (c.seqs - 1) * at.seq + (c.heads - 1) * at.head + r->slots;
 }
 
-// Whether `out` is the same array as `in`, or overlaps none of it.
+// Whether `out` is the same array as `in`, or overlaps none of it.  Arrays
+// with the same strides may have their rows between one another's.
 bool same_or_apart(const topk_kv_rows* in, const topk_kv_rows* out, const topk::KvCache& c) {
-    if (in->data == out->data) return in->seq_stride == out->seq_stride && in->head_stride == out->head_stride;
-    const char *a = static_cast<const char*>(in->data), *b = static_cast<const char*>(out->data);
-    return a + span(in, c) <= b || b + span(out, c) <= a;
+    const Steps at(in, c);
+    const bool alike = at == Steps(out, c);
+    if (in->data == out->data) return alike;
+    const int64_t apart =
+        (int64_t)(reinterpret_cast<uintptr_t>(out->data) - reinterpret_cast<uintptr_t>(in->data)) / 4;
+    if (apart >= span(in, c) || -apart >= span(out, c)) return true;
+    return alike && !rows_meet(at, c, in->slots, out->slots, apart);
 }
 
 int on_device(std::initializer_list<const void*> ps) {
