@@ -379,20 +379,25 @@ def reduce(x: torch.Tensor, op: str, out: torch.Tensor | None = None, stream=Non
     return out
 
 
-def _load_kv_binding():
-    """The compiled module that marshals the key-value cache operators' tensors."""
-    path = _build.BINDING_PATH
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
-    spec = importlib.util.spec_from_file_location("kv_binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                  for f in (_lib.topk_kv_append, _lib.topk_kv_attend, _lib.topk_kv_evict)))
-    return module
+class _KvBinding:
+    """The compiled module that marshals the key-value cache operators' tensors.  Loaded by their first call: the other
+    operators need only the library, whatever torch it was built beside."""
+
+    def __getattr__(self, name):
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_file_location("kv_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (_lib.topk_kv_append, _lib.topk_kv_attend, _lib.topk_kv_evict)))
+        for f in ("append", "attend", "evict"):
+            setattr(self, f, getattr(module, f))  # found without this function from now on
+        return getattr(module, name)
 
 
-_kv = _load_kv_binding()
+_kv = _KvBinding()
 
 
 def _kv_stream(stream):

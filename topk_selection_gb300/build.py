@@ -3,14 +3,18 @@
 Each .cu file compiles in parallel to an object file under ``_lib/``; the
 objects link into ``_lib/libtopk.so`` (CUDA runtime linked statically).
 Beside it, g++ compiles the Python binding of the key-value cache operators
-(csrc/kv_binding.cpp) against the installed torch into ``_lib/kv_binding.so``.
-Nothing is rebuilt when both are newer than every source.
+(csrc/kv_binding.cpp) against the installed torch into ``_lib/kv_binding-<torch's
+version><Python's suffix>``, so that a module built for another torch or Python
+is never taken for this one's.  Nothing is rebuilt when both are newer than
+every source.  The library needs no torch: where there is none, or the binding
+does not compile, it is built all the same.
 """
 from __future__ import annotations
 
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -22,7 +26,6 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtopk.so")
 BINDING_SRC = os.path.join(CSRC, "kv_binding.cpp")
-BINDING_PATH = os.path.join(LIB_DIR, "kv_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
@@ -44,10 +47,20 @@ def _inputs():
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def binding_path() -> str | None:
+    """Where the binding for the running Python and its torch belongs; None without torch."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    version = runpy.run_path(os.path.join(torch.submodule_search_locations[0], "version.py"))["__version__"]
+    return os.path.join(LIB_DIR, f"kv_binding-{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+    made = [p for p in (LIB_PATH, binding_path()) if p]
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -77,9 +90,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    binding = BINDING_PATH + f".tmp{os.getpid()}"
-    procs.append((BINDING_SRC, subprocess.Popen(_binding_command(binding), stdout=subprocess.PIPE,
-                                                stderr=subprocess.STDOUT, text=True)))
+    binding = binding_path()
+    if binding:
+        procs.append((BINDING_SRC, subprocess.Popen(_binding_command(binding + f".tmp{os.getpid()}"),
+                                                    stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -87,12 +101,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(out)
         if p.returncode != 0:
             failed.append(src)
+    if set(failed) <= {BINDING_SRC}:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], check=True)
+        os.replace(tmp, LIB_PATH)
     if failed:
         raise RuntimeError("compilation failed for: " + ", ".join(os.path.basename(f) for f in failed))
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], check=True)
-    os.replace(tmp, LIB_PATH)
-    os.replace(binding, BINDING_PATH)
+    if binding:
+        os.replace(binding + f".tmp{os.getpid()}", binding)
     return LIB_PATH
 
 
