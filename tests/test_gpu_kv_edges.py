@@ -469,3 +469,39 @@ def test_side_arrays_that_lie_between_one_another(tk):
     one = plain[:1]
     same = torch.as_strided(one, one.shape, (7 * one.stride(0), one.stride(1), 1), one.storage_offset())
     tk.kv_attend(q[:1], k, v, table[:1], lens[:1].clone(), weight=one, weight_out=same)
+
+
+def test_what_is_written_says_so(tk):
+    """Tensors that an operator writes count a change, as for torch's own; outputs without a gradient do not pretend
+    to have one."""
+    cache = _kv.Cache([40, 30], 2, 64, 16, torch.float16, "head", room=4, seed=38)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(2, 4, 64, device="cuda").half()
+    new = torch.randn(2, 2, 64, device="cuda").half()
+    weight = torch.zeros(2, 2, cache.capacity, device="cuda")
+    pos = torch.arange(cache.capacity, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+
+    def versions(*ts):
+        return [t._version for t in ts]
+
+    before = versions(k, v, weight, pos, lens, table, q, new)
+    tk.kv_append(k, v, table, lens, new, new, weight=weight, pos=pos, next_pos=lens)
+    after = versions(k, v, weight, pos, lens, table, q, new)
+    assert all(a > b for a, b in zip(after[:4], before[:4])) and after[4:] == before[4:]
+    out, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+    before = versions(weight, out, lse, k, v, q)
+    tk.kv_attend(q, k, v, table, lens, weight=weight, out=out, lse=lse)
+    after = versions(weight, out, lse, k, v, q)
+    assert all(a > b for a, b in zip(after[:3], before[:3])) and after[3:] == before[3:]
+    before = versions(k, v, weight, pos, lens)
+    tk.kv_evict(k, v, table, lens, weight, pos, lens.clone(), 16)
+    assert all(a > b for a, b in zip(versions(k, v, weight, pos, lens), before))
+    with torch.inference_mode():
+        tk.kv_attend(q.clone(), k, v, table, lens, weight=torch.zeros_like(weight))
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tk.kv_attend(q.clone().requires_grad_(), k, v, table, lens)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tk.kv_append(k, v, table, lens, new.clone().requires_grad_(), new)
+    with torch.no_grad():
+        got, _ = tk.kv_attend(q.clone().requires_grad_(), k, v, table, lens)
+    assert not got.requires_grad

@@ -420,7 +420,9 @@ def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
     pos, next_pos     int32 [seqs, heads, slots] and [seqs]: next_pos[b] + i is
                       written at the new slots
 
-    lens is not changed: add the tokens' numbers to it afterwards."""
+    lens is not changed: add the tokens' numbers to it afterwards.  Like the
+    other two operators it has no gradient: arguments that require grad are
+    refused outside torch.no_grad()."""
     rc = _kv.append(k_pages, v_pages, table, lens, k_new, v_new, starts, weight, pos, next_pos, _kv_stream(stream))
     if rc != TOPK_OK:
         raise TopKError(rc, "topk_kv_append")

@@ -7,6 +7,7 @@
 // to 15 us a call), so it is done here.  The library itself stays free of
 // torch: it is loaded by ctypes, which hands over its functions' addresses.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -156,6 +157,27 @@ struct Stream {
     }
 };
 
+// Refuses arguments that autograd follows: these operators have no backward
+// pass, and results without a history would pass for constants.
+void check_grad(const char* name, std::initializer_list<PyObject*> tensors) {
+    if (!c10::GradMode::is_enabled()) return;
+    for (PyObject* o : tensors)
+        if (o != Py_None && THPVariable_Unpack(o).requires_grad())
+            raise(PyExc_RuntimeError, std::string(name) +
+                                          " has no gradient, and one of its arguments requires grad: call it under "
+                                          "torch.no_grad(), or detach() the argument");
+}
+
+// Counts a change of tensors that a call has written, by which autograd knows
+// that what it saved of them is stale.
+void written(std::initializer_list<PyObject*> tensors) {
+    for (PyObject* o : tensors) {
+        if (o == Py_None) continue;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+}
+
 // Runs f with every exception turned into a Python one, after a check of the
 // number of arguments.
 template <typename F>
@@ -195,11 +217,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const topk_kv_rows weight = rows(a[7], "weight", at::kFloat, c), pos = rows(a[8], "pos", at::kInt, c);
         const int32_t* next_pos = ints(a[9], "next_pos", c, c.c.seqs);
         const Stream s(a[10], c);
+        check_grad("kv_append", {a[0], a[1], a[4], a[5], a[7]});
         if (k.size(0) == 0) return PyLong_FromLong(TOPK_OK);
-        return PyLong_FromLong(call(c, [&] {
+        const int rc = call(c, [&] {
             return g_append(&c.c, k.const_data_ptr(), ks, v.const_data_ptr(), vs, (int)k.size(0), starts, &weight,
                             &pos, next_pos, s.handle);
-        }));
+        });
+        if (rc == TOPK_OK) written({a[0], a[1], a[7], a[8]});
+        return PyLong_FromLong(rc);
     });
 }
 
@@ -221,6 +246,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const topk_kv_rows weight = rows(a[6], "weight", at::kFloat, c);
         const topk_kv_rows weight_out = a[7] == Py_None ? weight : rows(a[7], "weight_out", at::kFloat, c);
         const Stream s(a[10], c);
+        check_grad("kv_attend", {a[0], a[1], a[2], a[6], a[7], a[8], a[9]});
         const at::Tensor out = a[8] != Py_None
                                    ? tensor(a[8], "out", c.type, c.device, {c.c.seqs, q_heads, c.c.dim})
                                    : at::Tensor(at::detail::empty_cuda({c.c.seqs, q_heads, c.c.dim}, c.type, c.device,
@@ -235,6 +261,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s.handle);
         });
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
+        written({a[7] == Py_None ? a[6] : a[7], a[8], a[9]});
         PyObject* pair = PyTuple_New(2);
         if (!pair) throw Raised();
         PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
@@ -255,9 +282,13 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            pos_out = rows(a[11], "pos_out", at::kInt, c);
         int32_t* lens_out = const_cast<int32_t*>(ints(a[12], "lens_out", c, c.c.seqs));
         const Stream s(a[13], c);
-        return PyLong_FromLong(call(c, [&] {
-            return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out, s.handle);
-        }));
+        check_grad("kv_evict", {a[0], a[1], a[4], a[10]});
+        const int rc = call(c, [&] {
+            return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out,
+                           s.handle);
+        });
+        if (rc == TOPK_OK) written({a[0], a[1], a[10], a[11], a[12]});
+        return PyLong_FromLong(rc);
     });
 }
 
