@@ -505,3 +505,18 @@ def test_what_is_written_says_so(tk):
     with torch.no_grad():
         got, _ = tk.kv_attend(q.clone().requires_grad_(), k, v, table, lens)
     assert not got.requires_grad
+
+
+def test_an_empty_batch_is_nothing_to_do(tk):
+    cache = _kv.Cache([40], 2, 64, 16, torch.float16, "head", seed=39)
+    k, v, table, lens = cache.dev()
+    table, lens = table[:0], lens[:0]
+    weight, pos = torch.zeros(0, 2, 48, device="cuda"), torch.zeros(0, 2, 48, dtype=torch.int32, device="cuda")
+    before = k.clone()
+    new = torch.zeros(0, 2, 64, device="cuda").half()
+    tk.kv_append(k, v, table, lens, new, new, weight=weight, pos=pos, next_pos=lens)
+    out, lse = tk.kv_attend(torch.zeros(0, 4, 64, device="cuda").half(), k, v, table, lens, weight=weight)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    got = tk.kv_evict(k, v, table, lens, weight, pos, lens, 16)
+    assert got[0] is weight and got[2] is lens
+    assert torch.equal(k.view(torch.int16), before.view(torch.int16))

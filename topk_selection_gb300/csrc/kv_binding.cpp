@@ -256,7 +256,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                                                    c.device, std::nullopt));
         if (!out.is_contiguous() || !lse.is_contiguous())
             raise(PyExc_ValueError, "out and lse must be contiguous");
-        const int rc = call(c, [&] {
+        const int rc = c.c.seqs == 0 ? (int)TOPK_OK : call(c, [&] {  // an empty batch: nothing to do
             return g_attend(&c.c, q.const_data_ptr(), qs, (int)q_heads, (float)scale, out.data_ptr(),
                             static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s.handle);
         });
@@ -283,7 +283,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* lens_out = const_cast<int32_t*>(ints(a[12], "lens_out", c, c.c.seqs));
         const Stream s(a[13], c);
         check_grad("kv_evict", {a[0], a[1], a[4], a[10]});
-        const int rc = call(c, [&] {
+        const int rc = c.c.seqs == 0 ? (int)TOPK_OK : call(c, [&] {
             return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out,
                            s.handle);
         });
