@@ -520,3 +520,55 @@ def test_an_empty_batch_is_nothing_to_do(tk):
     got = tk.kv_evict(k, v, table, lens, weight, pos, lens, 16)
     assert got[0] is weight and got[2] is lens
     assert torch.equal(k.view(torch.int16), before.view(torch.int16))
+
+
+def bounds_of_finite(cache, q, scale, weight):
+    """_kv.attend with the scores of -inf left out of the bounds: they are
+    products of -inf, not sums that round, and their shares are exactly 0."""
+    out, lse, w, _, _, _ = _kv.attend(cache, q, scale, weight)
+    tol, lse_tol, w_tol = np.zeros_like(out), np.zeros_like(lse), np.zeros_like(w)
+    group = q.shape[1] // cache.heads
+    for b in range(q.shape[0]):
+        n = cache.lens[b]
+        k, v = (cache.rows(b, p).double().numpy() for p in (cache.k, cache.v))
+        for j in range(q.shape[1]):
+            h = j // group
+            qq = q[b, j].double().numpy()
+            with np.errstate(invalid="ignore"):
+                s = scale * (k[:, h] @ qq)
+            held = np.isfinite(s)
+            if not held.any():
+                continue
+            d = 2 * cache.dim * 2.0 ** -24 * abs(scale) * (np.abs(k[held, h]) @ np.abs(qq)).max()
+            p = np.where(held, np.exp(np.where(held, s, 0) - lse[b, j]), 0.0)
+            rel = 2 * d + 2.0 ** -20 + n * 2.0 ** -24
+            tol[b, j] = _kv.UNIT[cache.dtype] * np.abs(out[b, j]) + 2.0 ** -25 + \
+                (rel + 2.0 ** -15 + n * 2.0 ** -30) * (p @ np.abs(v[:, h])) + n * 2.0 ** -30 * np.abs(v[:, h]).max(0)
+            lse_tol[b, j] = rel + 2.0 ** -22 * abs(lse[b, j])
+            w_tol[b, h, :n] += np.where(held, p * rel + 2.0 ** -23 * np.abs(w[b, h, :n]), 0.0)
+    assert np.isfinite(tol).all() and np.isfinite(lse_tol).all() and np.isfinite(w_tol).all()
+    return out, lse, w, tol, lse_tol, w_tol
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,masked", [(300, [35]), (300, range(0, 256)), (700, range(100, 600)), (700, range(0, 699)),
+                                      (20001, range(0, 15000)), (20001, range(1, 20001, 2))])
+def test_scores_of_minus_infinity_among_finite_ones(tk, n, masked, dtype):
+    """Masked slots get a share of exactly nothing, whole tiles of them at the
+    front, in the middle and over several blocks included."""
+    cache = _kv.Cache([n, 40], 2, 64, 16, dtype, "token", seed=33)
+    q = torch.randn(2, 6, 64, generator=torch.Generator().manual_seed(34)).to(dtype)
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    for i in masked:
+        cache.k[cache.table[0, i // 16], i % 16, 0, 0] = float("-inf")
+    weight = torch.rand(2, 2, cache.capacity, generator=torch.Generator().manual_seed(35))
+    k, v, table, lens = cache.dev()
+    w = torch.zeros_like(weight).cuda()
+    out, lse = tk.kv_attend(q.cuda(), k, v, table, lens, weight=weight.cuda(), weight_out=w)
+    eo, el, ew, to, tl, tw = bounds_of_finite(cache, q, 0.125, weight)
+    _kv.close(out, eo, to)
+    _kv.close(lse, el, tl)
+    for b, m in enumerate(cache.lens):
+        _kv.close(w[b, :, :m], ew[b, :, :m], tw[b, :, :m])
+    at = list(masked)
+    assert torch.equal(w[0, 0, at].cpu(), weight[0, 0, at])
