@@ -572,3 +572,44 @@ def test_scores_of_minus_infinity_among_finite_ones(tk, n, masked, dtype):
         _kv.close(w[b, :, :m], ew[b, :, :m], tw[b, :, :m])
     at = list(masked)
     assert torch.equal(w[0, 0, at].cpu(), weight[0, 0, at])
+
+
+def rand_weight(seqs, heads, cap):
+    return torch.exp(2 * torch.randn(seqs, heads, cap, generator=torch.Generator().manual_seed(40)))
+
+
+@pytest.mark.parametrize("lens,heads,budget,page,room", [
+    ([2100 + 7 * i for i in range(20)], 16, 700, 16, 0),        # more than 304 rows, 256 threads each
+    ([5000 + i for i in range(10)], 31, 4000, 16, 0),
+    ([5200 + 3 * i for i in range(10)], 31, 4000, 16, 0),       # the same with 512
+    ([1500] * 20, 16, 100, 16, 9000),                           # short rows in a wide table
+    ([400300], 20, 100000, 1024, 0),                            # beyond shared memory, on more than 152 blocks
+])
+def test_evict_by_every_kind_of_block(tk, lens, heads, budget, page, room):
+    seqs, dim = len(lens), 8
+    width = -(-(max(lens) + room) // page)
+    k = torch.randint(-30000, 30000, (seqs * width, heads, page, dim), dtype=torch.int16, device="cuda",
+                      generator=torch.Generator("cuda").manual_seed(41)).view(torch.float16).transpose(1, 2)
+    v = k.flip(0).contiguous()
+    table = torch.randperm(seqs * width, device="cuda").to(torch.int32).reshape(seqs, width)
+    cap = width * page
+    weight = rand_weight(seqs, heads, cap)
+    weight[:, :, 5::11] = 0
+    pos = torch.arange(cap, dtype=torch.int32).repeat(seqs, heads, 1)
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def held(pool, b):
+        return pool.view(torch.int16)[table[b].long()].reshape(cap, heads, dim)
+
+    old = [(held(k, b).clone(), held(v, b).clone()) for b in range(seqs)]
+    w_out = torch.full((seqs, heads, budget), -5.0, device="cuda")
+    p_out = torch.full((seqs, heads, budget), -5, dtype=torch.int32, device="cuda")
+    tk.kv_evict(k, v, table, lens_d, weight.cuda(), pos.cuda(), lens_d, budget, 2, 50, w_out, p_out, lens_d.clone())
+    for b, n in enumerate(lens):
+        now = held(k, b), held(v, b)
+        for h in range(heads):
+            src = torch.from_numpy(_kv.evict_sources(weight[b, h].numpy(), pos[b, h].numpy(), n, n, budget, 2, 50))
+            assert torch.equal(p_out[b, h].cpu(), src.to(torch.int32))
+            assert torch.equal(w_out[b, h].cpu(), weight[b, h][src])
+            for was, is_ in zip(old[b], now):
+                assert torch.equal(is_[:budget, h], was[src.cuda(), h]) and torch.equal(is_[budget:, h], was[budget:, h])
