@@ -351,7 +351,8 @@ def test_waits_of_attend_run_out(tk, side, withhold, shape, what):
     want = tk.kv_attend(*args, weight=c["weight"], weight_out=torch.zeros_like(c["weight"]))
     tk.check_stream()
     rows, dim = c["q"].shape[0] * c["q"].shape[1], c["q"].shape[2]
-    out, lse = torch.full((rows + 16, dim), 7.0, dtype=c["q"].dtype, device="cuda"), torch.full((rows + 16,), 7.0).cuda()
+    out = torch.full((rows + 16, dim), 7.0, dtype=c["q"].dtype, device="cuda")
+    lse = torch.full((rows + 16,), 7.0, device="cuda")
     w = torch.full((seqs, heads, cap + 64), 7.0, device="cuda")
     s = side()
     withhold(what)

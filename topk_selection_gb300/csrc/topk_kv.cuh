@@ -91,9 +91,10 @@ int device_pointer(const void* p);
 // Counts n kernel launches.
 void note_launches(int n);
 
-cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k_new, const long long* k_stride,
-                             const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
-                             KvRows<float> weight, KvRows<int> pos, const int* next_pos);
+// sms: the device's number of SMs.
+cudaError_t kv_append_launch(int sms, cudaStream_t s, const KvCache& c, const uint16_t* k_new,
+                             const long long* k_stride, const uint16_t* v_new, const long long* v_stride, int tokens,
+                             const int* starts, KvRows<float> weight, KvRows<int> pos, const int* next_pos);
 
 struct KvAttend {
     const uint16_t* q;
@@ -105,9 +106,9 @@ struct KvAttend {
     KvRows<const float> weight;
     KvRows<float> weight_out;
 };
-size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a);
-cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, const KvState& state,
-                             int* launches);
+size_t kv_attend_scratch(int sms, const KvCache& c, const KvAttend& a);
+cudaError_t kv_attend_launch(int device, int sms, cudaStream_t s, const KvCache& c, const KvAttend& a,
+                             const KvState& state, int* launches);
 
 struct KvEvict {
     KvRows<const float> weight;
@@ -119,7 +120,7 @@ struct KvEvict {
     int* lens_out;
 };
 size_t kv_evict_scratch(const KvCache& c, const KvEvict& e);
-cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, const KvState& state,
-                            int* launches);
+cudaError_t kv_evict_launch(int device, int sms, cudaStream_t s, const KvCache& c, const KvEvict& e,
+                            const KvState& state, int* launches);
 
 }  // namespace topk

@@ -2,6 +2,7 @@
 // dispatch.  The contract is in include/topk.h.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -138,6 +139,19 @@ int on_device(std::initializer_list<const void*> ps) {
     return TOPK_OK;
 }
 
+// The current device, and its number of SMs, which is asked for once.
+cudaError_t current_device(int* device, int* sms) {
+    static std::atomic<int> counts[64];
+    cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>* known = *device < 64 ? &counts[*device] : nullptr;
+    *sms = known ? known->load(std::memory_order_relaxed) : 0;
+    if (*sms > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
+    if (e == cudaSuccess && known) known->store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -161,12 +175,13 @@ int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const i
                     present(pos) ? pos->data : nullptr, next_pos});
     if (rc != TOPK_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
+    int device = 0, sms = 0;
+    cudaError_t e = current_device(&device, &sms);
     if (e != cudaSuccess) return cuda_fail(e);
     const long long ks[2] = {k_new_stride[0], k_new_stride[1]}, vs[2] = {v_new_stride[0], v_new_stride[1]};
-    e = topk::kv_append_launch(s, c, static_cast<const uint16_t*>(k_new), ks, static_cast<const uint16_t*>(v_new), vs,
-                               tokens, starts, rows_of<float>(weight), rows_of<int>(pos), next_pos);
+    e = topk::kv_append_launch(sms, s, c, static_cast<const uint16_t*>(k_new), ks,
+                               static_cast<const uint16_t*>(v_new), vs, tokens, starts, rows_of<float>(weight),
+                               rows_of<int>(pos), next_pos);
     topk::note_unreleased_launch(device, s);  // behind the launch: another thread's may have come between
     if (e != cudaSuccess) return cuda_fail(e);
     topk::note_launch();
@@ -195,8 +210,8 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
                     present(weight_out) ? weight_out->data : nullptr});
     if (rc != TOPK_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
+    int device = 0, sms = 0;
+    cudaError_t e = current_device(&device, &sms);
     if (e != cudaSuccess) return cuda_fail(e);
     topk::KvAttend a = {};
     a.q = static_cast<const uint16_t*>(q);
@@ -209,10 +224,10 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
     a.weight = rows_of<const float>(weight);
     a.weight_out = rows_of<float>(weight_out);
     topk::KvState state;
-    rc = topk::kv_state(device, s, topk::kv_attend_scratch(device, c, a), &state);
+    rc = topk::kv_state(device, s, topk::kv_attend_scratch(sms, c, a), &state);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    e = topk::kv_attend_launch(device, s, c, a, state, &launches);
+    e = topk::kv_attend_launch(device, sms, s, c, a, state, &launches);
     topk::note_unreleased_launch(device, s);
     topk::note_launches(launches);
     return e == cudaSuccess ? TOPK_OK : cuda_fail(e);
@@ -240,8 +255,8 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
                     lens_out});
     if (rc != TOPK_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int device = 0;
-    cudaError_t err = cudaGetDevice(&device);
+    int device = 0, sms = 0;
+    cudaError_t err = current_device(&device, &sms);
     if (err != cudaSuccess) return cuda_fail(err);
     topk::KvEvict e = {};
     e.weight = rows_of<const float>(weight);
@@ -257,7 +272,7 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
     rc = topk::kv_state(device, s, topk::kv_evict_scratch(c, e), &state);
     if (rc != TOPK_OK) return rc;
     int launches = 0;
-    err = topk::kv_evict_launch(device, s, c, e, state, &launches);
+    err = topk::kv_evict_launch(device, sms, s, c, e, state, &launches);
     topk::note_unreleased_launch(device, s);
     topk::note_launches(launches);
     return err == cudaSuccess ? TOPK_OK : cuda_fail(err);

@@ -111,16 +111,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 
 }  // namespace
 
-cudaError_t kv_append_launch(cudaStream_t s, const KvCache& c, const uint16_t* k_new, const long long* k_stride,
-                             const uint16_t* v_new, const long long* v_stride, int tokens, const int* starts,
-                             KvRows<float> weight, KvRows<int> pos, const int* next_pos) {
+cudaError_t kv_append_launch(int sms, cudaStream_t s, const KvCache& c, const uint16_t* k_new,
+                             const long long* k_stride, const uint16_t* v_new, const long long* v_stride, int tokens,
+                             const int* starts, KvRows<float> weight, KvRows<int> pos, const int* next_pos) {
     AppendArgs a = {c, k_new, v_new, {k_stride[0], k_stride[1]}, {v_stride[0], v_stride[1]},
                     tokens, starts, weight, pos, next_pos, 1, 0};
     while ((1 << a.shift) < c.dim / 8) ++a.shift;  // dim is at most 256: 32 lanes
     const long long items = (long long)tokens * c.heads;
     // 16 warps an SM at least, then longer ones (40942 tokens of 8 heads: 164 us
     // with one item a warp, 59 with 8 or 16, 62 with 32).
-    while (a.per < 16 && items / (2 * a.per) >= 152 * 16) a.per *= 2;
+    while (a.per < 16 && items / (2 * a.per) >= sms * 16) a.per *= 2;
     const long long warps = (items + a.per - 1) / a.per, blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch_pdl(kv_append_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, s, a);

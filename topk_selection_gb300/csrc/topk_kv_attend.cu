@@ -978,7 +978,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
             if (!whole) {
                 // The group's P is free: its products are over, and it writes the next one behind a barrier.
                 static_assert(S::kPBytes >= kJoin * GP * sizeof(float), "a join's factors fit where P was");
-                auto* factor = reinterpret_cast<float(*)[GP]>(smem_raw + (p_buf + group * S::kPBytes - smem_addr(smem_raw)));
+                const uint32_t at = p_buf + group * S::kPBytes - smem_addr(smem_raw);
+                auto* factor = reinterpret_cast<float(*)[GP]>(smem_raw + at);
                 join_row<GP>(p, x.total, x.blocks, row_start, x.tiles, q0, heads, row_ml, factor, joined[group],
                              &arrived[group], 1 + group, me);
             }
@@ -993,7 +994,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
         // in flight end before the block does and tensor memory is freed.
         if (warp == kCopyK || warp == kCopyV) {
             const bool keys = warp == kCopyK;
-            const int full0 = keys ? S::kFullK : S::kFullV, items = issued[keys ? 0 : 1], q_loads = keys ? issued[2] : 0;
+            const int full0 = keys ? S::kFullK : S::kFullV;
+            const int items = issued[keys ? 0 : 1], q_loads = keys ? issued[2] : 0;
 #pragma unroll 1
             for (int i = max(0, items - S::kRing); i < items; ++i)
                 mbar_wait(&bars[full0 + i % S::kRing], (i / S::kRing) & 1);
@@ -1129,16 +1131,6 @@ int group_part(const KvCache& c, const KvAttend& a) {
     return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 || c.dim > 128 ? 8 : 16;
 }
 
-int sm_count(int device) {
-    static std::atomic<int> counts[64];
-    int n = device >= 0 && device < 64 ? counts[device].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 1;
-        if (device >= 0 && device < 64) counts[device].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 // The plan of a call, and its scratch when `scratch` is given.
 struct Plan {
     AttendArgs args;
@@ -1146,7 +1138,7 @@ struct Plan {
     size_t bytes;
 };
 
-Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
+Plan make_plan(int sms, const KvCache& c, const KvAttend& a, void* scratch) {
     Plan plan;
     AttendArgs& p = plan.args;
     const int gp = group_part(c, a);
@@ -1157,7 +1149,7 @@ Plan make_plan(int device, const KvCache& c, const KvAttend& a, void* scratch) {
     p.box = c.page_size & -c.page_size;
     if (p.box > kTile) p.box = kTile;
     const size_t rows = (size_t)c.seqs * p.rows, tiles = rows * ((c.capacity() + kTile - 1) / kTile);
-    plan.blocks = sm_count(device);
+    plan.blocks = sms;
     if ((size_t)plan.blocks > tiles) plan.blocks = (int)tiles;
     if (plan.blocks > kKvBlocks) plan.blocks = kKvBlocks;
     char* at = static_cast<char*>(scratch);
@@ -1219,13 +1211,13 @@ cudaError_t launch_dim(const Plan& plan, int gp, int device, cudaStream_t s, con
 
 }  // namespace
 
-size_t kv_attend_scratch(int device, const KvCache& c, const KvAttend& a) {
-    return make_plan(device, c, a, nullptr).bytes;
+size_t kv_attend_scratch(int sms, const KvCache& c, const KvAttend& a) {
+    return make_plan(sms, c, a, nullptr).bytes;
 }
 
-cudaError_t kv_attend_launch(int device, cudaStream_t s, const KvCache& c, const KvAttend& a, const KvState& state,
-                             int* launches) {
-    Plan plan = make_plan(device, c, a, state.scratch);
+cudaError_t kv_attend_launch(int device, int sms, cudaStream_t s, const KvCache& c, const KvAttend& a,
+                             const KvState& state, int* launches) {
+    Plan plan = make_plan(sms, c, a, state.scratch);
     plan.args.status = state.status;
     plan.args.spins = kv_spins_option();
     plan.args.withhold = kv_withhold_option();

@@ -529,8 +529,8 @@ size_t kv_evict_scratch(const KvCache& c, const KvEvict& e) {
     return 4 * (c.seqs + rows + 2 * rows * room_of(c, e));
 }
 
-cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const KvEvict& e, const KvState& state,
-                            int* launches) {
+cudaError_t kv_evict_launch(int device, int sms, cudaStream_t s, const KvCache& c, const KvEvict& e,
+                            const KvState& state, int* launches) {
     const int rows = c.seqs * c.heads;
     EvictArgs a = {c, e};
     a.room = room_of(c, e);
@@ -547,7 +547,7 @@ cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const 
     // block 1024 slots at least.  (Clusters of 16 were slower: 8 rows of
     // 131072 slots 53 us instead of 43, since not all eight run at once.)
     int blocks = 1;
-    while (blocks < 8 && rows * blocks * 2 <= 304 && c.capacity() / (blocks * 2) >= 1024) blocks *= 2;
+    while (blocks < 8 && rows * blocks * 2 <= 2 * sms && c.capacity() / (blocks * 2) >= 1024) blocks *= 2;
     while (blocks < 8 && (c.capacity() + blocks - 1) / blocks + 32 > kMostHeld) blocks *= 2;
     a.part = (((c.capacity() + blocks - 1) / blocks + 31) & ~31);
     const bool held = a.part <= kMostHeld;
@@ -557,9 +557,9 @@ cudaError_t kv_evict_launch(int device, cudaStream_t s, const KvCache& c, const 
     // 1500 10.9, with 512 11.2), and more than two of which share an SM (512 of
     // 1100: 14.5 and 18.9, of 4500 115 and 118, but of 8192 211 and 205).  Few
     // long ones need all the threads that an SM takes (8 of 131072: 42 us with 1024, 45 with 512).
-    if (blocks == 1 && c.capacity() <= (rows <= 304 ? 2048 : 5120))
+    if (blocks == 1 && c.capacity() <= (rows <= 2 * sms ? 2048 : 5120))
         err = select<256, true>(a, rows, blocks, device, s);
-    else if (rows * blocks <= 152)
+    else if (rows * blocks <= sms)
         err = held ? select<1024, true>(a, rows, blocks, device, s) : select<1024, false>(a, rows, blocks, device, s);
     else
         err = held ? select<512, true>(a, rows, blocks, device, s) : select<512, false>(a, rows, blocks, device, s);
