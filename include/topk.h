@@ -380,7 +380,9 @@ int topk_kv_attend(const struct topk_kv_cache* cache, const void* q, const int64
  *   lens_out             int32[seqs]: min(lens, budget); may be lens itself.
  *
  * One launch where at most 256 slots of a row can move, else two.  Scratch: 8
- * bytes per row and slot that can move, min(budget, capacity - budget).
+ * bytes per row and slot that can move, min(budget, capacity - budget): both
+ * go by the capacity, as the lengths are not known to the host, and so does
+ * the choice of blocks.  A table no wider than the sequences need is fastest.
  */
 int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* weight,
                   const struct topk_kv_rows* pos, const int32_t* next_pos, int budget, int sink, int recent,

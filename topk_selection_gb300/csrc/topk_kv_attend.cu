@@ -1,8 +1,10 @@
 // topk_kv_attend: attention of one new token over a paged cache.
 //
-// Every key and value is read once, and per 16-bit element there are only
-// 2 * group multiply-adds, so the operator is bound by HBM: 6.79 TB/s of
-// measured copy rate is 23 bytes per SM and clock.  With a group of eight
+// Every key and value is read once (by groups of up to 16 query heads, of 8
+// for dim > 128; a larger group is cut into parts that read them once each),
+// and per 16-bit element there are only 2 * group multiply-adds, so the
+// operator is bound by HBM: 6.79 TB/s of measured copy rate is 23 bytes per
+// SM and clock.  With a group of eight
 // query heads that is still more arithmetic than the scalar pipes do in that
 // time, so both products run on the tensor cores, with the cache as the
 // 128-row operand that goes from HBM to shared memory (TMA) to the tensor
@@ -177,7 +179,7 @@ __device__ __forceinline__ Walk find_range(const AttendArgs& p, int* sh) {
     Walk k;
     k.total = __reduce_add_sync(kFullMask, v);
     // One block to a row where one short sequence is all there is: a join costs
-    // as much as four tiles (300 slots of 2 heads, dim 64: 8.6 us a call instead of 10.4).
+    // as much as four tiles (300 slots of 2 heads, dim 64: 9.3 us a call instead of 10.6).
     k.blocks = min((int)gridDim.x, seqs == 1 && k.total <= 4 * p.rows ? p.rows : k.total);
     k.s = k.e = k.b = k.h = k.part = k.t = k.n = k.tiles = 0;
     if ((int)blockIdx.x < k.blocks) {  // uniform over the block
