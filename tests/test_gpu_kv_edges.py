@@ -36,6 +36,40 @@ def fill(cache, b, slot, pool, head, value):
     pool[cache.table[b, slot // cache.page], slot % cache.page, head] = value
 
 
+@pytest.mark.parametrize("dtype,group", [(torch.float16, 1), (torch.float16, 4), (torch.float16, 16),
+                                         (torch.bfloat16, 8)])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_a_long_rows_sum_does_not_drift(tk, dim, group, dtype):
+    """As many rows as SMs, so that a block adds up a whole long one, and a few large values at its end that cancel what
+    came before.  An addition of the product may leave 2^-23 of the sum that far, always in the same direction: 2^-17
+    for the 64 of them before the sum is put aside, and 2^-24 for each of the 2^7 times that it is, another 2^-17.
+    Shares are off by less than 2^-19 of themselves (scores are exact products, below 16).  In one piece it would be
+    2^13 additions, and 2^-12 in the mean."""
+    n, page = 2 ** 18, 1024
+    seqs = torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(44)
+    key = (torch.rand(n, generator=g) * 2 - 1).to(dtype)
+    key[-16:] = 8.0
+    p = torch.softmax(key.double(), 0)
+    v = torch.ones(n, dtype=torch.float64)
+    rest = p[:-16].sum()
+    for i in range(n - 16, n):  # a part of what is left each, and the last four all of it
+        v[i] = (-rest / p[i] / max(1, n - 4 - i)).to(dtype).double()
+        rest = rest + p[i] * v[i]
+    k_pool, v_pool = (torch.zeros(n // page, page, 1, dim, dtype=dtype, device="cuda") for _ in range(2))
+    k_pool.view(n, dim)[:, 0] = key.cuda()
+    v_pool.view(n, dim)[:] = v.to(dtype).cuda()[:, None]
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    q = torch.zeros(seqs, group, dim, dtype=dtype, device="cuda")
+    q[:, :, 0] = 1
+    lens = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    out, lse = tk.kv_attend(q, k_pool, v_pool, table, lens, scale=1.0)
+    want = (p * v).sum().item()
+    tol = _kv.UNIT[dtype] * abs(want) + 2.0 ** -25 + (2.0 ** -16 + 2.0 ** -19) * (p @ v.abs()).item()
+    assert (out.double() - want).abs().max().item() <= tol
+    assert (lse.double() - torch.logsumexp(key.double(), 0).item()).abs().max().item() <= 2.0 ** -19
+
+
 def scores_cache(scores, dim, dtype, heads=1, page=16, seed=30):
     """One sequence whose slots' scores are `scores` for a query of ones at
     element 0 and scale 1: keys hold them there, and zeros elsewhere."""

@@ -25,6 +25,13 @@
 // numbers, 16 bits: their 48 columns would take P's buffers from 16 to 32 KB,
 // and the rings fill the shared memory.
 //
+// The tensor core adds to O in float32, but not to nearest: over a long row
+// the error grows with its slots (16384 of them in one block: 7e-6 of O, and
+// 3% of float16 outputs lie beside the nearest number).  So with every new
+// reference, and every kFold tiles at least, the softmax threads add O up to
+// nearest in columns beside it and set it to zero (0.6% then; 393 us of 64 long
+// sequences as before, 12 heads on one 32.0 -> 32.2).
+//
 // Work is split evenly whatever the lengths are: all (sequence, head) rows'
 // tiles of 128 slots are numbered in order, and block c takes the range
 // [c * T / n, (c + 1) * T / n) of them.  A row that lies in one block is
@@ -70,6 +77,7 @@ constexpr int kJoin = 32;        // shares that one block joins at most
 constexpr float kSlack = 8.f;    // p <= 2^(kSlack + kBias) = 2^15: within f16's range
 constexpr float kBias = 7.f;     // and f16's smallest step, 2^-24, is 2^-31 of the largest p
 constexpr int kRingBytes = 192 * 1024;
+constexpr int kFold = 8;         // tiles of a softmax group that O adds up before it is put aside
 
 __device__ __forceinline__ uint16_t from_float(float x, int bf16) {
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
@@ -229,9 +237,11 @@ struct Shape {
     static constexpr int kM = DP == 64 ? 64 : 128;        // rows of one second product
     static constexpr int kOBlocks = kParts;
     // Tensor memory columns: two S buffers of 16, then O of each softmax
-    // group for this row, and of both for the row before.
+    // group for this row, and of both for the row before, then what is put
+    // aside of the same four.
     static constexpr int kTmemS = 0, kTmemO = 32, kOCols = kOBlocks * kPCols;
-    static constexpr int kTmemCols = 32 + 4 * kOCols <= 128 ? 128 : 32 + 4 * kOCols <= 256 ? 256 : 512;
+    static constexpr int kTmemF = kTmemO + 4 * kOCols, kFCols = kOBlocks * GP, kTmemEnd = kTmemF + 4 * kFCols;
+    static constexpr int kTmemCols = kTmemEnd <= 128 ? 128 : kTmemEnd <= 256 ? 256 : 512;
     static constexpr size_t kSmem = 1024 + kRingBytes + 2 * kQBytes + 2 * kPBytes;
     // Barriers, by their place in bars[].
     static constexpr int kFullK = 0, kFullV = kRing, kEmptyK = 2 * kRing, kEmptyV = 3 * kRing, kSFull = 4 * kRing,
@@ -318,6 +328,32 @@ __device__ __forceinline__ void split(const float (&p)[N], uint32_t* words) {
 #pragma unroll
     for (int i = 0; i < (TERMS * N + 1) / 2; ++i) words[i] = (uint32_t)e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
 }
+
+// The columns of STEP heads of a product with P, all TERMS of them; one head's
+// lie side by side.  Ready after tmem_wait_ld().
+template <int TERMS, int GP, int STEP>
+struct Terms {
+    float v[TERMS * STEP < 4 ? 4 : TERMS * STEP];
+    __device__ __forceinline__ void load(uint32_t at) {
+        if constexpr (GP == 1) {
+            tmem_ld<4>(at, v);
+        } else {
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) tmem_ld<STEP>(at + t * GP, v + t * STEP);
+        }
+    }
+    static __device__ __forceinline__ void clear(uint32_t at) {
+        constexpr int N = GP == 1 ? 4 : STEP;
+        const float zeros[N] = {};
+#pragma unroll
+        for (int t = 0; t < (GP == 1 ? 1 : TERMS); ++t) tmem_st<N>(at + t * GP, zeros);
+    }
+    // Head i's sum; float16 has two terms.
+    __device__ __forceinline__ float sum(int i, int bf16) const {
+        const float x = v[i] + v[STEP + i];
+        return TERMS == 3 && bf16 ? x + v[(TERMS - 1) * STEP + i] : x;
+    }
+};
 
 // N consecutive floats, as wide as they come.
 template <int N>
@@ -493,6 +529,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
     __shared__ float red[2][4][GP];                        // of each softmax group and its warps
     __shared__ __align__(16) float each[2][2][kRow];       // two numbers of each head for the group's threads
     __shared__ float told_m[4][GP], told_l[4][4][GP];      // what one group tells the other at a row's end
+    __shared__ bool told_aside[4];
     __shared__ float2 joined[2][GP];
     __shared__ unsigned arrived[2];
     __shared__ int issued[3];  // parts of keys and of values that were asked for, and queries
@@ -745,6 +782,8 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
             const int heads = min(GP, p.group - x.part * GP);
             const int tile0 = w.s + it0;
             const uint32_t my_o = my_tmem + S::kTmemO + ((piece & 1) * 2 + group) * S::kOCols;
+            const uint32_t my_f = my_tmem + S::kTmemF + ((piece & 1) * 2 + group) * S::kFCols;
+            bool aside = false;  // whether the columns beside O hold something
             const int k0 = (it0 ^ group) & 1;
 #pragma unroll 1
             for (int k = k0; k < n; k += 2) {
@@ -767,9 +806,10 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                         e[g] = fmaf(s[g], c, offset[g]);
                         top = fmaxf(top, e[g]);
                     }
-                    over = bar_any(1 + group, kSoftmax, (top > kSlack + kBias && me < valid) || !ok);
+                    const bool due = (k >> 1) % kFold == 0;
+                    over = bar_any(1 + group, kSoftmax, (top > kSlack + kBias && me < valid) || due || !ok);
                 }
-                // Some score has passed the reference by kSlack, or there is no reference yet.
+                // Some score has passed the reference by kSlack, there is no reference yet, or O has added up enough.
                 if (over) {
                     leave = bar_any(1 + group, kSoftmax, !ok);
                     if (leave) break;
@@ -800,21 +840,23 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                         ok = wait(S::kPFree + group, ((it >> 1) & 1) ^ 1);  // the group's tile before is in O
                         __syncwarp();
                         tc_fence_after();
-                        constexpr int kStep = GP < 8 ? 4 : 8;
+                        constexpr int kStep = GP < 8 ? GP : 8;
 #pragma unroll
-                        for (int o = 0; o < S::kOBlocks; ++o) {
+                        for (int j = 0; j < S::kFCols; j += kStep) {
+                            Terms<S::kTerms, GP, kStep> v;
+                            float sum[kStep] = {};
+                            const uint32_t at = my_o + j / GP * S::kPCols + j % GP;
+                            v.load(at);
+                            if (aside) tmem_ld<kStep>(my_f + j, sum);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < S::kTerms * GP; j += kStep) {
-                                float v[kStep];
-                                const uint32_t at = my_o + o * S::kPCols + j;
-                                tmem_ld<kStep>(at, v);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < kStep; ++i) v[i] *= f[(j + i) % GP];
-                                tmem_st<kStep>(at, v);
-                                tmem_wait_st();
-                            }
+                            for (int i = 0; i < kStep; ++i)
+                                sum[i] = (sum[i] + v.sum(i, p.c.bf16)) * f[(j + i) % GP];
+                            tmem_st<kStep>(my_f + j, sum);
+                            v.clear(at);
                         }
+                        tmem_wait_st();
+                        aside = true;
                         tc_fence_before();
                     }
                 }
@@ -883,6 +925,7 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 if ((final_it & 1) != group) {
                     if ((lane & (32 / GP - 1)) == 0) told_l[slot4][quarter][warp_head<GP>(lane)] = sum;
                     if (me < GP) told_m[slot4][me] = my_m;
+                    if (me == 0) told_aside[slot4] = aside;
                 } else {
                     ok = ok && wait(S::kTold + slot4, (piece >> 2) & 1);
                     ok = ok && wait(S::kPFree + group, (final_it >> 1) & 1);  // and all products before it
@@ -939,40 +982,37 @@ kv_attend_kernel(const __grid_constant__ AttendArgs p, const __grid_constant__ C
                 constexpr int kStep = GP < 8 ? GP : 8;
 #pragma unroll
                 for (int j = 0; j < GP; j += kStep) {
-                    // The columns of P's numbers in this group's O, then in the other's.
-                    float v[2 * S::kTerms][kStep], fa[kStep], fb[kStep];
-                    const uint32_t at = my_o + o * S::kPCols + j;
-                    const uint32_t other = group == 0 ? at + S::kOCols : at - S::kOCols;
-#pragma unroll
-                    for (int t = 0; t < S::kTerms; ++t) tmem_ld<kStep>(at + t * GP, v[t]);
-                    if (n > 1)
-#pragma unroll
-                        for (int t = 0; t < S::kTerms; ++t) tmem_ld<kStep>(other + t * GP, v[S::kTerms + t]);
+                    // This group's O, what it put aside, and the same of the other.
+                    Terms<S::kTerms, GP, kStep> own, other;
+                    float own_f[kStep] = {}, other_f[kStep] = {}, v[kStep], fa[kStep], fb[kStep];
+                    const uint32_t at = my_o + o * S::kPCols + j, at_f = my_f + o * GP + j;
+                    const int away = group == 0 ? 1 : -1;
+                    own.load(at);
+                    if (aside) tmem_ld<kStep>(at_f, own_f);
+                    if (n > 1) {
+                        other.load(at + away * S::kOCols);
+                        if (told_aside[slot4]) tmem_ld<kStep>(at_f + away * S::kFCols, other_f);
+                    }
                     load_row<kStep>(first_of + j, fa);
                     load_row<kStep>(second_of + j, fb);
                     tmem_wait_ld();
-                    auto sum_of = [&](int t, int i) {
-                        float x = v[t][i] + v[t + 1][i];
-                        if (S::kTerms == 3 && p.c.bf16) x += v[t + S::kTerms - 1][i];  // float16 has two
-                        return x;
-                    };
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
                         // A factor that has come down to 0 still lets a value that is not finite through.
-                        float x = sum_of(0, i) * fa[i];
-                        if (n > 1) x += sum_of(S::kTerms, i) * fb[i];
-                        v[0][i] = fa[i] < 0.f ? 0.f : x;
+                        v[i] = (own_f[i] + own.sum(i, p.c.bf16)) * fa[i];
+                        if (n > 1) v[i] += (other_f[i] + other.sum(i, p.c.bf16)) * fb[i];
+                        if (fa[i] < 0.f) v[i] = 0.f;
                     }
                     if (whole) {
                         uint16_t* to = p.a.out + (size_t)(q0 + j) * p.c.dim + d;
 #pragma unroll
                         for (int i = 0; i < kStep; ++i)
-                            if (in && j + i < heads) to[i * p.c.dim] = from_float(v[0][i], p.c.bf16);
+                            if (in && j + i < heads) to[i * p.c.dim] = from_float(v[i], p.c.bf16);
                     } else {
                         float* to = p.part_o + ((size_t)share * GP + j) * p.c.dim + d;
 #pragma unroll
                         for (int i = 0; i < kStep; ++i)
-                            if (in && j + i < heads) to[i * p.c.dim] = v[0][i];
+                            if (in && j + i < heads) to[i * p.c.dim] = v[i];
                     }
                 }
             }

@@ -91,7 +91,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float* r) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const float* r) {
-    static_assert(N == 4 || N == 8, "columns");
+    static_assert(N == 1 || N == 4 || N == 8, "columns");
+    if constexpr (N == 1)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"f"(r[0]), "r"(addr) : "memory");
     if constexpr (N == 4)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"f"(r[0]), "f"(r[1]), "f"(r[2]),
                      "f"(r[3]), "r"(addr)
