@@ -542,6 +542,26 @@ def test_what_is_written_says_so(tk):
     assert not got.requires_grad
 
 
+@pytest.mark.parametrize("name", ["weight", "weight_out", "out", "lse"])
+def test_what_is_no_tensor_is_refused(tk, name):
+    c = decoder(2, 40, 2, 2, 64)
+    given = dict(weight=c["weight"], weight_out=torch.zeros_like(c["weight"]), out=torch.zeros_like(c["q"]),
+                 lse=torch.zeros(2, 4, device="cuda"))
+    for bad in (5, "x", [1.0], c["q"].cpu().numpy()):
+        with pytest.raises(TypeError, match=name):
+            tk.kv_attend(c["q"], c["k"], c["v"], c["table"], c["lens"], **dict(given, **{name: bad}))
+    for i in range(4):
+        args = [c["k"], c["v"], c["table"], c["lens"], c["weight"], c["pos"], c["lens"]]
+        args[i] = 5
+        with pytest.raises(TypeError):
+            tk.kv_evict(*args, 16)
+    for key in ("weight", "pos", "next_pos", "starts"):
+        extra = dict(weight=c["weight"], pos=c["pos"], next_pos=c["lens"])
+        extra[key] = 5
+        with pytest.raises(TypeError, match=key):
+            tk.kv_append(c["k"], c["v"], c["table"], c["lens"], c["q"][:, :2], c["q"][:, :2], **extra)
+
+
 def test_an_empty_batch_is_nothing_to_do(tk):
     cache = _kv.Cache([40], 2, 64, 16, torch.float16, "head", seed=39)
     k, v, table, lens = cache.dev()

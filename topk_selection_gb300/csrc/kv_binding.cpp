@@ -157,7 +157,7 @@ struct Stream {
     }
 };
 
-// Refuses arguments that autograd follows: these operators have no backward
+// Refuses arguments (tensors or None, looked at before) that autograd follows: these operators have no backward
 // pass, and results without a history would pass for constants.
 void check_grad(const char* name, std::initializer_list<PyObject*> tensors) {
     if (!c10::GradMode::is_enabled()) return;
@@ -246,7 +246,6 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const topk_kv_rows weight = rows(a[6], "weight", at::kFloat, c);
         const topk_kv_rows weight_out = a[7] == Py_None ? weight : rows(a[7], "weight_out", at::kFloat, c);
         const Stream s(a[10], c);
-        check_grad("kv_attend", {a[0], a[1], a[2], a[6], a[7], a[8], a[9]});
         const at::Tensor out = a[8] != Py_None
                                    ? tensor(a[8], "out", c.type, c.device, {c.c.seqs, q_heads, c.c.dim})
                                    : at::Tensor(at::detail::empty_cuda({c.c.seqs, q_heads, c.c.dim}, c.type, c.device,
@@ -256,6 +255,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                                                    c.device, std::nullopt));
         if (!out.is_contiguous() || !lse.is_contiguous())
             raise(PyExc_ValueError, "out and lse must be contiguous");
+        check_grad("kv_attend", {a[0], a[1], a[2], a[6], a[7], a[8], a[9]});
         const int rc = c.c.seqs == 0 ? (int)TOPK_OK : call(c, [&] {  // an empty batch: nothing to do
             return g_attend(&c.c, q.const_data_ptr(), qs, (int)q_heads, (float)scale, out.data_ptr(),
                             static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s.handle);
