@@ -16,14 +16,14 @@
 //
 // Softmax is one pass.  p = 2^(s * scale * log2(e) - m + kBias), where m is a
 // reference that moves only when some score passes it by kSlack (a factor
-// 2^kSlack, far from float32's range), so that O is hardly ever rescaled.  P
-// enters the second product as a sum of 16-bit numbers, each what the ones
-// before it left, which the product adds up in columns of their own: two
-// numbers of float16 (22 bits), three of bfloat16 (24: all of float32's).
-// The product is far from its rate, so further columns cost what it takes to
-// split and store P.  Only 9 to 16 bfloat16 heads at once stay at two
-// numbers, 16 bits: their 48 columns would take P's buffers from 16 to 32 KB,
-// and the rings fill the shared memory.
+// 2^kSlack, far from float32's range), which is hardly ever.  P enters the
+// second product as a sum of 16-bit numbers, each what the ones before it
+// left, which the product adds up in columns of their own: two numbers of
+// float16 (22 bits), three of bfloat16 (24: all of float32's).  The product is
+// far from its rate, so further columns cost what it takes to split and store
+// P.  Only 9 to 16 bfloat16 heads at once stay at two numbers, 16 bits: their
+// 48 columns would take P's buffers from 16 to 32 KB, and the rings fill the
+// shared memory.
 //
 // The tensor core adds to O in float32, but not to nearest: over a long row
 // the error grows with its slots (16384 of them in one block: 7e-6 of O, and
