@@ -507,8 +507,7 @@ def test_side_arrays_that_lie_between_one_another(tk):
 
 
 def test_what_is_written_says_so(tk):
-    """Tensors that an operator writes count a change, as for torch's own; outputs without a gradient do not pretend
-    to have one."""
+    """Tensors that an operator writes count a change, as for torch's own."""
     cache = _kv.Cache([40, 30], 2, 64, 16, torch.float16, "head", room=4, seed=38)
     k, v, table, lens = cache.dev()
     q = torch.randn(2, 4, 64, device="cuda").half()
@@ -533,13 +532,53 @@ def test_what_is_written_says_so(tk):
     assert all(a > b for a, b in zip(versions(k, v, weight, pos, lens), before))
     with torch.inference_mode():
         tk.kv_attend(q.clone(), k, v, table, lens, weight=torch.zeros_like(weight))
-    with pytest.raises(RuntimeError, match="no gradient"):
-        tk.kv_attend(q.clone().requires_grad_(), k, v, table, lens)
-    with pytest.raises(RuntimeError, match="no gradient"):
-        tk.kv_append(k, v, table, lens, new.clone().requires_grad_(), new)
+
+
+def test_gradients_that_there_are_not(tk):
+    """Calls that autograd follows run, and say so: at the backward pass, by a warning, or at once where a tensor that
+    requires grad would be written."""
+    import warnings
+
+    c = decoder(2, 40, 2, 2, 64)
+    rest = c["k"], c["v"], c["table"], c["lens"]
+    want, want_lse = tk.kv_attend(c["q"], *rest)
+    assert not want.requires_grad
+    q = c["q"].clone().requires_grad_()
+    for of in (0, 1):
+        got = tk.kv_attend(2 * q / 2, *rest, weight=c["weight"].clone())
+        assert got[0].requires_grad and got[1].requires_grad and torch.equal(got[0], want)
+        with pytest.raises(RuntimeError, match="kv_attend is not implemented"):
+            got[of].float().sum().backward()
+    k = c["k"].clone().requires_grad_()
+    out, _ = tk.kv_attend(c["q"], k, *rest[1:])
+    with pytest.raises(RuntimeError, match="kv_attend is not implemented"):
+        out.float().sum().backward()
     with torch.no_grad():
-        got, _ = tk.kv_attend(q.clone().requires_grad_(), k, v, table, lens)
-    assert not got.requires_grad
+        got, _ = tk.kv_attend(q, *rest, out=torch.empty_like(want))
+    assert not got.requires_grad and torch.equal(got, want)
+    for given in (dict(out=torch.empty_like(want)), dict(lse=torch.empty_like(want_lse))):
+        with pytest.raises(RuntimeError, match="no gradient"):
+            tk.kv_attend(q, *rest, **given)
+    new = c["q"][:, :2].clone()
+    lens = c["lens"] - 1
+    with pytest.warns(UserWarning, match="no gradient"):
+        tk.kv_append(rest[0], rest[1], c["table"], lens, new.clone().requires_grad_(), new)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        tk.kv_append(rest[0], rest[1], c["table"], lens, new, new)
+        with torch.no_grad():
+            tk.kv_append(rest[0], rest[1], c["table"], lens, new.clone().requires_grad_(), new)
+        with pytest.raises(UserWarning):
+            tk.kv_append(rest[0], rest[1], c["table"], lens, new, new.clone().requires_grad_())
+    followed = c["weight"].clone().requires_grad_()
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tk.kv_attend(c["q"], *rest, weight=followed)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tk.kv_append(k, rest[1], c["table"], lens, new, new)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tk.kv_evict(*rest, followed, c["pos"], c["lens"], 16)
+    given = dict(weight_out=c["weight"].clone(), pos_out=c["pos"].clone(), lens_out=c["lens"].clone())
+    tk.kv_evict(*rest, followed, c["pos"], c["lens"], 16, **given)  # only read
 
 
 @pytest.mark.parametrize("name", ["weight", "weight_out", "out", "lse"])

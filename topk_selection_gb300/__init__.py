@@ -421,8 +421,8 @@ def kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                       written at the new slots
 
     lens is not changed: add the tokens' numbers to it afterwards.  Like the
-    other two operators it has no gradient: arguments that require grad are
-    refused outside torch.no_grad()."""
+    other two operators it has no gradient: tensors that are written must not
+    require grad, and it warns where k_new or v_new do (use torch.no_grad())."""
     rc = _kv.append(k_pages, v_pages, table, lens, k_new, v_new, starts, weight, pos, next_pos, _kv_stream(stream))
     if rc != TOPK_OK:
         raise TopKError(rc, "topk_kv_append")
@@ -440,7 +440,8 @@ def kv_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, tab
     defaults to dim ** -0.5.  With weight (float32 [seqs, heads, slots]), the
     attention that each slot gets, summed over its query heads, is added to it
     and written to weight_out (default: weight itself).  out and lse belong to
-    the stream of the call, as if made with it as the current one."""
+    the stream of the call, as if made with it as the current one.  A backward
+    pass that reaches them raises: there is none."""
     got = _kv.attend(q, k_pages, v_pages, table, lens, scale, weight, weight_out, out, lse, _kv_stream(stream))
     if type(got) is int:
         raise TopKError(got, "topk_kv_attend")

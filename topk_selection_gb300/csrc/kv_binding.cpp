@@ -10,6 +10,9 @@
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -157,15 +160,21 @@ struct Stream {
     }
 };
 
-// Refuses arguments (tensors or None, looked at before) that autograd follows: these operators have no backward
-// pass, and results without a history would pass for constants.
-void check_grad(const char* name, std::initializer_list<PyObject*> tensors) {
-    if (!c10::GradMode::is_enabled()) return;
+// Whether autograd follows one of these (tensors or None, looked at before).
+// The operators have no backward pass.
+bool followed(std::initializer_list<PyObject*> tensors) {
+    if (!c10::GradMode::is_enabled()) return false;
     for (PyObject* o : tensors)
-        if (o != Py_None && THPVariable_Unpack(o).requires_grad())
-            raise(PyExc_RuntimeError, std::string(name) +
-                                          " has no gradient, and one of its arguments requires grad: call it under "
-                                          "torch.no_grad(), or detach() the argument");
+        if (o != Py_None && THPVariable_Unpack(o).requires_grad()) return true;
+    return false;
+}
+
+// Refuses to write what autograd follows, as torch's own operators do.
+void check_written(const char* name, std::initializer_list<PyObject*> tensors) {
+    if (followed(tensors))
+        raise(PyExc_RuntimeError, std::string(name) +
+                                      " has no gradient, and a tensor that it writes requires grad: call it under "
+                                      "torch.no_grad(), or detach() the tensor");
 }
 
 // Counts a change of tensors that a call has written, by which autograd knows
@@ -217,7 +226,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const topk_kv_rows weight = rows(a[7], "weight", at::kFloat, c), pos = rows(a[8], "pos", at::kInt, c);
         const int32_t* next_pos = ints(a[9], "next_pos", c, c.c.seqs);
         const Stream s(a[10], c);
-        check_grad("kv_append", {a[0], a[1], a[4], a[5], a[7]});
+        check_written("kv_append", {a[0], a[1], a[7]});
+        if (followed({a[4], a[5]}) &&
+            PyErr_WarnEx(PyExc_UserWarning, "kv_append has no gradient: none will reach k_new and v_new", 2) != 0)
+            throw Raised();
         if (k.size(0) == 0) return PyLong_FromLong(TOPK_OK);
         const int rc = call(c, [&] {
             return g_append(&c.c, k.const_data_ptr(), ks, v.const_data_ptr(), vs, (int)k.size(0), starts, &weight,
@@ -255,13 +267,25 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                                                                    c.device, std::nullopt));
         if (!out.is_contiguous() || !lse.is_contiguous())
             raise(PyExc_ValueError, "out and lse must be contiguous");
-        check_grad("kv_attend", {a[0], a[1], a[2], a[6], a[7], a[8], a[9]});
+        check_written("kv_attend", {a[6], a[7], a[8], a[9]});
+        const bool follow = followed({a[0], a[1], a[2]});
+        if (follow && (a[8] != Py_None || a[9] != Py_None))
+            raise(PyExc_RuntimeError, "kv_attend has no gradient, and q or the pools require grad: out and lse cannot be "
+                                      "given then");
         const int rc = c.c.seqs == 0 ? (int)TOPK_OK : call(c, [&] {  // an empty batch: nothing to do
             return g_attend(&c.c, q.const_data_ptr(), qs, (int)q_heads, (float)scale, out.data_ptr(),
                             static_cast<float*>(lse.data_ptr()), &weight, &weight_out, s.handle);
         });
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
         written({a[7] == Py_None ? a[6] : a[7], a[8], a[9]});
+        if (follow) {  // a backward pass that comes here says that there is none
+            std::shared_ptr<torch::autograd::Node> node(new torch::autograd::NotImplemented("kv_attend"),
+                                                        torch::autograd::deleteNode);
+            node->set_next_edges(torch::autograd::collect_next_edges(q, THPVariable_Unpack(a[1]),
+                                                                     THPVariable_Unpack(a[2])));
+            torch::autograd::set_history(out, node);
+            torch::autograd::set_history(lse, node);
+        }
         PyObject* pair = PyTuple_New(2);
         if (!pair) throw Raised();
         PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
@@ -282,7 +306,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            pos_out = rows(a[11], "pos_out", at::kInt, c);
         int32_t* lens_out = const_cast<int32_t*>(ints(a[12], "lens_out", c, c.c.seqs));
         const Stream s(a[13], c);
-        check_grad("kv_evict", {a[0], a[1], a[4], a[10]});
+        check_written("kv_evict", {a[0], a[1], a[10]});
         const int rc = c.c.seqs == 0 ? (int)TOPK_OK : call(c, [&] {
             return g_evict(&c.c, &weight, &pos, next_pos, budget, sink, recent, &weight_out, &pos_out, lens_out,
                            s.handle);
