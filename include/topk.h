@@ -389,6 +389,148 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
                   const struct topk_kv_rows* weight_out, const struct topk_kv_rows* pos_out, int32_t* lens_out,
                   struct CUstream_st* stream);
 
+/*
+ * How the heads of queries and keys are normed and turned by their positions:
+ * topk_kv_rotate and topk_kv_append_rotated.  For a head's elements x
+ *   y = x * rsqrt(mean(x^2) + eps) * w            with a norm, else y = x,
+ * and then for each pair p of them, (a, b), at position n
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = n * freq[p].
+ * Elements that belong to no pair stay as they are.  All in float32, rounded
+ * once at the end; an angle is right to 2^-32 turns and 2^-22 of the turns of
+ * position 2^31, whatever the position.
+ *
+ *   freq      float32[pairs], device memory: radians per position, of either
+ *             sign, below 2^16.
+ *   pairs     1 to dim / 2.
+ *   pairing   TOPK_KV_HALVES: pair p is elements p and p + pairs;
+ *             TOPK_KV_NEIGHBOURS: elements 2p and 2p + 1.
+ *   q_norm, k_norm
+ *             norm weights of the data's type, device memory, 16-byte aligned;
+ *             null: no norm.  One row of dim for all heads (stride 0), or one
+ *             for each head, the stride apart (a multiple of 8).
+ *   eps       not negative, finite.
+ */
+enum topk_kv_pairing { TOPK_KV_HALVES = 0, TOPK_KV_NEIGHBOURS = 1 };
+
+struct topk_kv_rotation {
+    const float* freq;
+    int pairs, pairing;
+    const void* q_norm;
+    int64_t q_norm_stride;
+    const void* k_norm;
+    int64_t k_norm_stride;
+    float eps;
+};
+
+/* A tensor [tokens, heads, dim]: token t, head h at t * stride[0] + h *
+ * stride[1], dim elements side by side; 16-byte aligned, strides positive
+ * multiples of 8. */
+struct topk_kv_heads {
+    void* data; /* null: absent */
+    int64_t stride[2];
+    int heads;
+};
+
+/*
+ * topk_kv_rotate -- norm and turn queries and keys that stand in no cache.
+ *
+ *   dtype     TOPK_KV_F16 or TOPK_KV_BF16, of everything but freq.
+ *   dim       a multiple of 8, at most 256.
+ *   pos       int32[tokens]: each token's position.
+ *   q, k      inputs, either may be absent; q_out, k_out: their results, of as
+ *             many heads.  An output may be its own input (the same address
+ *             and strides); otherwise it overlaps neither input nor the other
+ *             output (all may lie in one array of rows of tokens), nor itself.
+ *
+ * Device pointers; the call only enqueues, one launch.
+ */
+int topk_kv_rotate(int dtype, int tokens, int dim, const struct topk_kv_rotation* rotation, const int32_t* pos,
+                   const struct topk_kv_heads* q, const struct topk_kv_heads* k, const struct topk_kv_heads* q_out,
+                   const struct topk_kv_heads* k_out, struct CUstream_st* stream);
+
+/*
+ * topk_kv_append_rotated -- topk_kv_append with the keys normed and turned on
+ * their way to the pages, and the same tokens' queries with them.  Values are
+ * written as they are.  Token i of sequence b has the position next_pos[b] + i,
+ * or, without next_pos, that of its slot, lens[b] + i (lens as clamped).
+ *
+ *   tokens, starts, weight, pos, next_pos
+ *             as topk_kv_append's; next_pos may come without pos.
+ *   k_new, v_new
+ *             inputs of the cache's number of heads.
+ *   q, q_out  both or neither; q_out as topk_kv_rotate's, which may be q
+ *             itself, and overlaps neither k_new nor v_new.
+ *
+ * A token whose key and value are dropped (beyond the capacity, or a page that
+ * the table does not name) has its query turned all the same.  Tokens from
+ * starts[seqs] on are ignored: their rows of q_out are not touched.  One
+ * launch.
+ */
+int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_kv_rotation* rotation, int tokens,
+                           const int32_t* starts, const struct topk_kv_heads* k_new, const struct topk_kv_heads* v_new,
+                           const struct topk_kv_rows* weight, const struct topk_kv_rows* pos, const int32_t* next_pos,
+                           const struct topk_kv_heads* q, const struct topk_kv_heads* q_out,
+                           struct CUstream_st* stream);
+
+/*
+ * topk_sample_rows -- a token from each row of logits, by one uniform number
+ * per row.
+ *
+ * Order: topk_rows_f32's, -0 equal to +0 (value descending, the lower column
+ * first among equals).  With the weights w_i = exp((x_i - max) / temperature)
+ * a prefix of the order is kept, the shortest of these:
+ *   top_k  its first top_k entries; below 1, or not below cols: no limit;
+ *   top_p  the least number of entries whose weights add up to at least top_p
+ *          times those that top_k keeps; from 1 on: no limit; at least one;
+ *   min_p  the entries with w_i >= min_p (1 if it is above that); not above 0:
+ *          no limit; at least one.
+ * The token is the first entry of the order up to and with which the weights
+ * are more than u times those that are kept, and
+ *   logp = log(w_token / kept weights).
+ * Temperature 0 takes the first entry of the order, with logp 0, whatever the
+ * other parameters.  Temperatures count as 2^-60 at least and 2^60 at most.
+ * Entries of -inf are never taken.  u counts as 0 below 0, and as 1 - 2^-24
+ * from there on.
+ *
+ * A row has no distribution where a logit is NaN or +inf or all are -inf, or
+ * its temperature is negative or one of its parameters or u is NaN: its token
+ * is -1 and its logp NaN.
+ *
+ * Sums are exact sums of weights right to 2^-21.5, and where that does not
+ * tell an entry from its neighbour, of weights right to 2^-36: the token is
+ * the definition's unless u (or top_p) lies within some 2^-36 of a border.
+ * Entries below 2^-61.9 of the largest weight count as nothing.
+ *
+ *   logits   row r at r * stride elements, cols of them side by side, of
+ *            dtype TOPK_KV_F16, TOPK_KV_BF16 or TOPK_SAMPLE_F32, aligned to
+ *            their size; cols at most 2^21.
+ *   sampling one value of each parameter for all rows, or, where the pointer
+ *            is not null, an array of one per row.  The values are checked
+ *            here (TOPK_ERR_INVALID_ARG: a negative temperature, NaN).
+ *   u        float32[rows].
+ *   token    int32[rows].
+ *   logp     float32[rows].
+ *
+ * Device pointers (the struct is host memory); the call only enqueues, one
+ * launch, and has no scratch.  Equal inputs give equal outputs, bit for bit.
+ */
+enum topk_sample_dtype { TOPK_SAMPLE_F32 = 2 };
+
+struct topk_sampling {
+    float temperature;
+    const float* temperatures;
+    int top_k;
+    const int32_t* top_ks;
+    float top_p;
+    const float* top_ps;
+    float min_p;
+    const float* min_ps;
+};
+
+int topk_sample_rows(const void* logits, int dtype, int64_t stride, int rows, int cols,
+                     const struct topk_sampling* sampling, const float* u, int32_t* token, float* logp,
+                     struct CUstream_st* stream);
+
 /* Bytes of the device array that topk_i32_noalloc uses as scratch. */
 #define TOPK_NOALLOC_SCRATCH_BYTES (1u << 20)
 

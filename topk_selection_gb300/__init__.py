@@ -1,8 +1,8 @@
 """TopK selection on one GB300 (sm_103a): thin Python binding of libtopk.so.
 
 Argument marshalling only -- every step of the selection runs in the CUDA
-kernels behind the C ABI declared in include/topk.h (the key-value cache
-operators' marshalling is compiled: csrc/kv_binding.cpp).  PyTorch supplies device
+kernels behind the C ABI declared in include/topk.h (the marshalling of what a
+decoding step calls, kv_* and sample_rows, is compiled: csrc/kv_binding.cpp).  PyTorch supplies device
 memory and the current stream.  There is no CPU fallback: if the library has
 not been built, importing the binding raises.
 
@@ -12,6 +12,11 @@ not been built, importing the binding raises.
     kv_append, kv_attend, kv_evict
                             -> a decoder's paged key-value cache: append, attend
                                with accumulated weights, keep the best slots
+    kv_rotate, kv_append_rotated
+                            -> norms of queries' and keys' heads and the position
+                               rotation, by themselves or on the way to the pages
+    sample_rows             -> a token of each row of logits: temperature, top-k,
+                               top-p, min-p
 
 The first two accept CUDA tensors (asynchronous on the current stream) or CPU tensors
 (the library stages them through device memory and returns when done).
@@ -30,12 +35,14 @@ __all__ = ["topk_i32", "topk_rows_f32", "topk_i32_ptr", "topk_rows_f32_ptr", "To
            "status_string", "release_workspace", "launch_count", "last_cuda_error", "library_path",
            "check_stream", "set_option", "OPT_STAGE2_CAP", "OPT_RADIX_CAP", "OPT_RADIX_SAMPLE_RANK",
            "reduce", "reduce_ptr", "REDUCE_OPS", "topk_items_f32", "topk_items_f32_ptr", "sort_u32",
-           "sort_u32_ptr", "kv_append", "kv_attend", "kv_evict", "KV_MAX_DIM"]
+           "sort_u32_ptr", "kv_append", "kv_attend", "kv_evict", "KV_MAX_DIM", "kv_rotate", "kv_append_rotated",
+           "sample_rows", "SAMPLE_MAX_COLS"]
 
 MAX_K = 131072      # topk_i32, topk_u32, topk_f32
 NOALLOC_MAX_K = 32768  # topk_i32_noalloc
 MAX_K_ROWS = 1024   # topk_rows_f32
-KV_MAX_DIM = 256    # kv_append, kv_attend, kv_evict
+KV_MAX_DIM = 256    # the kv_ operators
+SAMPLE_MAX_COLS = 1 << 21  # sample_rows
 (TOPK_OK, TOPK_ERR_INVALID_ARG, TOPK_ERR_UNSUPPORTED, TOPK_ERR_NO_MEMORY, TOPK_ERR_CUDA,
  TOPK_ERR_DEVICE_TIMEOUT) = range(6)
 
@@ -105,6 +112,12 @@ def _load():
     lib.topk_kv_attend.restype = ci
     lib.topk_kv_evict.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, vp]
     lib.topk_kv_evict.restype = ci
+    lib.topk_kv_rotate.argtypes = [ci, ci, ci, vp, vp, vp, vp, vp, vp, vp]
+    lib.topk_kv_rotate.restype = ci
+    lib.topk_kv_append_rotated.argtypes = [vp, vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.topk_kv_append_rotated.restype = ci
+    lib.topk_sample_rows.argtypes = [vp, ci, ctypes.c_int64, ci, ci, vp, vp, vp, vp, vp]
+    lib.topk_sample_rows.restype = ci
     lib.topk_last_launch_early.argtypes = []
     lib.topk_last_launch_early.restype = ci
     return lib
@@ -380,8 +393,8 @@ def reduce(x: torch.Tensor, op: str, out: torch.Tensor | None = None, stream=Non
 
 
 class _KvBinding:
-    """The compiled module that marshals the key-value cache operators' tensors.  Loaded by their first call: the other
-    operators need only the library, whatever torch it was built beside."""
+    """The compiled module that marshals the tensors of the key-value cache operators and sample_rows.  Loaded by their
+    first call: the other operators need only the library, whatever torch it was built beside."""
 
     def __getattr__(self, name):
         path = _build.binding_path()
@@ -391,8 +404,9 @@ class _KvBinding:
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (_lib.topk_kv_append, _lib.topk_kv_attend, _lib.topk_kv_evict)))
-        for f in ("append", "attend", "evict"):
+                      for f in (_lib.topk_kv_append, _lib.topk_kv_attend, _lib.topk_kv_evict, _lib.topk_kv_rotate,
+                                _lib.topk_kv_append_rotated, _lib.topk_sample_rows)))
+        for f in ("append", "attend", "evict", "rotate", "append_rotated", "sample"):
             setattr(self, f, getattr(module, f))  # found without this function from now on
         return getattr(module, name)
 
@@ -467,6 +481,76 @@ def kv_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, 
     if rc != TOPK_OK:
         raise TopKError(rc, "topk_kv_evict")
     return weight_out, pos_out, lens_out
+
+
+def kv_rotate(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, freq: torch.Tensor,
+              q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+              pairing: str = "halves", q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+              stream=None):
+    """Norms of queries' and keys' heads and their rotation by position, in one
+    pass: (q_out, k_out) -- topk_kv_rotate in include/topk.h.
+
+    q, k            [tokens, heads, dim] float16 or bfloat16, any strides of 16
+                    bytes (views of one fused projection); either may be None
+    pos             int32 [tokens], each token's position
+    freq            float32 [pairs]: pair p is turned by pos * freq[p] radians,
+                    right at any position; elements past 2 * pairs stay
+    q_norm, k_norm  weights of x * rsqrt(mean(x^2) + eps) * w, [dim] or
+                    [heads, dim], of q's type; None: no norm
+    pairing         "halves": elements p and p + pairs; "neighbours": 2p, 2p + 1
+    q_out, k_out    default to new tensors of the call's stream; may be q and k
+                    themselves
+
+    A backward pass that reaches them raises: there is none."""
+    got = _kv.rotate(q, k, pos, freq, q_norm, k_norm, eps, pairing, q_out, k_out, _kv_stream(stream))
+    if type(got) is int:
+        raise TopKError(got, "topk_kv_rotate")
+    return got
+
+
+def kv_append_rotated(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      k_new: torch.Tensor, v_new: torch.Tensor, freq: torch.Tensor,
+                      starts: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                      pos: torch.Tensor | None = None, next_pos: torch.Tensor | None = None,
+                      k_norm: torch.Tensor | None = None, eps: float = 1e-6, pairing: str = "halves",
+                      q: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None, stream=None):
+    """kv_append with the keys normed and rotated on their way to the pages, and
+    the same tokens' queries with them: q_out, None without q --
+    topk_kv_append_rotated in include/topk.h.
+
+    Arguments are kv_append's and kv_rotate's.  Token i of sequence b is at
+    position next_pos[b] + i, or, without next_pos, lens[b] + i: once a cache
+    has been evicted from, positions run ahead of the slots.  next_pos may come
+    without pos.  Like kv_append it has no gradient: it warns where k_new, v_new
+    or k_norm require grad, and a backward pass that reaches q_out raises."""
+    got = _kv.append_rotated(k_pages, v_pages, table, lens, k_new, v_new, freq, starts, weight, pos, next_pos, k_norm,
+                             eps, pairing, q, q_norm, q_out, _kv_stream(stream))
+    if type(got) is int:
+        raise TopKError(got, "topk_kv_append_rotated")
+    return got
+
+
+def sample_rows(logits: torch.Tensor, u: torch.Tensor, temperature: float | torch.Tensor = 1.0,
+                top_k: int | torch.Tensor = 0, top_p: float | torch.Tensor = 1.0, min_p: float | torch.Tensor = 0.0,
+                token: torch.Tensor | None = None, logp: torch.Tensor | None = None, stream=None):
+    """A token from each row of logits, by one uniform number per row: (token
+    int32 [rows], logp float32 [rows]) -- topk_sample_rows in include/topk.h.
+
+    logits is [rows, cols] float16, bfloat16 or float32 with contiguous rows, u
+    float32 [rows] in [0, 1).  In the order of topk_rows_f32 (ties: the lower
+    column) the kept entries are the shortest of: the first top_k; the least
+    number with top_p of their weight; those with at least min_p of the largest
+    weight.  The token is the first whose running weight passes u times the
+    kept weight, logp the logarithm of its share of it.  Each parameter is one
+    number, or a tensor of one per row (float32; top_k int32).  Temperature 0
+    takes the best token, with logp 0.  A row without a distribution (NaN, +inf,
+    nothing above -inf) gives token -1 and logp NaN.  logp has no gradient: a
+    backward pass that reaches it raises."""
+    got = _kv.sample(logits, u, temperature, top_k, top_p, min_p, token, logp, _kv_stream(stream))
+    if type(got) is int:
+        raise TopKError(got, "topk_sample_rows")
+    return got
 
 
 class _null:

@@ -1,5 +1,6 @@
-// Python binding of the key-value cache operators: checks of tensors and
-// marshalling into the C ABI's structures (include/topk.h), nothing else.
+// Python binding of a decoding step's operators (the key-value cache's and
+// the sampling of rows): checks of tensors and marshalling into the C ABI's
+// structures (include/topk.h), nothing else.
 //
 // A decoder calls these operators several times per token and layer, and a
 // small call takes the GPU a few microseconds.  Reading the shapes, strides
@@ -15,6 +16,9 @@
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
+#include <cstring>
 #include <exception>
 #include <initializer_list>
 #include <optional>
@@ -27,6 +31,9 @@ namespace {
 decltype(&topk_kv_append) g_append = nullptr;
 decltype(&topk_kv_attend) g_attend = nullptr;
 decltype(&topk_kv_evict) g_evict = nullptr;
+decltype(&topk_kv_rotate) g_rotate = nullptr;
+decltype(&topk_kv_append_rotated) g_append_rotated = nullptr;
+decltype(&topk_sample_rows) g_sample = nullptr;
 
 // A Python exception that is already set, on its way out.
 struct Raised {};
@@ -145,8 +152,8 @@ struct Stream {
     CUstream_st* handle;
     std::optional<c10::cuda::CUDAStreamGuard> on;
 
-    Stream(PyObject* o, const Cache& c) {
-        const c10::DeviceIndex device = c.device.index();
+    Stream(PyObject* o, const Cache& c) : Stream(o, c.device.index()) {}
+    Stream(PyObject* o, c10::DeviceIndex device) {
         if (o == Py_None) {
             handle = c10::cuda::getCurrentCUDAStream(device).stream();
             return;
@@ -202,13 +209,18 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F f) {
 }
 
 template <typename F>
-int call(const Cache& c, F f) {
-    const c10::cuda::CUDAGuard on(c.device);
+int call(c10::Device device, F f) {
+    const c10::cuda::CUDAGuard on(device);
     int rc = 0;
     Py_BEGIN_ALLOW_THREADS
     rc = f();
     Py_END_ALLOW_THREADS
     return rc;
+}
+
+template <typename F>
+int call(const Cache& c, F f) {
+    return call(c.device, f);
 }
 
 // (k_pages, v_pages, table, lens, k_new, v_new, starts, weight, pos, next_pos, stream) -> status
@@ -316,17 +328,259 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (address of topk_kv_append, of topk_kv_attend, of topk_kv_evict)
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised();
+    return v;
+}
+
+// What the two operators that rotate have in common, of `dim` elements a head.
+struct Rotation {
+    topk_kv_rotation r = {};
+
+    // A norm's weights, one row for all heads or one for each.
+    const void* norm(PyObject* o, const char* name, at::ScalarType type, c10::Device device, int64_t heads, int64_t dim,
+                     int64_t* stride) {
+        *stride = 0;
+        if (o == Py_None) return nullptr;
+        if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + " must be a torch.Tensor");
+        const bool shared = THPVariable_Unpack(o).dim() == 1;
+        const at::Tensor& t = shared ? tensor(o, name, type, device, {dim}) : tensor(o, name, type, device, {heads, dim});
+        int64_t apart[2] = {0, 0};
+        strides(t, name, apart);
+        if (!shared) *stride = t.size(0) == 1 ? 0 : apart[0];
+        return t.const_data_ptr();
+    }
+
+    Rotation(PyObject* freq, PyObject* q_norm, PyObject* k_norm, PyObject* eps, PyObject* pairing, at::ScalarType type,
+             c10::Device device, int64_t q_heads, int64_t heads, int64_t dim) {
+        const at::Tensor& f = tensor(freq, "freq", at::kFloat, device, {-1});
+        if (!f.is_contiguous()) raise(PyExc_ValueError, "freq must be contiguous");
+        if (f.size(0) < 1 || 2 * f.size(0) > dim)
+            raise(PyExc_ValueError, "freq must have 1 to dim / 2 elements, got " + std::to_string(f.size(0)));
+        r.freq = static_cast<const float*>(f.const_data_ptr());
+        r.pairs = (int)f.size(0);
+        const char* name = PyUnicode_Check(pairing) ? PyUnicode_AsUTF8(pairing) : nullptr;
+        if (name && !std::strcmp(name, "halves")) r.pairing = TOPK_KV_HALVES;
+        else if (name && !std::strcmp(name, "neighbours")) r.pairing = TOPK_KV_NEIGHBOURS;
+        else raise(PyExc_ValueError, "pairing must be \"halves\" or \"neighbours\"");
+        r.eps = (float)number(eps);
+        r.q_norm = norm(q_norm, "q_norm", type, device, q_heads, dim, &r.q_norm_stride);
+        r.k_norm = norm(k_norm, "k_norm", type, device, heads, dim, &r.k_norm_stride);
+    }
+};
+
+// A tensor [tokens, heads, dim], both of them any if below 0.
+topk_kv_heads heads_of(const at::Tensor& t, const char* name) {
+    if (t.size(1) > INT32_MAX) raise(PyExc_ValueError, std::string(name) + " has too many heads");
+    topk_kv_heads h = {const_cast<void*>(t.const_data_ptr()), {0, 0}, (int)t.size(1)};
+    strides(t, name, h.stride);
+    return h;
+}
+
+// The output of a rotation: the one given, or a new one.
+at::Tensor rotated(PyObject* o, const char* name, const at::Tensor& in) {
+    const int64_t tokens = in.size(0), heads = in.size(1), dim = in.size(2);
+    if (o == Py_None)
+        return at::Tensor(at::detail::empty_cuda({tokens, heads, dim}, in.scalar_type(), in.device(), std::nullopt));
+    return tensor(o, name, in.scalar_type(), in.device(), {tokens, heads, dim});
+}
+
+// Refuses a gradient that would get lost without a word: what a call returns
+// anew gets a backward pass that says that there is none.
+void check_followed(const char* name, const char* of, std::initializer_list<PyObject*> read,
+                    std::initializer_list<PyObject*> given) {
+    for (PyObject* o : given)
+        if (o != Py_None && followed(read))
+            raise(PyExc_RuntimeError, std::string(name) + " has no gradient, and " + of +
+                                          " require grad: outputs cannot be given then");
+}
+
+void no_backward(const char* name, std::initializer_list<PyObject*> read, std::initializer_list<const at::Tensor*> made) {
+    torch::autograd::variable_list from;
+    for (PyObject* o : read)
+        if (o != Py_None) from.push_back(THPVariable_Unpack(o));
+    std::shared_ptr<torch::autograd::Node> node(new torch::autograd::NotImplemented(name), torch::autograd::deleteNode);
+    node->set_next_edges(torch::autograd::collect_next_edges(from));
+    for (const at::Tensor* t : made)
+        if (t->defined()) torch::autograd::set_history(*t, node);
+}
+
+PyObject* wrapped(const at::Tensor& t) {
+    if (!t.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(t);
+}
+
+PyObject* two(const at::Tensor& a, const at::Tensor& b) {
+    PyObject* pair = PyTuple_New(2);
+    if (!pair) throw Raised();
+    PyTuple_SET_ITEM(pair, 0, wrapped(a));
+    PyTuple_SET_ITEM(pair, 1, wrapped(b));
+    return pair;
+}
+
+// (q, k, pos, freq, q_norm, k_norm, eps, pairing, q_out, k_out, stream) -> (q_out, k_out), or a status
+PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        PyObject* const some = a[0] != Py_None ? a[0] : a[1];
+        if (some == Py_None) raise(PyExc_ValueError, "q and k cannot both be absent");
+        if (!THPVariable_Check(some)) raise(PyExc_TypeError, "q and k must be a torch.Tensor");
+        const at::Tensor& lead = THPVariable_Unpack(some);
+        const at::ScalarType type = lead.scalar_type();
+        const c10::Device device = lead.device();
+        if (type != at::kHalf && type != at::kBFloat16)
+            raise(PyExc_TypeError, "q and k must be float16 or bfloat16 tensors");
+        if (!device.is_cuda()) raise(PyExc_ValueError, "q and k must be CUDA tensors");
+        const char* const lead_name = a[0] != Py_None ? "q" : "k";
+        tensor(some, lead_name, type, device, {-1, -1, -1});
+        const int64_t tokens = lead.size(0), dim = lead.size(2);
+        if (tokens > INT32_MAX || dim > INT32_MAX) raise(PyExc_ValueError, "too many tokens");
+        const at::Tensor q = a[0] == Py_None ? at::Tensor() : tensor(a[0], "q", type, device, {tokens, -1, dim});
+        const at::Tensor k = a[1] == Py_None ? at::Tensor() : tensor(a[1], "k", type, device, {tokens, -1, dim});
+        if ((!q.defined() && (a[4] != Py_None || a[8] != Py_None)) || (!k.defined() && (a[5] != Py_None || a[9] != Py_None)))
+            raise(PyExc_ValueError, "a norm or an output was given for what is absent");
+        const at::Tensor& pos = tensor(a[2], "pos", at::kInt, device, {tokens});
+        if (!pos.is_contiguous()) raise(PyExc_ValueError, "pos must be contiguous");
+        const Rotation rotation(a[3], a[4], a[5], a[6], a[7], type, device, q.defined() ? q.size(1) : 0,
+                                k.defined() ? k.size(1) : 0, dim);
+        const Stream s(a[10], device.index());
+        check_written("kv_rotate", {a[8], a[9]});
+        check_followed("kv_rotate", "q, k or the norms", {a[0], a[1], a[4], a[5]}, {a[8], a[9]});
+        const at::Tensor q_out = q.defined() ? rotated(a[8], "q_out", q) : at::Tensor();
+        const at::Tensor k_out = k.defined() ? rotated(a[9], "k_out", k) : at::Tensor();
+        topk_kv_heads h[4] = {};
+        if (q.defined()) {
+            h[0] = heads_of(q, "q");
+            h[2] = heads_of(q_out, "q_out");
+        }
+        if (k.defined()) {
+            h[1] = heads_of(k, "k");
+            h[3] = heads_of(k_out, "k_out");
+        }
+        const int rc = tokens == 0 ? (int)TOPK_OK : call(device, [&] {
+            return g_rotate(type == at::kBFloat16 ? TOPK_KV_BF16 : TOPK_KV_F16, (int)tokens, (int)dim, &rotation.r,
+                            static_cast<const int32_t*>(pos.const_data_ptr()), &h[0], &h[1], &h[2], &h[3], s.handle);
+        });
+        if (rc != TOPK_OK) return PyLong_FromLong(rc);
+        written({a[8], a[9]});
+        if (followed({a[0], a[1], a[4], a[5]})) no_backward("kv_rotate", {a[0], a[1], a[4], a[5]}, {&q_out, &k_out});
+        return two(q_out, k_out);
+    });
+}
+
+// (k_pages, v_pages, table, lens, k_new, v_new, freq, starts, weight, pos, next_pos, k_norm, eps, pairing, q, q_norm,
+// q_out, stream) -> q_out or None, or a status
+PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 18, [&]() -> PyObject* {
+        const Cache c = cache(a[0], a[1], a[2], a[3]);
+        const at::Tensor& k = tensor(a[4], "k_new", c.type, c.device, {-1, c.c.heads, c.c.dim});
+        const at::Tensor& v = tensor(a[5], "v_new", c.type, c.device, {k.size(0), c.c.heads, c.c.dim});
+        const int64_t tokens = k.size(0);
+        if (tokens > INT32_MAX) raise(PyExc_ValueError, "too many tokens");
+        const int32_t* starts = ints(a[7], "starts", c, (int64_t)c.c.seqs + 1);
+        if (!starts && tokens != c.c.seqs)
+            raise(PyExc_ValueError, "without starts there must be one token for each sequence");
+        if (a[9] != Py_None && a[10] == Py_None) raise(PyExc_ValueError, "pos needs next_pos");
+        const topk_kv_rows weight = rows(a[8], "weight", at::kFloat, c), pos = rows(a[9], "pos", at::kInt, c);
+        const int32_t* next_pos = ints(a[10], "next_pos", c, c.c.seqs);
+        const at::Tensor q = a[14] == Py_None ? at::Tensor() : tensor(a[14], "q", c.type, c.device, {tokens, -1, c.c.dim});
+        if (!q.defined() && (a[15] != Py_None || a[16] != Py_None))
+            raise(PyExc_ValueError, "q_norm or q_out was given without q");
+        const Rotation rotation(a[6], a[15], a[11], a[12], a[13], c.type, c.device, q.defined() ? q.size(1) : 0,
+                                c.c.heads, c.c.dim);
+        const Stream s(a[17], c);
+        check_written("kv_append_rotated", {a[0], a[1], a[8], a[16]});
+        check_followed("kv_append_rotated", "q or q_norm", {a[14], a[15]}, {a[16]});
+        const at::Tensor q_out = q.defined() ? rotated(a[16], "q_out", q) : at::Tensor();
+        if (followed({a[4], a[5], a[11]}) &&
+            PyErr_WarnEx(PyExc_UserWarning,
+                         "kv_append_rotated has no gradient: none will reach k_new, v_new and k_norm", 2) != 0)
+            throw Raised();
+        topk_kv_heads h[4] = {heads_of(k, "k_new"), heads_of(v, "v_new"), {}, {}};
+        if (q.defined()) {
+            h[2] = heads_of(q, "q");
+            h[3] = heads_of(q_out, "q_out");
+        }
+        const int rc = tokens == 0 ? (int)TOPK_OK : call(c, [&] {
+            return g_append_rotated(&c.c, &rotation.r, (int)tokens, starts, &h[0], &h[1], &weight, &pos, next_pos, &h[2],
+                                    &h[3], s.handle);
+        });
+        if (rc != TOPK_OK) return PyLong_FromLong(rc);
+        written({a[16]});
+        if (tokens) written({a[0], a[1], a[8], a[9]});
+        if (followed({a[14], a[15]})) no_backward("kv_append_rotated", {a[14], a[15]}, {&q_out});
+        return wrapped(q_out);
+    });
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, token, logp, stream) -> (token, logp), or a status
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        if (!THPVariable_Check(a[0])) raise(PyExc_TypeError, "logits must be a torch.Tensor");
+        const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
+        const c10::Device device = THPVariable_Unpack(a[0]).device();
+        if (type != at::kHalf && type != at::kBFloat16 && type != at::kFloat)
+            raise(PyExc_TypeError, "logits must be a float16, bfloat16 or float32 tensor");
+        if (!device.is_cuda()) raise(PyExc_ValueError, "logits must be a CUDA tensor");
+        const at::Tensor& x = tensor(a[0], "logits", type, device, {-1, -1});
+        const int64_t rows = x.size(0), cols = x.size(1);
+        if (rows > INT32_MAX || cols > INT32_MAX) raise(PyExc_ValueError, "logits has too many rows or columns");
+        if (cols < 1) raise(PyExc_ValueError, "logits must have a column");
+        if (cols > 1 && x.stride(1) != 1) raise(PyExc_ValueError, "the rows of logits must be contiguous");
+        auto vector = [&](PyObject* o, const char* name, at::ScalarType t) {
+            const at::Tensor& v = tensor(o, name, t, device, {rows});
+            if (!v.is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be contiguous");
+            return const_cast<void*>(v.const_data_ptr());
+        };
+        const float* u = static_cast<const float*>(vector(a[1], "u", at::kFloat));
+        topk_sampling p = {};
+        auto parameter = [&](PyObject* o, const char* name, float* one, const float** each) {
+            if (THPVariable_Check(o)) *each = static_cast<const float*>(vector(o, name, at::kFloat));
+            else *one = (float)number(o);
+        };
+        parameter(a[2], "temperature", &p.temperature, &p.temperatures);
+        if (THPVariable_Check(a[3])) p.top_ks = static_cast<const int32_t*>(vector(a[3], "top_k", at::kInt));
+        else p.top_k = integer(a[3]);
+        parameter(a[4], "top_p", &p.top_p, &p.top_ps);
+        parameter(a[5], "min_p", &p.min_p, &p.min_ps);
+        if (!p.temperatures && !(p.temperature >= 0)) raise(PyExc_ValueError, "temperature must not be negative");
+        const Stream s(a[8], device.index());
+        if (a[6] != Py_None) vector(a[6], "token", at::kInt);
+        if (a[7] != Py_None) vector(a[7], "logp", at::kFloat);
+        check_written("sample_rows", {a[7]});
+        check_followed("sample_rows", "the logits", {a[0]}, {a[7]});
+        const at::Tensor token = a[6] != Py_None ? THPVariable_Unpack(a[6])
+                                                 : at::Tensor(at::detail::empty_cuda({rows}, at::kInt, device, std::nullopt));
+        const at::Tensor logp = a[7] != Py_None ? THPVariable_Unpack(a[7])
+                                                : at::Tensor(at::detail::empty_cuda({rows}, at::kFloat, device, std::nullopt));
+        const int rc = rows == 0 ? (int)TOPK_OK : call(device, [&] {
+            return g_sample(x.const_data_ptr(),
+                            type == at::kFloat ? TOPK_SAMPLE_F32 : type == at::kBFloat16 ? TOPK_KV_BF16 : TOPK_KV_F16,
+                            rows == 1 ? std::max(cols, x.stride(0)) : x.stride(0), (int)rows, (int)cols, &p, u,
+                            static_cast<int32_t*>(token.data_ptr()), static_cast<float*>(logp.data_ptr()), s.handle);
+        });
+        if (rc != TOPK_OK) return PyLong_FromLong(rc);
+        written({a[6], a[7]});
+        if (followed({a[0]})) no_backward("sample_rows", {a[0]}, {&logp});
+        return two(token, logp);
+    });
+}
+
+// (address of topk_kv_append, of topk_kv_attend, of topk_kv_evict, of topk_kv_rotate, of topk_kv_append_rotated, of
+// topk_sample_rows)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 3, [&]() -> PyObject* {
-        void* f[3];
-        for (int i = 0; i < 3; ++i) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        void* f[6];
+        for (int i = 0; i < 6; ++i) {
             f[i] = PyLong_AsVoidPtr(a[i]);
             if (!f[i]) raise(PyExc_ValueError, "a function's address is missing");
         }
         g_append = reinterpret_cast<decltype(g_append)>(f[0]);
         g_attend = reinterpret_cast<decltype(g_attend)>(f[1]);
         g_evict = reinterpret_cast<decltype(g_evict)>(f[2]);
+        g_rotate = reinterpret_cast<decltype(g_rotate)>(f[3]);
+        g_append_rotated = reinterpret_cast<decltype(g_append_rotated)>(f[4]);
+        g_sample = reinterpret_cast<decltype(g_sample)>(f[5]);
         Py_RETURN_NONE;
     });
 }
@@ -338,6 +592,9 @@ PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
 PyMethodDef methods[] = {{"append", fast(append), METH_FASTCALL, nullptr},
                          {"attend", fast(attend), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
+                         {"rotate", fast(rotate), METH_FASTCALL, nullptr},
+                         {"append_rotated", fast(append_rotated), METH_FASTCALL, nullptr},
+                         {"sample", fast(sample), METH_FASTCALL, nullptr},
                          {"bind", fast(bind), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -88,6 +88,8 @@ int kv_spins_option();
 int kv_withhold_option();
 // TOPK_OK for device or managed memory, TOPK_ERR_INVALID_ARG for host memory.
 int device_pointer(const void* p);
+// The current device, and its number of SMs, which is asked for once.
+cudaError_t current_device(int* device, int* sms);
 // Counts n kernel launches.
 void note_launches(int n);
 
@@ -95,6 +97,26 @@ void note_launches(int n);
 cudaError_t kv_append_launch(int sms, cudaStream_t s, const KvCache& c, const uint16_t* k_new,
                              const long long* k_stride, const uint16_t* v_new, const long long* v_stride, int tokens,
                              const int* starts, KvRows<float> weight, KvRows<int> pos, const int* next_pos);
+
+struct KvRotate {
+    const uint16_t *q, *k, *v;
+    long long qs[2], ks[2], vs[2];  // elements between tokens, heads
+    uint16_t *q_out, *k_out;
+    long long qos[2], kos[2];
+    int tokens, q_heads, heads, dim;
+    int half;         // turned pairs of a head
+    bool neighbours;  // pairs of elements side by side, not half of the turned ones apart
+    const float* freq;
+    const uint16_t *q_norm, *k_norm;  // null: no norm
+    long long q_norm_stride, k_norm_stride;  // elements between heads, 0 where they share one
+    float eps, per_dim;
+    const int* pos;  // of each token; null in an append, which has what follows
+    const int *starts, *next_pos;
+    KvRows<float> weight;
+    KvRows<int> pos_rows;
+};
+// c: the cache of an append, or null.
+cudaError_t kv_rotate_launch(int sms, cudaStream_t s, const KvCache* c, const KvRotate& r, bool bf16);
 
 struct KvAttend {
     const uint16_t* q;

@@ -5,12 +5,30 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
+#include <utility>
 
 #include "../../include/topk.h"
 #include "topk_internal.h"
 #include "topk_kv.cuh"
 
+namespace topk {
+cudaError_t current_device(int* device, int* sms) {
+    static std::atomic<int> counts[64];
+    cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>* known = *device < 64 ? &counts[*device] : nullptr;
+    *sms = known ? known->load(std::memory_order_relaxed) : 0;
+    if (*sms > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
+    if (e == cudaSuccess && known) known->store(*sms, std::memory_order_relaxed);
+    return e;
+}
+}  // namespace topk
+
 namespace {
+
+using topk::current_device;
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
@@ -139,17 +157,76 @@ int on_device(std::initializer_list<const void*> ps) {
     return TOPK_OK;
 }
 
-// The current device, and its number of SMs, which is asked for once.
-cudaError_t current_device(int* device, int* sms) {
-    static std::atomic<int> counts[64];
-    cudaError_t e = cudaGetDevice(device);
-    if (e != cudaSuccess) return e;
-    std::atomic<int>* known = *device < 64 ? &counts[*device] : nullptr;
-    *sms = known ? known->load(std::memory_order_relaxed) : 0;
-    if (*sms > 0) return cudaSuccess;
-    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
-    if (e == cudaSuccess && known) known->store(*sms, std::memory_order_relaxed);
-    return e;
+bool present(const topk_kv_heads* h) { return h && h->data; }
+
+// The elements between the first of a tensor and the one behind its last.
+int64_t span(const topk_kv_heads& h, int tokens, int dim) {
+    return (tokens - 1) * h.stride[0] + (h.heads - 1) * h.stride[1] + dim;
+}
+
+bool same(const topk_kv_heads& x, const topk_kv_heads& y) {
+    return x.data == y.data && x.heads == y.heads && x.stride[0] == y.stride[0] && x.stride[1] == y.stride[1];
+}
+
+// Whether two tensors share no element: one ends before the other begins, or
+// both lie in rows of tokens of one array, in columns of their own.  Less than
+// that is not looked for.
+bool apart(const topk_kv_heads& x, const topk_kv_heads& y, int tokens, int dim) {
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.data) - reinterpret_cast<uintptr_t>(x.data));
+    const int64_t x_all = span(x, tokens, dim), y_all = span(y, tokens, dim);
+    if (d >= 2 * x_all || -d >= 2 * y_all) return true;
+    const int64_t row = x.stride[0], e = d / 2;
+    if (tokens < 2 || y.stride[0] != row || (d & 1)) return false;
+    const int64_t x_row = (x.heads - 1) * x.stride[1] + dim, y_row = (y.heads - 1) * y.stride[1] + dim;
+    const int64_t at = (e % row + row) % row;  // of y's row, behind the start of one of x's
+    return at >= x_row && at + y_row <= row;
+}
+
+// A tensor that is read; `written`: one whose heads do not lie in one another.
+int check_heads(const topk_kv_heads& h, int tokens, int dim, bool written) {
+    if (h.heads < 1 || misaligned(h.data, 16) || !strides_ok(h.stride, 2)) return TOPK_ERR_INVALID_ARG;
+    if (h.heads > (1 << 16)) return TOPK_ERR_UNSUPPORTED;
+    constexpr int64_t kMost = int64_t(1) << 44;  // elements that addresses have room for
+    if ((tokens > 1 && h.stride[0] > kMost / (tokens - 1)) || (h.heads > 1 && h.stride[1] > kMost / (h.heads - 1)))
+        return TOPK_ERR_INVALID_ARG;
+    if (!written) return TOPK_OK;
+    const int64_t t = h.stride[0], n = h.stride[1];
+    const bool one_token = tokens == 1, one_head = h.heads == 1;
+    const bool fits = ((one_head || n >= dim) && (one_token || t >= (one_head ? 0 : (h.heads - 1) * n) + dim)) ||
+                      ((one_token || t >= dim) && (one_head || n >= (one_token ? 0 : (tokens - 1) * t) + dim));
+    return fits ? TOPK_OK : TOPK_ERR_INVALID_ARG;
+}
+
+// The parts of a rotation that do not depend on the data, and its norms'.
+int check_rotation(const topk_kv_rotation* r, int dim, topk::KvRotate* out) {
+    if (!r || !r->freq || misaligned(r->freq, 4) || r->pairs < 1 || r->pairs > dim / 2) return TOPK_ERR_INVALID_ARG;
+    if (r->pairing != TOPK_KV_HALVES && r->pairing != TOPK_KV_NEIGHBOURS) return TOPK_ERR_INVALID_ARG;
+    if (!(r->eps >= 0) || !std::isfinite(r->eps)) return TOPK_ERR_INVALID_ARG;
+    for (const auto& [norm, stride] : {std::pair(r->q_norm, r->q_norm_stride), std::pair(r->k_norm, r->k_norm_stride)})
+        if (norm && (misaligned(norm, 16) || (stride != 0 && !strides_ok(&stride, 1)))) return TOPK_ERR_INVALID_ARG;
+    out->dim = dim;
+    out->half = r->pairs;
+    out->neighbours = r->pairing == TOPK_KV_NEIGHBOURS;
+    out->freq = r->freq;
+    out->q_norm = static_cast<const uint16_t*>(r->q_norm);
+    out->k_norm = static_cast<const uint16_t*>(r->k_norm);
+    out->q_norm_stride = r->q_norm_stride;
+    out->k_norm_stride = r->k_norm_stride;
+    out->eps = r->eps;
+    out->per_dim = 1.f / dim;
+    return TOPK_OK;
+}
+
+void take(const topk_kv_heads* h, const uint16_t** data, long long* strides) {
+    *data = static_cast<const uint16_t*>(h->data);
+    strides[0] = h->stride[0];
+    strides[1] = h->stride[1];
+}
+
+void take(const topk_kv_heads* h, uint16_t** data, long long* strides) {
+    *data = static_cast<uint16_t*>(h->data);
+    strides[0] = h->stride[0];
+    strides[1] = h->stride[1];
 }
 
 }  // namespace
@@ -183,6 +260,119 @@ int topk_kv_append(const struct topk_kv_cache* cache, const void* k_new, const i
                                static_cast<const uint16_t*>(v_new), vs, tokens, starts, rows_of<float>(weight),
                                rows_of<int>(pos), next_pos);
     topk::note_unreleased_launch(device, s);  // behind the launch: another thread's may have come between
+    if (e != cudaSuccess) return cuda_fail(e);
+    topk::note_launch();
+    return TOPK_OK;
+}
+
+int topk_kv_rotate(int dtype, int tokens, int dim, const struct topk_kv_rotation* rotation, const int32_t* pos,
+                   const struct topk_kv_heads* q, const struct topk_kv_heads* k, const struct topk_kv_heads* q_out,
+                   const struct topk_kv_heads* k_out, struct CUstream_st* stream) {
+    if (dtype != TOPK_KV_F16 && dtype != TOPK_KV_BF16) return TOPK_ERR_INVALID_ARG;
+    if (tokens < 0 || dim < 1 || (!present(q) && !present(k)) || present(q) != present(q_out) ||
+        present(k) != present(k_out))
+        return TOPK_ERR_INVALID_ARG;
+    if ((dim & 7) || dim > TOPK_KV_MAX_DIM) return TOPK_ERR_UNSUPPORTED;
+    topk::KvRotate r = {};
+    int rc = check_rotation(rotation, dim, &r);
+    if (rc != TOPK_OK) return rc;
+    if (tokens == 0) return TOPK_OK;
+    if (!pos || misaligned(pos, 4)) return TOPK_ERR_INVALID_ARG;
+    const topk_kv_heads* const pairs[2][2] = {{q, q_out}, {k, k_out}};
+    for (const auto& [in, out] : pairs) {
+        if (!present(in)) continue;
+        if ((rc = check_heads(*in, tokens, dim, false)) != TOPK_OK) return rc;
+        if ((rc = check_heads(*out, tokens, dim, true)) != TOPK_OK) return rc;
+        if (in->heads != out->heads || (!same(*in, *out) && !apart(*in, *out, tokens, dim)))
+            return TOPK_ERR_INVALID_ARG;
+    }
+    if (present(q) && present(k) &&
+        (!apart(*q_out, *k_out, tokens, dim) || !apart(*q_out, *k, tokens, dim) || !apart(*k_out, *q, tokens, dim)))
+        return TOPK_ERR_INVALID_ARG;
+    rc = on_device({present(q) ? q->data : nullptr, present(k) ? k->data : nullptr, present(q) ? q_out->data : nullptr,
+                    present(k) ? k_out->data : nullptr, pos, r.freq, r.q_norm, r.k_norm});
+    if (rc != TOPK_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int device = 0, sms = 0;
+    cudaError_t e = current_device(&device, &sms);
+    if (e != cudaSuccess) return cuda_fail(e);
+    r.tokens = tokens;
+    r.pos = pos;
+    if (present(q)) {
+        r.q_heads = q->heads;
+        take(q, &r.q, r.qs);
+        take(q_out, &r.q_out, r.qos);
+    } else {
+        r.q_norm = nullptr;
+    }
+    if (present(k)) {
+        r.heads = k->heads;
+        take(k, &r.k, r.ks);
+        take(k_out, &r.k_out, r.kos);
+    } else {
+        r.k_norm = nullptr;
+    }
+    e = topk::kv_rotate_launch(sms, s, nullptr, r, dtype == TOPK_KV_BF16);
+    topk::note_unreleased_launch(device, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    topk::note_launch();
+    return TOPK_OK;
+}
+
+int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_kv_rotation* rotation, int tokens,
+                           const int32_t* starts, const struct topk_kv_heads* k_new, const struct topk_kv_heads* v_new,
+                           const struct topk_kv_rows* weight, const struct topk_kv_rows* pos, const int32_t* next_pos,
+                           const struct topk_kv_heads* q, const struct topk_kv_heads* q_out,
+                           struct CUstream_st* stream) {
+    topk::KvCache c;
+    int rc = check_cache(cache, &c);
+    if (rc != TOPK_OK) return rc;
+    if (tokens < 0 || (!starts && tokens != c.seqs)) return TOPK_ERR_INVALID_ARG;
+    if ((present(pos) && !next_pos) || present(q) != present(q_out)) return TOPK_ERR_INVALID_ARG;
+    topk::KvRotate r = {};
+    if ((rc = check_rotation(rotation, c.dim, &r)) != TOPK_OK) return rc;
+    if (present(weight) && (rc = check_rows(weight, c, c.capacity())) != TOPK_OK) return rc;
+    if (present(pos) && (rc = check_rows(pos, c, c.capacity())) != TOPK_OK) return rc;
+    if (tokens == 0) return TOPK_OK;
+    if (!present(k_new) || !present(v_new) || misaligned(starts, 4) || misaligned(next_pos, 4))
+        return TOPK_ERR_INVALID_ARG;
+    if (k_new->heads != c.heads || v_new->heads != c.heads) return TOPK_ERR_INVALID_ARG;
+    if ((rc = check_heads(*k_new, tokens, c.dim, false)) != TOPK_OK ||
+        (rc = check_heads(*v_new, tokens, c.dim, false)) != TOPK_OK)
+        return rc;
+    if (present(q)) {
+        if ((rc = check_heads(*q, tokens, c.dim, false)) != TOPK_OK ||
+            (rc = check_heads(*q_out, tokens, c.dim, true)) != TOPK_OK)
+            return rc;
+        if (q->heads != q_out->heads || (!same(*q, *q_out) && !apart(*q, *q_out, tokens, c.dim)) ||
+            !apart(*k_new, *q_out, tokens, c.dim) || !apart(*v_new, *q_out, tokens, c.dim))
+            return TOPK_ERR_INVALID_ARG;
+    }
+    rc = on_device({c.k, c.v, c.table, c.lens, k_new->data, v_new->data, starts, present(weight) ? weight->data : nullptr,
+                    present(pos) ? pos->data : nullptr, next_pos, present(q) ? q->data : nullptr,
+                    present(q) ? q_out->data : nullptr, r.freq, r.q_norm, r.k_norm});
+    if (rc != TOPK_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int device = 0, sms = 0;
+    cudaError_t e = current_device(&device, &sms);
+    if (e != cudaSuccess) return cuda_fail(e);
+    r.tokens = tokens;
+    r.heads = c.heads;
+    take(k_new, &r.k, r.ks);
+    take(v_new, &r.v, r.vs);
+    if (present(q)) {
+        r.q_heads = q->heads;
+        take(q, &r.q, r.qs);
+        take(q_out, &r.q_out, r.qos);
+    } else {
+        r.q_norm = nullptr;
+    }
+    r.starts = starts;
+    r.next_pos = next_pos;
+    r.weight = rows_of<float>(weight);
+    r.pos_rows = rows_of<int>(pos);
+    e = topk::kv_rotate_launch(sms, s, &c, r, c.bf16);
+    topk::note_unreleased_launch(device, s);
     if (e != cudaSuccess) return cuda_fail(e);
     topk::note_launch();
     return TOPK_OK;
