@@ -116,7 +116,7 @@ struct KvRotate {
     KvRows<int> pos_rows;
 };
 // c: the cache of an append, or null.
-cudaError_t kv_rotate_launch(int sms, cudaStream_t s, const KvCache* c, const KvRotate& r, bool bf16);
+cudaError_t kv_rotate_launch(int device, int sms, cudaStream_t s, const KvCache* c, const KvRotate& r, bool bf16);
 
 struct KvAttend {
     const uint16_t* q;

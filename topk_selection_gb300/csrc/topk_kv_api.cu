@@ -185,7 +185,8 @@ bool apart(const topk_kv_heads& x, const topk_kv_heads& y, int tokens, int dim) 
 // A tensor that is read; `written`: one whose heads do not lie in one another.
 int check_heads(const topk_kv_heads& h, int tokens, int dim, bool written) {
     if (h.heads < 1 || misaligned(h.data, 16) || !strides_ok(h.stride, 2)) return TOPK_ERR_INVALID_ARG;
-    if (h.heads > (1 << 16)) return TOPK_ERR_UNSUPPORTED;
+    if (h.heads > (1 << 16) || tokens > (1 << 30) || h.stride[0] >= (int64_t(1) << 34) || h.stride[1] >= (int64_t(1) << 34))
+        return TOPK_ERR_UNSUPPORTED;
     constexpr int64_t kMost = int64_t(1) << 44;  // elements that addresses have room for
     if ((tokens > 1 && h.stride[0] > kMost / (tokens - 1)) || (h.heads > 1 && h.stride[1] > kMost / (h.heads - 1)))
         return TOPK_ERR_INVALID_ARG;
@@ -203,7 +204,8 @@ int check_rotation(const topk_kv_rotation* r, int dim, topk::KvRotate* out) {
     if (r->pairing != TOPK_KV_HALVES && r->pairing != TOPK_KV_NEIGHBOURS) return TOPK_ERR_INVALID_ARG;
     if (!(r->eps >= 0) || !std::isfinite(r->eps)) return TOPK_ERR_INVALID_ARG;
     for (const auto& [norm, stride] : {std::pair(r->q_norm, r->q_norm_stride), std::pair(r->k_norm, r->k_norm_stride)})
-        if (norm && (misaligned(norm, 16) || (stride != 0 && !strides_ok(&stride, 1)))) return TOPK_ERR_INVALID_ARG;
+        if (norm && (misaligned(norm, 16) || (stride != 0 && (!strides_ok(&stride, 1) || stride >= (int64_t(1) << 34)))))
+            return TOPK_ERR_INVALID_ARG;
     out->dim = dim;
     out->half = r->pairs;
     out->neighbours = r->pairing == TOPK_KV_NEIGHBOURS;
@@ -312,7 +314,7 @@ int topk_kv_rotate(int dtype, int tokens, int dim, const struct topk_kv_rotation
     } else {
         r.k_norm = nullptr;
     }
-    e = topk::kv_rotate_launch(sms, s, nullptr, r, dtype == TOPK_KV_BF16);
+    e = topk::kv_rotate_launch(device, sms, s, nullptr, r, dtype == TOPK_KV_BF16);
     topk::note_unreleased_launch(device, s);
     if (e != cudaSuccess) return cuda_fail(e);
     topk::note_launch();
@@ -371,7 +373,7 @@ int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_
     r.next_pos = next_pos;
     r.weight = rows_of<float>(weight);
     r.pos_rows = rows_of<int>(pos);
-    e = topk::kv_rotate_launch(sms, s, &c, r, c.bf16);
+    e = topk::kv_rotate_launch(device, sms, s, &c, r, c.bf16);
     topk::note_unreleased_launch(device, s);
     if (e != cudaSuccess) return cuda_fail(e);
     topk::note_launch();
