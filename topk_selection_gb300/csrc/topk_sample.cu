@@ -41,14 +41,24 @@ namespace topk {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+#ifndef SM
+#define SM 3
+#endif
+#ifndef SB
+#define SB 4
+#endif
 constexpr int kBins = 64;
-constexpr int kList = 1024;         // elements that a list has room for
+constexpr int kList = 512;          // elements that a list has room for
 constexpr int kMostBlocks = 8;      // of a cluster
 constexpr int kBits = 41;           // a weight of 1 in its octave is 2^kBits
-constexpr int kPart = 21;           // bits of a 42-bit weight that a cell adds up at a time
-constexpr int kCellAdds = 240;      // elements that a cell has room for: 240 * 2^24 < 2^32
-constexpr int kListShift = 11;      // and in a list 2^(kBits + kListShift): 1024 of them stay below 2^63
-constexpr int kMaxCols = 1 << 21;   // 2^21 weights of an octave stay below 2^63
+constexpr int kFastBits = 24;       // and a fast one 2^kFastBits
+constexpr int kListShift = 11;      // in a list 2^(kBits + kListShift): kList of them stay below 2^63
+constexpr int kMaxCols = 1 << 21;   // 2^21 weights of an octave, each below 2^(kBits + 0.5), stay below 2^63
+#ifndef SG
+#define SG 4
+#endif
+constexpr int kGroup = SG;           // vectors of a thread's group, whose largest value is kept
+constexpr int kMostFew = 512;       // top_k up to which a threshold is looked for first
 
 struct SampleArgs {
     const char* logits;
@@ -56,14 +66,20 @@ struct SampleArgs {
     int rows, cols;
     topk_sampling p;
     double log_min_p;  // of p.min_p
-    int pieces;        // of a warp's share, as many of its elements as cells have room for in each
+    int rounds;        // groups of a thread
     const float* u;
     int32_t* token;
     float* logp;
-    int fine;  // 1: 42 bits from the start
 };
 
 enum Type { kF16, kBf16, kF32 };
+
+// NaN if one is.
+__device__ __forceinline__ float larger_of(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 template <Type kType>
 struct Logit {
@@ -81,6 +97,31 @@ struct Logit {
         if constexpr (kType == kF32) return __uint_as_float(w[i]);
         else if constexpr (kType == kBf16) return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
         else return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu)));
+    }
+    // The same where i is not known to the compiler.
+    static __device__ __forceinline__ float pick(const int4& v, int i) {
+        const int k = kType == kF32 ? i : i >> 1;
+        const unsigned w = (unsigned)(k < 2 ? k == 0 ? v.x : v.y : k == 2 ? v.z : v.w);
+        if constexpr (kType == kF32) return __uint_as_float(w);
+        else return widen((Word)(i & 1 ? w >> 16 : w));
+    }
+    // The largest of a vector's values and m's, as 32 bits of the type; NaN if there is one.
+    static __device__ __forceinline__ unsigned largest(unsigned m, const int4& v) {
+        const unsigned w[4] = {(unsigned)v.x, (unsigned)v.y, (unsigned)v.z, (unsigned)v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = larger(m, w[i]);
+        return m;
+    }
+    static __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
+        if constexpr (kType == kF32) a = __float_as_uint(larger_of(__uint_as_float(a), __uint_as_float(b)));
+        else if constexpr (kType == kBf16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return a;
+    }
+    static constexpr unsigned kNothing = kType == kF32 ? kNone : kNone * 0x10001u;
+    static __device__ __forceinline__ float single(unsigned m) {
+        if constexpr (kType == kF32) return __uint_as_float(m);
+        else return larger_of(widen((Word)m), widen((Word)(m >> 16)));
     }
     // The type's values in order, numbered; -0 and +0 have a number each.
     static __device__ __forceinline__ unsigned number(float x) {
@@ -106,7 +147,7 @@ struct alignas(16) Exchange {
     unsigned long long bins[kBins];
     unsigned long long list[kList];
     int count;
-    float top;
+    float top, low;  // the largest value; the least of the threads' largest ones
 };
 
 struct Shared {
@@ -118,11 +159,37 @@ struct Shared {
     unsigned long long octave[kBins];      // weights of each octave, in its own unit
     unsigned long long before[kBins + 1];  // weights above each octave; the last one: of all
     int upper[kBins], lower[kBins];     // bounds on the number of elements down to and with each octave
-    unsigned long long table[64];       // 2^(i / 64), times 2^kBits
+    unsigned long long table[65];       // kPowers
     unsigned long long scan[kWarps];
-    float warp_top[kWarps];
+    float warp_top[kWarps], warp_low[kWarps];
     float min_from;
 };
+
+// Where a block adds up weights: [2][kBins][32] cells, a column for each lane
+// so that no two meet, a weight's upper bits in the first half and its lower
+// ones in the second; and the largest values of the threads' groups behind
+// them, [rounds][kThreads].
+constexpr int kCells = kBins * 32;
+__device__ __forceinline__ unsigned* cell_memory() {
+    extern __shared__ __align__(16) unsigned memory[];
+    return memory;
+}
+
+// 2^(i / 64 - 1/2), i from 0 to 64, times 2^kBits.
+struct Powers {
+    unsigned long long at[65];
+    constexpr Powers() : at() {
+        for (int i = 0; i < 65; ++i) {
+            double term = 1, sum = 0;
+            for (int n = 1; n < 30; ++n) {  // the series of e^((i / 64 - 1/2) ln 2)
+                sum += term;
+                term *= (i - 32) * (0.69314718055994530942 / 64) / n;
+            }
+            at[i] = (unsigned long long)(sum * (double)(1ull << kBits) + 0.5);
+        }
+    }
+};
+__constant__ const Powers kPowers;
 
 // Sums of weights are whole numbers of 2^-kBits times a weight of 1 in the
 // largest value's octave; within an octave o, of 2^-(kBits + o).
@@ -141,23 +208,22 @@ __device__ __forceinline__ Sum times(Sum a, float f, bool up) {
     return whole + (up && rest);
 }
 
-enum What { kCount, kFast, kFineHigh, kFineLow };
+enum What { kCount, kFast, kFineHigh, kFineLow };  // the last two: 28 upper and 14 lower bits of 42-bit weights
 enum By { kOctaves, kLinear, kNumbers };
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: what is added to it is rounded to a whole number
 
-// The weight of x in its octave with 42 bits: 2^f from a table of 2^(i / 64)
-// and the series of e^a for the rest, with what is lost in a sum or product
-// kept as a second number.
-__device__ __noinline__ unsigned long long fine_weight(float x, float top, float c_hi, float c_lo,
+// 2^(c (x - ref)) in its octave with 42 bits: 2^f, -1/2 <= f <= 1/2, from a
+// table and the series of e^a for the rest, with what is lost in a sum or
+// product kept as a second number.
+__device__ __forceinline__ unsigned long long fine_weight(float x, float ref, float c_hi, float c_lo,
                                                        const unsigned long long* table) {
-    const float d = x - top, v = d - x, d_lo = (x - (d - v)) - (top + v);
-    const float n = __fmaf_rd(d, c_hi, kMagic) - kMagic;
+    const float d = x - ref, n = fmaf(d, c_hi, kMagic) - kMagic;
     const float p = d * c_hi;
     const float f = p - n;
-    const float f_lo = fmaf(d, c_hi, -p) + fmaf(d, c_lo, d_lo * c_hi) + (p - (f + n));
-    const int i = min(63, (int)(f * 64.f));
-    const float r = f - i * 0.015625f;
+    const float f_lo = fmaf(d, c_hi, -p) + d * c_lo + (p - (f + n));
+    const int i = min(max((int)fmaf(f, 64.f, 32.f), 0), 64);
+    const float r = f - (i - 32) * 0.015625f;
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.9046543e-9f;
     const float a = r * kLn2, a_lo = fmaf(r, kLn2, -a) + fmaf(r, kLn2Low, f_lo * kLn2);
     const float all = a + a_lo, q = all * all * fmaf(all, fmaf(all, 1.f / 24, 1.f / 6), 0.5f);
@@ -173,55 +239,105 @@ struct Row {
     int skip, end;      // elements of the first vector before the row; skip + cols
     int v0, v1;         // this warp's vectors
     float top;          // the largest value
-    // Fast weights are 2^(c (x - ref)); ref is 0 where c * top is small enough
-    // for that, else the largest value (then what differs from it too much to
-    // be subtracted exactly has no weight).  Fine ones have ref = top.
+    // Weights are 2^(c (x - ref)).  ref is 0 where c * top is small enough for
+    // that, else the largest value: what differs from it by so much that the
+    // difference is not exact has no weight.
     float ref, c_hi, c_lo, low;  // low: what lies below it has no weight
-    int octave0;                 // bits of kMagic plus the largest value's exponent
+    int octave0;                 // bits of kMagic plus the octave of the largest value
     bool fine;
+    int rounds;             // groups of a thread
+    float* groups;          // their largest values, [rounds][kThreads]
 
+    int whole0, whole1;  // the warp's vectors that lie in the row whole; one before them and one behind may not
+
+    __device__ __forceinline__ static int4 nothing() {
+        return make_int4((int)L::kNothing, (int)L::kNothing, (int)L::kNothing, (int)L::kNothing);
+    }
+    // One of the warp's vectors; what is not the row's is -inf.
     __device__ __forceinline__ int4 load(int v) const {
-        const int at = v * L::kMany;
-        if (at >= skip && at + L::kMany <= end) return __ldg(reinterpret_cast<const int4*>(base) + v);
+        if (v >= whole0 && v < whole1) return __ldg(reinterpret_cast<const int4*>(base) + v);
         union { int4 v; typename L::Word w[L::kMany]; } r;
+        const int at = v * L::kMany;
         for (int i = 0; i < L::kMany; ++i)
             r.w[i] = at + i >= skip && at + i < end ? __ldg(reinterpret_cast<const typename L::Word*>(base) + at + i) : L::kNone;
         return r.v;
     }
-
-    // f(vector, its number) for each of the warp's vectors, by all lanes at once; what is past the end is -inf.
-    template <typename F>
-    __device__ __forceinline__ void each_vector(int from, int to, F f) const {
-        constexpr int kUnroll = 4;
-        const int lane = threadIdx.x & 31;
-        union { int4 v; typename L::Word w[L::kMany]; } none;
-        for (int i = 0; i < L::kMany; ++i) none.w[i] = L::kNone;
-        for (int v = from + lane; v - lane < to; v += 32 * kUnroll) {
-            int4 raw[kUnroll];
+    // A group's vectors, v and each 32nd after it; all loads are under way before any is waited for.
+    __device__ __forceinline__ void load_group(int v, bool on, int4 (&raw)[kGroup]) const {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) raw[u] = v + 32 * u < to ? load(v + 32 * u) : none.v;
+        for (int u = 0; u < kGroup; ++u) {
+            raw[u] = nothing();
+            if (on && v + 32 * u >= whole0 && v + 32 * u < whole1) raw[u] = __ldg(reinterpret_cast<const int4*>(base) + v + 32 * u);
+        }
+        if (v0 == whole0 && v1 == whole1) return;
+        if (on && v == v0 && v < whole0) raw[0] = load(v);
+        const int last = v1 - 1;
+        if (on && last >= whole1 && last >= v && last < v + 32 * kGroup && ((last - v) & 31) == 0) {
+            const int4 x = load(last);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) f(raw[u], v + 32 * u);
+            for (int u = 0; u < kGroup; ++u)
+                if (v + 32 * u == last) raw[u] = x;
         }
     }
+    // f(vector, its number) for the thread's vectors in rounds [from, to) whose
+    // group has a value from `least` on; what is past the row's end is -inf.
+    template <typename F>
+    __device__ __forceinline__ void each_vector(int from, int to, float least, F f) const {
+        const int lane = threadIdx.x & 31;
+        for (int i = from; i < to; ++i) {
+            const bool on = groups[i * kThreads + threadIdx.x] >= least;
+            if (!__any_sync(kFullMask, on)) continue;
+            const int v = v0 + i * (32 * kGroup) + lane;
+            int4 raw[kGroup];
+            load_group(v, on, raw);
+            if (!on) continue;
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) f(raw[u], v + 32 * u);
+        }
+    }
+    // The groups' largest values, and the thread's.
+    __device__ __forceinline__ float look_through() const {
+        const int lane = threadIdx.x & 31;
+        float all = -INFINITY;
+        for (int i = 0; i < rounds; ++i) {
+            const int v = v0 + i * (32 * kGroup) + lane;
+            int4 raw[kGroup];
+            load_group(v, true, raw);
+            unsigned m = L::kNothing;
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) m = L::largest(m, raw[u]);
+            const float x = L::single(m);
+            groups[i * kThreads + threadIdx.x] = x;
+            all = larger_of(all, x);
+        }
+        return all;
+    }
 
-    // Bits of kMagic plus the exponent of x's weight.
-    __device__ __forceinline__ float magic(float x) const { return __fmaf_rd(x - ref, c_hi, kMagic); }
+    // kMagic plus the whole number nearest to x's exponent.
+    __device__ __forceinline__ float magic(float x) const { return fmaf(x - ref, c_hi, kMagic); }
     __device__ __forceinline__ int octave(float x) const { return octave0 - __float_as_int(magic(x)); }
 
-    // The weight of x in its octave, 2^23 to 2^24.
+    // The weight of x in its octave, 2^(kFastBits - 1/2) to 2^(kFastBits + 1/2):
+    // 1 + f q(f) with q interpolating (2^f - 1) / f at Chebyshev's points, off
+    // by 2^-27.5 of it; roundings make that 2^-23.6.  (The special function unit
+    // gives 2^-22.)
     __device__ __forceinline__ unsigned fast(float x, float t) const {
-        const float d = x - ref, n = t - kMagic, f = __saturatef(fmaf(d, c_lo, fmaf(d, c_hi, -n)));
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(f));
-        return __float_as_uint(w) - 0x3F000000u;
+        const float d = x - ref, f = fmaf(d, c_lo, fmaf(d, c_hi, kMagic - t));
+        constexpr float kOne = 1 << kFastBits;
+        float q = 0.00015453163f * kOne;
+        q = fmaf(q, f, 0.0013390863f * kOne);
+        q = fmaf(q, f, 0.0096180826f * kOne);
+        q = fmaf(q, f, 0.0555035711f * kOne);
+        q = fmaf(q, f, 0.2402265076f * kOne);
+        q = fmaf(q, f, 0.6931471880f * kOne);
+        return __float2uint_rn(fmaf(q, f, kOne));
     }
-    // The same with 42 bits, 2^41 to 2^42.
-    __device__ __forceinline__ unsigned long long slow(float x, const unsigned long long* table) const {
-        return fine_weight(x, top, c_hi, c_lo, table);
+    // The same with 42 bits, 2^(kBits - 1/2) to 2^(kBits + 1/2).
+    __device__ __forceinline__ Sum slow(float x, const unsigned long long* table) const {
+        return fine_weight(x, ref, c_hi, c_lo, table);
     }
-    __device__ __forceinline__ unsigned long long weight(float x, const unsigned long long* table) const {
-        return fine ? slow(x, table) : (unsigned long long)fast(x, magic(x)) << (kBits - 23);
+    __device__ __forceinline__ Sum weight(float x, const unsigned long long* table) const {
+        return fine ? slow(x, table) : (Sum)fast(x, magic(x)) << (kBits - kFastBits);
     }
 };
 
@@ -235,14 +351,31 @@ __device__ __forceinline__ void cluster_sync(int blocks) {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// A region: the elements from `lo` to `hi`, with the weights above it, and how
-// those in it are cut into 64 bins, the largest values first.
+// A region: the elements from `lo` to `hi`, and how they are cut into 64 bins,
+// the largest values first.
 struct Region {
     float lo, hi;
     By by;
-    float scale;   // kLinear
+    float scale;      // kLinear
     unsigned number;  // kNumbers: hi's
     int shift;
+};
+
+// A prefix of the order: what is above `value`, and the first `ties` that equal it.
+struct Prefix {
+    float value;
+    int ties;
+    Sum sum;     // of its weights
+    bool exact;  // whether of 42-bit ones
+};
+
+// An element of the order: the weights before it and up to and with it, and
+// where it is: at `index` in the list, or the `index`-th that equals `value`.
+struct Place {
+    Sum before, through;
+    int index;
+    bool in_list;
+    float value;
 };
 
 template <Type kType>
@@ -250,18 +383,23 @@ struct Sampler {
     using L = Logit<kType>;
     Row<kType> row;
     Shared& s;
-    unsigned* cells;  // [kBins][kThreads]
-    int blocks, rank, turn, pieces;
+    int blocks, rank, turn = 0;
+    // The list, or, where there are too many equal elements, those: what is above them.
     int listed = 0;       // elements in the list
-    int list_octave = 0;  // the octave in which it begins
+    Sum base = 0;         // weights above the octave in which it begins, or above itself
+    int list_octave = 0;  // that octave
     Sum list_from = 0;    // weights in that octave above it
+    float list_top = 0;   // no element in between is above this one
+    bool exact = false;   // whether what is above it is known to 42 bits
+    int equal = 0;        // the number of equal elements
 
-    __device__ Sampler(Shared& s, unsigned* cells) : s(s), cells(cells) {}
+    __device__ Sampler(Shared& s) : s(s) {}
 
     __device__ __forceinline__ Exchange& mine() { return s.exchange[turn]; }
     __device__ __forceinline__ const Exchange* theirs(int r) {
         return blocks == 1 ? &s.exchange[turn] : cg::this_cluster().map_shared_rank(&s.exchange[turn], r);
     }
+    __device__ __forceinline__ Region everything() const { return {row.low, row.top, kOctaves, 0.f, 0u, 0}; }
 
     __device__ __forceinline__ int bin(const Region& g, float x) const {
         if (g.by == kOctaves) return row.octave(x);
@@ -269,53 +407,63 @@ struct Sampler {
         return (int)((g.number - L::number(x + 0.f)) >> g.shift);
     }
 
-    // Adds up `what` of the region's elements by bins over the cluster, into s.bins.
+    // Adds up `what` of the region's elements by bins over the cluster, into
+    // s.bins.  kHot: fast weights by octaves, where every element up to the top
+    // counts.
     template <bool kHot>
-    __device__ void add_up(const Region& g, What what, int shift) {
-        const int tid = threadIdx.x;
-        Sum sum = 0;  // of bin tid / 4, by a quarter of the threads
-        constexpr int step = 32 * (kCellAdds / L::kMany);  // vectors of a warp that its cells have room for
-        int from = row.v0;
-        for (int piece = 0; piece < pieces; ++piece, from += step) {
-            for (int b = 0; b < kBins; ++b) cells[b * kThreads + tid] = 0;
-            const int to = min(from + step, row.v1);
+    __device__ void add_up(const Region& g, What what) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        unsigned *high = cell_memory() + lane, *low = high + kCells;
+        // A cell has 2^21 / 8 / 32 numbers at most, below 2^14.
+        const int split = what == kFast ? kFastBits / 2 : 14;
+        row.each_vector(0, row.rounds, g.lo, [&](const int4& v, int) {
             if constexpr (kHot) {
-                row.each_vector(from, to, [&](const int4& v, int) {
 #pragma unroll
-                    for (int i = 0; i < L::kMany; ++i) {
-                        const float x = L::at(v, i);
-                        if (x >= g.lo) {
-                            const float t = row.magic(x);
-                            cells[min((unsigned)(row.octave0 - __float_as_int(t)), kBins - 1u) * kThreads + tid] += row.fast(x, t);
-                        }
+                for (int i = 0; i < L::kMany; ++i) {
+                    const float x = L::at(v, i);
+                    if (x >= g.lo) {
+                        const float t = row.magic(x);
+                        const unsigned w = row.fast(x, t), at = min((unsigned)(row.octave0 - __float_as_int(t)), kBins - 1u) * 32;
+                        atomicAdd(high + at, w >> (kFastBits / 2));
+                        atomicAdd(low + at, w & ((1u << (kFastBits / 2)) - 1));
                     }
-                });
-            } else {
-                row.each_vector(from, to, [&](const int4& v, int) {
-                    for (int i = 0; i < L::kMany; ++i) {
-                        const float x = L::at(v, i);
-                        if (x >= g.lo && x <= g.hi) {
-                            unsigned w = 1;
-                            if (what == kFast) w = row.fast(x, row.magic(x));
-                            if (what == kFineHigh) w = (unsigned)(row.slow(x, s.table) >> kPart);
-                            if (what == kFineLow) w = (unsigned)row.slow(x, s.table) & ((1u << kPart) - 1);
-                            cells[min((unsigned)bin(g, x), kBins - 1u) * kThreads + tid] += w;
-                        }
+                }
+            } else if (L::single(L::largest(L::kNothing, v)) >= g.lo) {
+#pragma unroll 1
+                for (int i = 0; i < L::kMany; ++i) {
+                    const float x = L::pick(v, i);
+                    if (!(x >= g.lo && x <= g.hi)) continue;
+                    unsigned w = 1;
+                    if (what == kFast) w = row.fast(x, row.magic(x));
+                    if (what == kFineHigh || what == kFineLow) {
+                        const Sum m = row.slow(x, s.table);
+                        w = what == kFineHigh ? (unsigned)(m >> 14) : (unsigned)m & 0x3FFFu;
                     }
-                });
+                    const unsigned at = min((unsigned)bin(g, x), kBins - 1u) * 32;
+                    atomicAdd(high + at, w >> split);
+                    atomicAdd(low + at, w & ((1u << split) - 1));
+                }
             }
-            __syncthreads();
-            const uint4* from4 = reinterpret_cast<const uint4*>(cells + (tid >> 2) * kThreads + (tid & 3) * (kThreads / 4));
-#pragma unroll 4
-            for (int i = 0; i < kThreads / 16; ++i) {
-                const uint4 q = from4[(i + tid) & (kThreads / 16 - 1)];
-                sum += (Sum)q.x + q.y + ((Sum)q.z + q.w);
-            }
-            __syncthreads();
+        });
+        __syncthreads();
+        // A bin's 32 columns by kEach threads, which leave zeros behind.
+        constexpr int kEach = kThreads / kBins, kVectors = 32 / kEach / 4;
+        Sum sum = 0;
+        uint4* mine4 = reinterpret_cast<uint4*>(cell_memory()) + tid * kVectors;
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const uint4 h = mine4[i], l = mine4[i + kCells / 4], zero = {0, 0, 0, 0};
+            sum += (((Sum)h.x + h.y + h.z + h.w) << split) + ((Sum)l.x + l.y + l.z + l.w);
+            mine4[i] = mine4[i + kCells / 4] = zero;
         }
-        sum += __shfl_xor_sync(kFullMask, sum, 1);
-        sum += __shfl_xor_sync(kFullMask, sum, 2);
-        if ((tid & 3) == 0) mine().bins[tid >> 2] = sum;
+#pragma unroll
+        for (int d = 1; d < kEach; d <<= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+        if (tid % kEach == 0) mine().bins[tid / kEach] = sum;
+        join_bins(what == kFineLow, what == kFast ? kBits - kFastBits : what == kFineHigh ? 14 : 0);
+    }
+    // The blocks' bins -> s.bins, and what is above each.  add: to what is there.
+    __device__ void join_bins(bool add, int shift) {
+        const int tid = threadIdx.x;
         cluster_sync(blocks);
         if (tid < 32) {  // two bins each
             Sum v[kMostBlocks][2] = {};
@@ -332,14 +480,24 @@ struct Sampler {
                 b0 += v[r][0];
                 b1 += v[r][1];
             }
-            b0 = (what == kFineLow ? s.bins[2 * tid] : 0) + (b0 << shift);
-            b1 = (what == kFineLow ? s.bins[2 * tid + 1] : 0) + (b1 << shift);
+            b0 = (add ? s.bins[2 * tid] : 0) + (b0 << shift);
+            b1 = (add ? s.bins[2 * tid + 1] : 0) + (b1 << shift);
             s.bins[2 * tid] = b0;
             s.bins[2 * tid + 1] = b1;
             write_scan(s.above, b0, b1);
         }
         turn ^= 1;
         __syncthreads();
+    }
+    __device__ void add_up_weights(const Region& g) {
+        if (row.fine) {
+            add_up<false>(g, kFineHigh);
+            add_up<false>(g, kFineLow);
+        } else if (g.by == kOctaves) {
+            add_up<true>(g, kFast);
+        } else {
+            add_up<false>(g, kFast);
+        }
     }
     // Sums of the bins before each: two of a lane's, by one warp.
     static __device__ void write_scan(Sum* to, Sum b0, Sum b1) {
@@ -361,16 +519,6 @@ struct Sampler {
         const Sum next = i < kBins ? sums[i + 1] : 0, all = sums[kBins];
         const int at = __syncthreads_count(i < kBins && (strict ? next <= t : next < t));
         return min(at, __syncthreads_count(i < kBins && next < all));
-    }
-    __device__ void add_up_weights(const Region& g) {
-        if (row.fine) {
-            add_up<false>(g, kFineHigh, kPart);
-            add_up<false>(g, kFineLow, 0);
-        } else if (g.by == kOctaves) {
-            add_up<true>(g, kFast, kBits - 23);
-        } else {
-            add_up<false>(g, kFast, kBits - 23);
-        }
     }
 
     // The smallest number k in [lo, hi] for which f(value of k), which is true
@@ -415,34 +563,48 @@ struct Sampler {
         while (range >> g.shift >= kBins) ++g.shift;
     }
 
-    // Collects the region's elements, at most kList, and sorts and sums them up.
-    __device__ void gather(const Region& g, int octave, Sum in_octave) {
+    // Collects the elements from lo to hi, which begin in `octave` below
+    // in_octave weights of it, and sorts and sums them up.  False, and no
+    // list, if they are more than fit.
+    __device__ bool gather(float lo, float hi, int octave, Sum in_octave) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         if (tid == 0) mine().count = 0;
         __syncthreads();
-        row.each_vector(row.v0, row.v1, [&](const int4& v, int at) {
-#pragma unroll
+        row.each_vector(0, row.rounds, lo, [&](const int4& v, int at) {
+            if (!(L::single(L::largest(L::kNothing, v)) >= lo)) return;
+#pragma unroll 1
             for (int i = 0; i < L::kMany; ++i) {
-                const float x = L::at(v, i);
-                if (x >= g.lo && x <= g.hi) {
-                    const int n = atomicAdd(&mine().count, 1);
-                    const unsigned b = __float_as_uint(x + 0.f), key = b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
-                    if (n < kList)
-                        mine().list[n] = (unsigned long long)key << 32 | ~(unsigned)(at * L::kMany + i - row.skip);
-                }
+                const float x = L::pick(v, i);
+                if (!(x >= lo && x <= hi)) continue;
+                const int n = atomicAdd(&mine().count, 1);
+                const unsigned b = __float_as_uint(x + 0.f), key = b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
+                if (n < kList)
+                    mine().list[n] = (unsigned long long)key << 32 | ~(unsigned)(at * L::kMany + i - row.skip);
             }
         });
         cluster_sync(blocks);
-        int n = 0;
-        for (int r = 0; r < blocks; ++r) {
-            const Exchange* e = theirs(r);
-            const int some = min(e->count, kList);
-            for (int i = tid; i < some; i += kThreads)
-                if (n + i < kList) s.list[n + i] = e->list[i];
-            n += some;
+        int counts[kMostBlocks], n = 0;
+#pragma unroll
+        for (int r = 0; r < kMostBlocks; ++r) counts[r] = r < blocks ? theirs(r)->count : 0;
+#pragma unroll
+        for (int r = 0; r < kMostBlocks; ++r) n += counts[r];
+        const bool fits = n <= kList;
+        if (fits) {
+            n = 0;
+#pragma unroll
+            for (int r = 0; r < kMostBlocks; ++r) {
+                if (counts[r] == 0) continue;
+                const Exchange* e = theirs(r);
+                for (int i = tid; i < counts[r]; i += kThreads) s.list[n + i] = e->list[i];
+                n += counts[r];
+            }
         }
-        n = min(n, kList);
         turn ^= 1;
+        listed = equal = 0;
+        if (!fits || n == 0) {
+            __syncthreads();
+            return false;
+        }
         const int size = next_pow2(max(n, 2));
         for (int i = n + tid; i < size; i += kThreads) s.list[i] = 0;
         block_sort_smem_desc(s.list, size);
@@ -453,7 +615,7 @@ struct Sampler {
             const int at = tid * kPer + i;
             if (at < n) {
                 const float x = listed_value(at);
-                sum += row.weight(x, s.table) << kListShift >> (row.octave(x) - octave);
+                sum += row.slow(x, s.table) << kListShift >> (row.octave(x) - octave);
             }
             own[i] = sum;
         }
@@ -474,6 +636,10 @@ struct Sampler {
         listed = n;
         list_octave = octave;
         list_from = in_octave;
+        list_top = hi;
+        exact = hi == row.top;
+        base = exact ? 0 : s.before[octave];
+        return true;
     }
     __device__ __forceinline__ float listed_value(int i) const {
         const unsigned k = (unsigned)(s.list[i] >> 32);
@@ -481,109 +647,233 @@ struct Sampler {
     }
     // Weights up to and with element i - 1 of the list.
     __device__ __forceinline__ Sum list_sum(int i) const {
-        return s.before[list_octave] + ((list_from + (i > 0 ? s.through[i - 1] >> kListShift : 0)) >> list_octave);
+        return base + ((list_from + (i > 0 ? s.through[i - 1] >> kListShift : 0)) >> list_octave);
+    }
+    // Whether the first element up to and with which the weights are more than
+    // t (strict) or not less is in the list, or one of the equal elements.
+    __device__ __forceinline__ bool holds(Sum t, bool strict) const {
+        if (listed) {
+            const Sum to = list_sum(listed);
+            return t >= list_sum(0) && (strict ? t < to : t <= to) && (strict || t > list_sum(0) || exact);
+        }
+        return equal > 0;
+    }
+    __device__ Place place(Sum t, bool strict) {
+        const Sum rel = t > base ? (t - base) << list_octave : 0, in = rel > list_from ? rel - list_from : 0;
+        if (listed) {
+            const Sum edge = in << kListShift;
+            int count = 0;
+            for (int i = threadIdx.x; i - (int)threadIdx.x < listed; i += kThreads)
+                count += __syncthreads_count(i < listed && (strict ? s.through[i] <= edge : s.through[i] < edge));
+            const int i = min(count, listed - 1);
+            return {list_sum(i), list_sum(i + 1), i, true, listed_value(i)};
+        }
+        const Sum w = exact ? row.slow(list_top, s.table) : row.weight(list_top, s.table);
+        const Sum i = min(strict ? in / w : (in > 0 ? in - 1 : 0) / w, (Sum)max(equal - 1, 0));
+        return {base + ((list_from + i * w) >> list_octave), base + ((list_from + (i + 1) * w) >> list_octave), (int)i, false,
+                list_top};
+    }
+    // The prefix up to and with a place.
+    __device__ Prefix prefix_to(const Place& p) {
+        int ties = p.index + 1;
+        if (p.in_list) {
+            ties = 0;
+            for (int i = threadIdx.x; i - (int)threadIdx.x <= p.index; i += kThreads)
+                ties += __syncthreads_count(i <= p.index && listed_value(i) == p.value);
+        }
+        return {p.value, ties, p.through, exact};
     }
 
-    // An element of the order: the weights before it and up to and with it,
-    // and where it is: at `index` in the list, or the `index`-th that equals
-    // `value`.
-    struct Place {
-        Sum before, through;
-        int index;
-        bool in_list;
-        float value;
-    };
+    // Weights lie between 2^(kBits - 1/2) and 2^(kBits + 1/2), and 2^-14 of
+    // that beside: how many of them there are at most, and at least.
+    static constexpr Sum kLightest = 1554944255987ull - (1ull << 27), kHeaviest = 3109888511976ull + (1ull << 28);
+    __device__ __forceinline__ static Sum most(Sum sum) { return sum / kLightest; }
+    __device__ __forceinline__ static Sum least(Sum sum) { return (sum + kHeaviest - 1) / kHeaviest; }
 
-    __device__ Place in_list(Sum t, bool strict) {
-        const Sum from = s.before[list_octave], rel = t > from ? (t - from) << list_octave : 0;
-        const Sum edge = rel > list_from ? (rel - list_from) << kListShift : 0;
-        int count = 0;
-        for (int i = threadIdx.x; i - (int)threadIdx.x < listed; i += kThreads)
-            count += __syncthreads_count(i < listed && (strict ? s.through[i] <= edge : s.through[i] < edge));
-        const int i = max(min(count, listed - 1), 0);
-        return {list_sum(i), list_sum(i + 1), i, true, listed_value(i)};
-    }
-
-    // The first element up to and with which the weights are more than t
-    // (strict) or not less.
-    __device__ Place find(Sum t, bool strict) {
-        if (listed && t >= list_sum(0) && t <= list_sum(listed)) return in_list(t, strict);
+    // Makes the list, or the run of equal elements, in which the first element
+    // lies up to and with which the weights are more than t (strict) or not less.
+    __device__ void look_for(Sum t, bool strict) {
         const int o = bin_of(s.before, t, strict);
-        Region g = {row.low, row.top, kOctaves, 0.f, 0u, 0};
+        Region g = everything();
         if (s.upper[o] <= kList) {  // all down to there
-            gather(part(g, 0, o), 0, 0);
-            return in_list(t, strict);
+            gather(part(g, 0, o).lo, row.top, 0, 0);
+            return;
         }
         g = part(g, o, o);
         const Sum rel = t > s.before[o] ? (t - s.before[o]) << o : 0;
-        Sum above = 0, room = most(s.octave[o]);  // both of the octave
+        narrow(g, o, s.octave[o], most(s.octave[o]), false, [&](Sum above) {
+            return bin_of(s.above, rel > above ? rel - above : 0, strict);
+        });
+    }
+    // Cuts a region of octave o, with `sum` of weights and at most `room`
+    // elements, until it fits a list or is one value.  pick(weights above):
+    // the bin to go on with; counted: the room is known by counting, and pick
+    // finds the counts in s.bins.
+    template <typename F>
+    __device__ void narrow(Region g, int o, Sum sum, Sum room, bool counted, F pick) {
+        Sum above = 0;
         for (int level = 0; room > kList && g.lo != g.hi; ++level) {
             cut(g, level);
+            int b = 0;
+            if (counted) {
+                add_up<false>(g, kCount);
+                b = pick(above);
+                room = s.bins[b];
+            }
             add_up_weights(g);
-            const int b = bin_of(s.above, rel > above ? rel - above : 0, strict);
+            if (!counted) {
+                b = pick(above);
+                room = most(s.bins[b]);
+            }
             above += s.above[b];
-            room = most(s.bins[b]);
+            sum = s.bins[b];
             g = part(g, b, b);
         }
         if (room <= kList) {
-            gather(g, o, above);
-            return in_list(t, strict);
+            gather(g.lo, g.hi, o, above);
+            return;
         }
-        return equals(g.hi, o, above, strict ? (rel > above ? rel - above : 0) / row.weight(g.hi, s.table)
-                                             : ((rel > above ? rel - above : 1) - 1) / row.weight(g.hi, s.table));
+        const Sum w = row.weight(g.hi, s.table);
+        listed = 0;
+        equal = (int)min(sum / w, (Sum)kMaxCols);
+        list_octave = o;
+        list_from = above;
+        list_top = g.hi;
+        exact = row.fine;
+        base = s.before[o];
     }
-    // The i-th, from 0, of the elements that equal x, with `above` in octave o above them.
-    __device__ Place equals(float x, int o, Sum above, Sum i) {
-        const Sum w = row.weight(x, s.table), from = s.before[o];
-        i = min(i, (Sum)kMaxCols);
-        return {from + ((above + i * w) >> o), from + ((above + (i + 1) * w) >> o), (int)i, false, x};
-    }
-    // Weights of 2^kBits at least: how many there are at most.
-    __device__ __forceinline__ static Sum most(Sum sum) { return sum / ((1ull << kBits) - (1ull << (kBits - 15))); }
 
-    // Weights of the first k elements of the order.
-    __device__ Sum first_k(int k) {
+    // The first k elements of the order.
+    __device__ Prefix first_k(int k) {
         const int reach = __syncthreads_count(threadIdx.x < kBins - 1 && s.lower[threadIdx.x] < k);  // no further than here
-        const Region all = {row.low, row.top, kOctaves, 0.f, 0u, 0};
         if (s.upper[reach] <= kList) {
-            gather(part(all, 0, reach), 0, 0);
-            return list_sum(min(k, listed));
+            gather(part(everything(), 0, reach).lo, row.top, 0, 0);
+            return prefix_of(min(k, listed));
         }
-        add_up<false>(all, kCount, 0);
-        if (s.above[kBins] <= (Sum)k) return s.before[kBins];
+        add_up<false>(everything(), kCount);
+        if (s.above[kBins] <= (Sum)k) return all();
         const int o = bin_of(s.above, k, false);
-        Sum need = k - s.above[o], room = s.bins[o], above = 0;
-        Region g = part(all, o, o);
-        for (int level = 0; room > kList && g.lo != g.hi; ++level) {
-            cut(g, level);
-            add_up<false>(g, kCount, 0);
+        Sum need = k - s.above[o], room = s.bins[o];
+        narrow(part(everything(), o, o), o, s.octave[o], room, true, [&](Sum) {
             const int b = bin_of(s.above, need, false);
             need -= s.above[b];
-            room = s.bins[b];
-            add_up_weights(g);
-            above += s.above[b];
-            g = part(g, b, b);
+            return b;
+        });
+        if (listed) return prefix_of((int)min(need, (Sum)listed));
+        const Sum w = row.weight(list_top, s.table);
+        return {list_top, (int)need, base + ((list_from + need * w) >> list_octave), row.fine};
+    }
+    __device__ Prefix prefix_of(int n) {  // of the list's first n
+        return prefix_to({list_sum(n - 1), list_sum(n), n - 1, true, listed_value(n - 1)});
+    }
+    __device__ Prefix all() const { return {-INFINITY, 0, s.before[kBins], row.fine}; }
+
+    // Weights of 42 bits of what is above x, and of a prefix.
+    __device__ void add_up_exactly(float x, Sum* above, Prefix* p) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        Sum a = 0, b = 0;
+        const float from = fmaxf(row.low, fminf(x, p->value));
+        row.each_vector(0, row.rounds, from, [&](const int4& v, int) {
+            if (!(L::single(L::largest(L::kNothing, v)) >= from)) return;
+#pragma unroll 1
+            for (int i = 0; i < L::kMany; ++i) {
+                const float y = L::pick(v, i);
+                if (!(y >= row.low && (y > x || y > p->value))) continue;
+                const int o = row.octave(y);
+                const Sum w = (row.slow(y, s.table) + ((1ull << o) >> 1)) >> o;
+                if (y > x) a += w;
+                if (y > p->value) b += w;
+            }
+        });
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            a += __shfl_xor_sync(kFullMask, a, d);
+            b += __shfl_xor_sync(kFullMask, b, d);
         }
-        if (room <= kList) {
-            gather(g, o, above);
-            return list_sum((int)min(need, (Sum)listed));
+        if (tid < kBins) mine().bins[tid] = 0;
+        __syncthreads();
+        if (lane == 0) {
+            mine().bins[2 * warp] = a;
+            mine().bins[2 * warp + 1] = b;
         }
-        return equals(g.hi, o, above, need - 1).through;
+        cluster_sync(blocks);
+        a = b = 0;
+        for (int r = 0; r < blocks; ++r) {
+            const Sum* q = theirs(r)->bins;
+            for (int w = 0; w < kWarps; ++w) {
+                a += q[2 * w];
+                b += q[2 * w + 1];
+            }
+        }
+        turn ^= 1;
+        *above = a;
+        if (!p->exact && p->ties > 0) {
+            const int o = row.octave(p->value);
+            b += (row.slow(p->value, s.table) * p->ties + ((1ull << o) >> 1)) >> o;
+        }
+        if (!p->exact) p->sum = b;
+        p->exact = true;
     }
 
-    // Weights of the values from `from` on.
-    __device__ Sum down_to(float from) {
-        if (listed && list_octave == 0 && list_from == 0 && listed_value(listed - 1) < from) {
+    // Where the weights pass `share` of a prefix: more than that (strict) or
+    // not less.  False where weights of 24 bits do not tell, nor those of 42 of
+    // what is above the elements that they led to.
+    __device__ bool find(Prefix* p, float share, bool strict, Place* at) {
+        Sum t = times(p->sum, share, !strict);
+        if (!holds(t, strict) || !listed) look_for(t, strict);
+        *at = place(t, strict);
+        if (row.fine || (p->exact && exact) || !near_border(t, *at, *p)) return true;
+        Sum above = 0;
+        add_up_exactly(list_top, &above, p);
+        if (!exact) {
+            base = above;
+            list_from = 0;
+            exact = true;
+        }
+        t = times(p->sum, share, !strict);
+        if (!inside(t, strict)) return false;
+        *at = place(t, strict);
+        return true;
+    }
+    // Whether t lies between what is above the list, or the equal elements, and what is above those behind it.
+    __device__ __forceinline__ bool inside(Sum t, bool strict) const {
+        Sum to;
+        if (listed) to = list_sum(listed);
+        else to = base + ((list_from + row.slow(list_top, s.table) * equal) >> list_octave);
+        const Sum from = base + (list_from >> list_octave);
+        return strict ? t >= from && t < to : (t > from || base == 0) && t <= to;
+    }
+    // Whether t is so near one of an element's borders that weights of 24 bits
+    // do not tell on which side it lies.  With the sums b above the list, l in
+    // it (which is exact) and z of the prefix, of weights off by a share e at
+    // most, t / z lies off by e ((1 - t / z) b + t / z (z - b)) / z at most.
+    // Where only one of b and z is made of such weights, by e b or e t.
+    __device__ __forceinline__ bool near_border(Sum t, const Place& p, const Prefix& of) {
+        const Sum all = of.sum, left = all > t ? all - t : 0, in = listed ? list_sum(listed) - list_sum(0) : 0;
+        // e is 2^-23.4; with (1 - u) b and u (z - b - l) both below min(t, z - t):
+        const Sum room = (of.exact == exact ? min(t, left) + in : t) >> 22;
+        return (p.before > 0 && (t > p.before ? t - p.before : 0) < room) ||
+               (p.through < all && (p.through > t ? p.through - t : 0) < room);
+    }
+
+    // The part of a prefix from `from` on.
+    __device__ Prefix down_to(const Prefix& p, float from) {
+        if (p.value >= from) return p;  // all of it
+        // A number below `from`, and above every value below that.
+        const Prefix q = {nextafterf(from, -INFINITY), 0, 0, row.fine};
+        if (listed && base == 0 && exact && listed_value(listed - 1) < from) {
             int count = 0;
             for (int i = threadIdx.x; i - (int)threadIdx.x < listed; i += kThreads)
                 count += __syncthreads_count(i < listed && listed_value(i) >= from);
-            return list_sum(count);
+            return {q.value, 0, list_sum(count), true};
         }
-        const Region g = {fmaxf(from, row.low), row.top, kOctaves, 0.f, 0u, 0};
+        Region g = everything();
+        g.lo = fmaxf(from, row.low);
         add_up_weights(g);
         Sum all = 0;
         for (int i = 0; i < kBins; ++i) all += s.bins[i] >> i;
-        return all;
+        __syncthreads();
+        return {q.value, 0, all, row.fine};
     }
 
     // The sums of all octaves -> what is above each, and bounds on numbers.
@@ -611,8 +901,31 @@ struct Sampler {
         }
         __syncthreads();
     }
-    // Weights of 2^(kBits + 1) at most: how many there are at least.
-    __device__ __forceinline__ static Sum least(Sum sum) { return (sum + (2ull << kBits) - 1) >> (kBits + 1); }
+
+    // A number that at least k elements are not below, and not many more: by
+    // the groups' largest values, in 64 bins between the least of the threads'
+    // largest ones and the largest.  -inf if they do not tell.
+    __device__ float threshold(int k, float least) {
+        const int tid = threadIdx.x;
+        const float scale = kBins / (row.top - least);
+        if (!(scale > 0 && scale < FLT_MAX)) return -INFINITY;  // the same for the cluster
+        if (tid < kBins) mine().bins[tid] = 0;
+        __syncthreads();
+        for (int i = 0; i < row.rounds; ++i) {
+            const float x = row.groups[i * kThreads + tid];
+            if (x >= least) {
+                const int b = kBins - 1 - min(kBins - 1, (int)((x - least) * scale));
+                atomicAdd(reinterpret_cast<unsigned*>(&mine().bins[b]), 1u);  // its lower half
+            }
+        }
+        __syncthreads();
+        join_bins(false, 0);
+        if (s.above[kBins] < (Sum)k) return -INFINITY;
+        const int b = bin_of(s.above, k, false);
+        // A little below the bin's edge, for the roundings of both ways.
+        return fmaf((float)(kBins - 1 - b), (row.top - least) * (1.f / kBins), least) -
+               (fabsf(row.top) + fabsf(least)) * 0x1p-20f;
+    }
 
     // The column of the i-th element that equals x, counting from 0; by the
     // warp that has it, -1 from all others.
@@ -625,7 +938,7 @@ struct Sampler {
             return m;
         };
         int count = 0;
-        row.each_vector(row.v0, row.v1, [&](const int4& v, int) { count += __popc(matches(v)); });
+        row.each_vector(0, row.rounds, x, [&](const int4& v, int) { count += __popc(matches(v)); });
         count = __reduce_add_sync(kFullMask, count);
         if (lane == 0) mine().bins[warp] = (unsigned long long)count;
         cluster_sync(blocks);
@@ -662,60 +975,60 @@ struct Sampler {
     }
 };
 
-// Whether t is so near one of an element's borders that weights of 24 bits do not tell on which side it lies.
-__device__ __forceinline__ bool near_border(Sum t, Sum before, Sum through, Sum all) {
-    const Sum room = min(t, all > t ? all - t : 0) >> 20;
-    return (before > 0 && (t > before ? t - before : 0) < room) || (through < all && (through > t ? through - t : 0) < room);
-}
-
 template <Type kType>
-__global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, SM) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
     using L = Logit<kType>;
-    extern __shared__ __align__(16) unsigned cells[];
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int r = blockIdx.x / blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();  // launched early (launch_pdl): the previous kernel's writes first
 
-    Sampler<kType> sampler(s, cells);
+    Sampler<kType> sampler(s);
     Row<kType>& row = sampler.row;
     sampler.blocks = blocks;
     sampler.rank = rank;
-    sampler.turn = 0;
-    sampler.pieces = a.pieces;
     const char* start = a.logits + r * a.stride;
     row.skip = (int)((reinterpret_cast<uintptr_t>(start) & 15) / L::kBytes);
     row.base = start - row.skip * L::kBytes;
     row.end = row.skip + a.cols;
+    row.rounds = a.rounds;
+    row.groups = reinterpret_cast<float*>(cell_memory() + 2 * kCells);
+    for (int i = tid; i < kCells / 2; i += kThreads) reinterpret_cast<uint4*>(cell_memory())[i] = {0, 0, 0, 0};
     const int vectors = (row.end + L::kMany - 1) / L::kMany;
     // Contiguous shares: of a block, and of each of its warps.
     const int parts = blocks * kWarps, share = (vectors + parts - 1) / parts;
     row.v0 = min((rank * kWarps + warp) * share, vectors);
     row.v1 = min(row.v0 + share, vectors);
+    row.whole0 = max(row.v0, row.skip > 0 ? 1 : 0);
+    row.whole1 = max(min(row.v1, row.end / L::kMany), row.whole0);
+    if (tid < 65) s.table[tid] = kPowers.at[tid];
 
-    // The largest value; NaN if there is one.
-    float top = -INFINITY;
-    row.each_vector(row.v0, row.v1, [&](const int4& v, int) {
-#pragma unroll
-        for (int i = 0; i < L::kMany; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(L::at(v, i)));
-    });
+    // The largest value, NaN if there is one; and the least of the threads' largest.
+    float top = row.look_through(), low = top > -INFINITY ? top : INFINITY;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const float y = __shfl_xor_sync(kFullMask, top, d);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(y));
+        top = larger_of(top, __shfl_xor_sync(kFullMask, top, d));
+        low = fminf(low, __shfl_xor_sync(kFullMask, low, d));
     }
-    if (lane == 0) s.warp_top[warp] = top;
+    if (lane == 0) {
+        s.warp_top[warp] = top;
+        s.warp_low[warp] = low;
+    }
     __syncthreads();
     if (tid == 0) {
-        for (int w = 0; w < kWarps; ++w) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(s.warp_top[w]));
+        for (int w = 1; w < kWarps; ++w) {
+            top = larger_of(top, s.warp_top[w]);
+            low = fminf(low, s.warp_low[w]);
+        }
         s.exchange[0].top = top;
+        s.exchange[0].low = low;
     }
     cluster_sync(blocks);
     for (int b = 0; b < blocks; ++b) {
-        const float y = sampler.theirs(b)->top;
-        if (b == 0) top = y;
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(y));
+        const float y = sampler.theirs(b)->top, z = sampler.theirs(b)->low;
+        top = b == 0 ? y : larger_of(top, y);
+        low = b == 0 ? z : fminf(low, z);
     }
     sampler.turn ^= 1;
     top += 0.f;  // -0 is 0
@@ -742,6 +1055,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
     constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299e-8f;
     row.c_hi = kLog2e / temperature;
     row.c_lo = (fmaf(-row.c_hi, temperature, kLog2e) + kLog2eLow) / temperature;
+    row.ref = fabsf(top) * row.c_hi >= 128.f ? top : 0.f;
+    row.octave0 = __float_as_int(row.magic(top));
+    row.fine = false;
     // 61.9 octaves below the largest value: no element from there on is in
     // octave 64, whatever the rounding.
     row.low = fmaxf(__fmaf_ru(temperature, -42.9f, top), -FLT_MAX);
@@ -756,56 +1072,60 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
         if (!cut_p) row.low = fmaxf(row.low, min_from);
     }
 
-    for (int pass = a.fine; pass < 2; ++pass) {
-        row.fine = pass == 1;
-        row.ref = row.fine || fabsf(top) * row.c_hi >= 128.f ? top : 0.f;
-        row.octave0 = __float_as_int(row.magic(top));
-        if (row.fine && tid < 64) s.table[tid] = (unsigned long long)__double2ll_rn(exp2(tid / 64.0) * 0x1p41);
-        __syncthreads();
-        sampler.listed = 0;
-        const Region all = {row.low, top, kOctaves, 0.f, 0u, 0};
-        sampler.add_up_weights(all);
-        sampler.octaves();
-        Sum kept = s.before[kBins];
-        if (cut_k) kept = sampler.first_k(top_k);
+    Place at = {};
+    Prefix kept = {};
+    // Where few elements can be meant, they are collected at once.
+    float from = greedy ? top : cut_m && !cut_p ? min_from : -INFINITY;
+    if (cut_k && top_k <= kMostFew) from = fmaxf(from, sampler.threshold(top_k, low));
+    bool found = from > -INFINITY && sampler.gather(fmaxf(from, row.low), top, 0, 0);
+    if (found) {
+        kept = sampler.prefix_of(cut_k ? min(top_k, sampler.listed) : sampler.listed);
         if (cut_p) {
-            const Sum t = times(kept, fmaxf(top_p, 0.f), true);
-            const auto at = sampler.find(t, false);
-            if (!row.fine && near_border(t, at.before, at.through, kept)) continue;
-            kept = min(kept, at.through);
-            if (cut_m) kept = min(kept, sampler.down_to(min_from));
+            found = sampler.find(&kept, fmaxf(top_p, 0.f), false, &at);
+            kept = sampler.prefix_to(at);
+            if (cut_m) kept = sampler.down_to(kept, min_from);
         }
-        const Sum t = times(kept, u, false);
-        const auto at = sampler.find(t, true);
-        if (!row.fine && near_border(t, at.before, at.through, kept)) continue;
-        int column;
-        bool writes;
-        if (at.in_list) {
-            column = (int)~(unsigned)s.list[at.index];
-            writes = rank == 0 && tid == 0;
+        found = sampler.find(&kept, u, true, &at);
+    }
+    for (int pass = 0; pass < 2 && !found; ++pass) {
+        row.fine = pass == 1;
+        sampler.listed = sampler.equal = 0;
+        sampler.add_up_weights(sampler.everything());
+        sampler.octaves();
+        kept = cut_k ? sampler.first_k(top_k) : sampler.all();
+        if (cut_p) {
+            if (!sampler.find(&kept, fmaxf(top_p, 0.f), false, &at)) continue;
+            kept = sampler.prefix_to(at);
+            if (cut_m) kept = sampler.down_to(kept, min_from);
+        }
+        found = sampler.find(&kept, u, true, &at);
+    }
+    int column;
+    bool writes;
+    if (at.in_list) {
+        column = (int)~(unsigned)s.list[at.index];
+        writes = rank == 0 && tid == 0;
+    } else {
+        column = sampler.column_of(at.value, at.index);
+        writes = column >= 0 && lane == 0;
+    }
+    if (writes) {
+        const Sum w = at.through - at.before, rest = kept.sum > w ? kept.sum - w : 0;
+        // log(w / kept): near 1 by what the others have, else from the value
+        // itself, which is exact.
+        float logp;
+        if (greedy || rest == 0) {
+            logp = 0.f;
+        } else if (w > rest) {
+            logp = log1pf(-((float)rest / (float)kept.sum));
         } else {
-            column = sampler.column_of(at.value, at.index);
-            writes = column >= 0 && lane == 0;
+            const double c = (double)row.c_hi + row.c_lo;
+            const int octave0 = row.octave0 - __float_as_int(kMagic);
+            logp = (float)((((double)at.value - row.ref) * c - octave0 + kBits - log2f((float)kept.sum)) *
+                           0.69314718055994530942);
         }
-        if (writes) {
-            const Sum w = at.through - at.before, rest = kept > w ? kept - w : 0;
-            // log(w / kept): near 1 by what the others have, else from the
-            // value itself, which is exact.
-            float logp;
-            if (greedy || rest == 0) {
-                logp = 0.f;
-            } else if (w > rest) {
-                logp = log1pf(-((float)rest / (float)kept));
-            } else {
-                const double c = (double)row.c_hi + row.c_lo;
-                const int octave0 = row.octave0 - __float_as_int(kMagic);
-                logp = (float)((((double)at.value - row.ref) * c - octave0 + kBits - log2f((float)kept)) *
-                               0.69314718055994530942);
-            }
-            a.token[r] = column;
-            a.logp[r] = logp;
-        }
-        break;
+        a.token[r] = column;
+        a.logp[r] = logp;
     }
     cluster_sync(blocks);  // no block leaves while another reads its shared memory
 }
@@ -813,21 +1133,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_rows_kernel(const __grid_c
 template <Type kType>
 cudaError_t launch(SampleArgs& a, int device, int sms, cudaStream_t s) {
     auto kernel = sample_rows_kernel<kType>;
-    constexpr int kSmem = kBins * kThreads * 4;
-    static std::atomic<unsigned long long> allowed{0};
-    const cudaError_t e = allow_smem(kernel, kSmem, device, allowed);
-    if (e != cudaSuccess) return e;
     int blocks = 1;
-    while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 2048 && (long long)a.rows * blocks * 2 <= 4 * sms) blocks *= 2;
-    while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 16384) blocks *= 2;
+    while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 1024 && (long long)a.rows * blocks * 2 <= SB * sms) blocks *= 2;
+    while (blocks < kMostBlocks && (long long)kMostBlocks * a.cols > (long long)blocks * kMaxCols) blocks *= 2;
     // A row has a vector more at most than its elements fill.
     const int vectors = (a.cols + Logit<kType>::kMany - 1) / Logit<kType>::kMany + 1, parts = blocks * kWarps;
-    constexpr int kPiece = 32 * (kCellAdds / Logit<kType>::kMany);
-    a.pieces = ((vectors + parts - 1) / parts + kPiece - 1) / kPiece;
+    a.rounds = ((vectors + parts - 1) / parts + 32 * kGroup - 1) / (32 * kGroup);
+    // 32 rounds are the most that kMaxCols take.
+    constexpr int kMostRounds = ((kMaxCols / Logit<kType>::kMany + 1) / (kMostBlocks * kWarps) + 32 * kGroup) / (32 * kGroup);
+    const int smem = (2 * kCells + a.rounds * kThreads) * 4;
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = allow_smem(kernel, (2 * kCells + kMostRounds * kThreads) * 4, device, allowed);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * blocks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it waits before it reads anything
@@ -842,16 +1163,7 @@ cudaError_t launch(SampleArgs& a, int device, int sms, cudaStream_t s) {
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-std::atomic<int> g_sums{0};
-
 }  // namespace
-
-bool set_sample_sums(int value) {
-    if (value < 0 || value > 1) return false;
-    g_sums.store(value, std::memory_order_relaxed);
-    return true;
-}
-
 }  // namespace topk
 
 extern "C" int topk_sample_rows(const void* logits, int dtype, int64_t stride, int rows, int cols,
@@ -880,8 +1192,7 @@ extern "C" int topk_sample_rows(const void* logits, int dtype, int64_t stride, i
     cudaError_t e = current_device(&device, &sms);
     if (e == cudaSuccess) {
         SampleArgs a = {static_cast<const char*>(logits), (long long)stride * bytes, rows, cols, p,
-                        p.min_p > 0 ? std::log(std::fmin((double)p.min_p, 1.0)) : 0.0, 0, u, token, logp,
-                        g_sums.load(std::memory_order_relaxed)};
+                        p.min_p > 0 ? std::log(std::fmin((double)p.min_p, 1.0)) : 0.0, 0, u, token, logp};
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         e = dtype == TOPK_SAMPLE_F32 ? launch<kF32>(a, device, sms, s)
             : dtype == TOPK_KV_BF16  ? launch<kBf16>(a, device, sms, s)
