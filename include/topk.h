@@ -395,8 +395,8 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
  *   y = x * rsqrt(mean(x^2) + eps) * w            with a norm, else y = x,
  * and then for each pair p of them, (a, b), at position n
  *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = n * freq[p].
- * Elements that belong to no pair stay as they are.  All in float32, rounded
- * once at the end; an angle is right to 2^-32 turns and 2^-22 of the turns of
+ * Elements that belong to no pair stay as they are.  All in float32 (squares
+ * past its range are infinite, and the head then 0), rounded once at the end; an angle is right to 2^-32 turns and 2^-22 of the turns of
  * position 2^31, whatever the position.
  *
  *   freq      float32[pairs], device memory: radians per position, of either
@@ -496,7 +496,7 @@ int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_
  * its temperature is negative or one of its parameters or u is NaN: its token
  * is -1 and its logp NaN.
  *
- * Sums are exact sums of weights right to 2^-21.5, and where that does not
+ * Sums are exact sums of weights right to 2^-23.4, and where that does not
  * tell an entry from its neighbour, of weights right to 2^-36: the token is
  * the definition's unless u (or top_p) lies within some 2^-36 of a border.
  * Entries below 2^-61.9 of the largest weight count as nothing.

@@ -23,8 +23,8 @@ def each(value, rows):
 
 
 def check(tk, x, u, **kw):
-    """Compares every row; the parameters in kw are numbers or tensors.  Weights are right to 2^-20, so a logarithm of
-    their quotient to 2^-18, besides its own roundings."""
+    """Compares every row; the parameters in kw are numbers or tensors.  Weights are right to 2^-23.4, so a logarithm of
+    their quotient to 2^-18 with room, besides its own roundings."""
     rows = x.shape[0]
     there = {n: v.cuda() if isinstance(v, torch.Tensor) else v for n, v in kw.items()}
     token, logp = tk.sample_rows(x.cuda(), u.cuda(), **there)
@@ -280,3 +280,104 @@ def test_refusals(tk):
         logp.sum().backward()
     with pytest.raises(RuntimeError, match="no gradient"):
         tk.sample_rows(y, u, logp=torch.zeros(4).cuda())
+
+
+@pytest.mark.parametrize("dtype,cols", [(F16, 2 ** 21), (F32, 2 ** 21), (BF16, 1300003)])
+def test_the_widest_rows(tk, dtype, cols):
+    x, u = logits(2, cols, dtype, spread=2.0, seed=30), uniform(2, 31)
+    for kw in (dict(), dict(top_p=0.95), dict(top_k=50), dict(top_k=100000, top_p=0.9)):
+        check(tk, x, u, **kw)
+    flat = torch.full((1, cols), -3.0).to(dtype)
+    token, _ = tk.sample_rows(flat.cuda(), torch.tensor([0.75]).cuda())
+    assert token.item() == int(0.75 * cols)
+
+
+def test_two_streams_at_once(tk):
+    """Calls on two streams share nothing."""
+    x, u = logits(60, 50000, BF16, seed=32), uniform(60, 33)
+    xd, ud = x.cuda(), u.cuda()
+    want = check(tk, x, u, top_p=0.9)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [tk.sample_rows(xd, ud, top_p=0.9, stream=streams[i % 2])[0] for i in range(10)]
+    torch.cuda.synchronize()
+    assert all(t.tolist() == want for t in got)
+
+
+def test_a_decoders_steps(tk):
+    """Rotated append, attention, eviction and sampling together, as a decoder makes them, against torch in 64 bits: one
+    layer whose hidden state picks the next token's embedding; a captured step is the same as an eager one."""
+    seqs, heads, group, dim, page, vocabulary, budget = 3, 2, 2, 64, 16, 2000, 24
+    g = torch.Generator().manual_seed(34)
+    q_heads, width = heads * group, 4
+    embed = torch.randn(vocabulary, (q_heads + 2 * heads) * dim, generator=g).to(BF16)
+    head = (torch.randn(q_heads * dim, vocabulary, generator=g) * 0.3).to(BF16)
+    norm = (1 + 0.1 * torch.randn(dim, generator=g)).to(BF16)
+    freq = (1000.0 ** (-torch.arange(32) / 32)).float()
+    steps = 40
+    u = torch.rand(steps, seqs, generator=g)
+    dev = dict(device="cuda")
+
+    def run(captured):
+        k, v = (torch.zeros(seqs * width, heads, page, dim, dtype=BF16, **dev).transpose(1, 2) for _ in range(2))
+        table = torch.arange(seqs * width, dtype=torch.int32, **dev).reshape(seqs, width)
+        lens, seen = (torch.zeros(seqs, dtype=torch.int32, **dev) for _ in range(2))
+        weight = torch.zeros(seqs, heads, width * page, **dev)
+        pos = torch.zeros(seqs, heads, width * page, dtype=torch.int32, **dev)
+        token, logp = torch.arange(seqs, dtype=torch.int32, **dev), torch.zeros(seqs, **dev)
+        e, w, n, f, now = embed.cuda(), head.cuda(), norm.cuda(), freq.cuda(), torch.zeros(seqs, **dev)
+        rows = []
+
+        def step():
+            x = e[token.long()].view(seqs, -1, dim)
+            q, kn, vn = x.split([q_heads, heads, heads], 1)
+            q = tk.kv_append_rotated(k, v, table, lens, kn, vn, f, weight=weight, pos=pos, next_pos=seen, k_norm=n, q=q,
+                                     q_norm=n)
+            lens.add_(1)
+            seen.add_(1)
+            out, _ = tk.kv_attend(q, k, v, table, lens, weight=weight)
+            tk.kv_evict(k, v, table, lens, weight, pos, seen, budget, sink=2, recent=8)
+            tk.sample_rows(out.reshape(seqs, -1) @ w, now, temperature=0.8, top_k=40, top_p=0.9, token=token, logp=logp)
+
+        step_of = step
+        if captured:
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                step()  # allocates what a capture may not
+                for t in (lens, seen, weight, pos, k, v):
+                    t.zero_()
+                token.copy_(torch.arange(seqs))
+                graph = torch.cuda.CUDAGraph()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(graph, stream=side):
+                    step()
+            torch.cuda.synchronize()
+            step_of = graph.replay
+        for i in range(steps):
+            now.copy_(u[i])
+            step_of()
+            rows.append((token.tolist(), logp.clone(), lens.tolist(), seen.tolist()))
+        torch.cuda.synchronize()
+        return rows, [t.cpu() for t in (k, v, weight, pos)]
+
+    eager, state = run(False)
+    replayed, state2 = run(True)
+    assert [r[0] for r in eager] == [r[0] for r in replayed]
+    assert all(torch.equal(a, b) for a, b in zip(state, state2))
+    assert eager[-1][2] == [budget] * seqs and eager[-1][3] == [steps] * seqs
+    # Until the first eviction, one sequence's first steps by the definitions.
+    b, keys, values, token = 1, [], [], 1
+    for i in range(budget - 1):
+        x = embed[token].view(-1, dim)
+        at = np.array([i])
+        q = torch.from_numpy(_rotate.rotate(x[None, :q_heads], at, freq, norm)[0][0]).to(BF16).double()
+        keys.append(torch.from_numpy(_rotate.rotate(x[None, q_heads:q_heads + heads], at, freq, norm)[0][0]).to(BF16).double())
+        values.append(x[q_heads + heads:].double())
+        kk, vv = (torch.stack(s).repeat_interleave(group, 1) for s in (keys, values))
+        p = torch.softmax(torch.einsum("hd,thd->ht", q, kk) * dim ** -0.5, -1)
+        logits_ = (torch.einsum("ht,thd->hd", p, vv).to(BF16).double().reshape(-1) @ head.double()).to(BF16)
+        ranked = torch.softmax(logits_.double() / 0.8, 0)
+        token = eager[i][0][b]
+        # The projection's and the attention's roundings may move a border: the token is one that is kept, or nearly.
+        assert ranked[token] >= torch.sort(ranked, descending=True).values[44]

@@ -7,21 +7,35 @@
 // token is where C passes u times the kept weight.  So all that is ever asked
 // is where C (or the rank) passes a number, and how large C is there.
 //
-// One cluster of blocks has a row.  Bound by HBM for large batches in float32
-// and by instructions in 16 bits: an exponential and a bin for each element.
-//   1. The row's largest value.
-//   2. The weights of each octave (factor of two below the largest), 64 of
-//      them.  A weight is a 24-bit number times 2^octave, so octaves are sums of
-//      integers: exact, in any order.  Each thread adds in cells of its own.
-//   3. The octave that is asked for is cut into 64 parts, and the part again,
+// One cluster of blocks has a row; its parts stay in L2 between the passes.
+//   1. The row's largest value, and that of each thread's groups of vectors:
+//      later passes read only the groups that can have what they look for.
+//   2. Where few elements can be meant (top_k up to 512, min_p, temperature 0),
+//      they are collected at once: for top_k, those that are not below a number
+//      that at least k groups' largest values reach.
+//   3. Else, or where those were too many: the weights of each octave (factor of
+//      two), 64 of them.  A weight is a 24-bit number times 2^octave, so octaves
+//      are sums of integers: exact, in any order.  A block adds up in cells of
+//      shared memory, two atomic additions an element (4.4 cycles of an SM for
+//      32 elements; cells of each thread's own cost 3.5, but their 64 KB left
+//      two blocks to an SM).
+//   4. The octave that is asked for is cut into 64 parts, and the part again,
 //      until what is left fits a list (or is one value, whose elements are
-//      equal).  Usually everything down to that octave fits at once.
-//   4. The list is sorted and summed up, and gives the answer.
+//      equal).
+//   5. The list, of at most 512 elements, is sorted and summed up with weights
+//      of 42 bits, right to 2^-36, and gives the answer.
 //
-// A weight is off by 2^-21.5 of itself, so a number that lies within 2^-20 of
-// an element's border (relative, of the smaller side) cannot be told from its
-// neighbour's.  Such a row goes through 2 to 4 once more with weights of 42
-// bits, right to 2^-36.
+// A sum of fast weights is off by 2^-23.4 of itself at most.  A number that lies
+// nearer to an element's border than that could put it is looked up once more
+// with exact sums of 42-bit weights: one pass for what is above the list, and,
+// should the number lie outside the list after all, 3 to 5 with 42 bits.
+//
+// What bounds it: the passes' latencies (a barrier of the cluster costs 1 to 2
+// us, and there are 3 of them for top_k, 6 for top_p) and instructions, 20 an
+// element for 3 and 4; HBM only where nothing but 1 is done.  Measured: one row
+// of 131072 (bfloat16, top_k 50, top_p 0.95) 13 us; 256 of 160000 the same 36 us
+// (2.2 TB/s); 64 of 131001 float32 with top_p 0.95 93 us; 128 of 32768, nothing
+// cut off, 33 us; 512 of 262144 float32 with min_p 288 us (1.9 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,23 +55,15 @@ namespace topk {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-#ifndef SM
-#define SM 3
-#endif
-#ifndef SB
-#define SB 4
-#endif
+constexpr int kBlocksPerSm = 4;  // 64 registers a thread: what spills, spills between passes (64 rows with top_p: 96 us, 102 with three blocks)
 constexpr int kBins = 64;
-constexpr int kList = 512;          // elements that a list has room for
+constexpr int kList = 512;          // elements that a list has room for (with 1024, 114 us instead of 93 for 64 rows with top_p)
 constexpr int kMostBlocks = 8;      // of a cluster
 constexpr int kBits = 41;           // a weight of 1 in its octave is 2^kBits
 constexpr int kFastBits = 24;       // and a fast one 2^kFastBits
 constexpr int kListShift = 11;      // in a list 2^(kBits + kListShift): kList of them stay below 2^63
 constexpr int kMaxCols = 1 << 21;   // 2^21 weights of an octave, each below 2^(kBits + 0.5), stay below 2^63
-#ifndef SG
-#define SG 4
-#endif
-constexpr int kGroup = SG;           // vectors of a thread's group, whose largest value is kept
+constexpr int kGroup = 4;           // vectors of a thread's group, whose largest value is kept
 constexpr int kMostFew = 512;       // top_k up to which a threshold is looked for first
 
 struct SampleArgs {
@@ -162,7 +168,7 @@ struct Shared {
     unsigned long long table[65];       // kPowers
     unsigned long long scan[kWarps];
     float warp_top[kWarps], warp_low[kWarps];
-    float min_from;
+    float min_from, part_lo, part_hi;
 };
 
 // Where a block adds up weights: [2][kBins][32] cells, a column for each lane
@@ -299,10 +305,13 @@ struct Row {
     __device__ __forceinline__ float look_through() const {
         const int lane = threadIdx.x & 31;
         float all = -INFINITY;
+        int4 next[kGroup];
+        load_group(v0 + lane, true, next);
         for (int i = 0; i < rounds; ++i) {
-            const int v = v0 + i * (32 * kGroup) + lane;
             int4 raw[kGroup];
-            load_group(v, true, raw);
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) raw[u] = next[u];
+            if (i + 1 < rounds) load_group(v0 + (i + 1) * (32 * kGroup) + lane, true, next);
             unsigned m = L::kNothing;
 #pragma unroll
             for (int u = 0; u < kGroup; ++u) m = L::largest(m, raw[u]);
@@ -408,22 +417,28 @@ struct Sampler {
     }
 
     // Adds up `what` of the region's elements by bins over the cluster, into
-    // s.bins.  kHot: fast weights by octaves, where every element up to the top
-    // counts.
-    template <bool kHot>
+    // s.bins.  kWay: fast weights by octaves, where every element up to the
+    // top counts; fast weights in kLinear bins; or as `what` and the region
+    // say, which is rare.
+    enum Way { kByOctaves, kByLinear, kAnyhow };
+    template <Way kWay>
     __device__ void add_up(const Region& g, What what) {
         const int tid = threadIdx.x, lane = tid & 31;
         unsigned *high = cell_memory() + lane, *low = high + kCells;
         // A cell has 2^21 / 8 / 32 numbers at most, below 2^14.
         const int split = what == kFast ? kFastBits / 2 : 14;
         row.each_vector(0, row.rounds, g.lo, [&](const int4& v, int) {
-            if constexpr (kHot) {
+            if constexpr (kWay != kAnyhow) {
 #pragma unroll
                 for (int i = 0; i < L::kMany; ++i) {
                     const float x = L::at(v, i);
-                    if (x >= g.lo) {
+                    if (x >= g.lo && (kWay == kByOctaves || x <= g.hi)) {
                         const float t = row.magic(x);
-                        const unsigned w = row.fast(x, t), at = min((unsigned)(row.octave0 - __float_as_int(t)), kBins - 1u) * 32;
+                        const unsigned w = row.fast(x, t);
+                        const int b = kWay == kByOctaves
+                                          ? row.octave0 - __float_as_int(t)
+                                          : kBins - 1 - min(kBins - 1, (int)((x - g.lo) * g.scale));
+                        const unsigned at = min((unsigned)b, kBins - 1u) * 32;
                         atomicAdd(high + at, w >> (kFastBits / 2));
                         atomicAdd(low + at, w & ((1u << (kFastBits / 2)) - 1));
                     }
@@ -491,12 +506,14 @@ struct Sampler {
     }
     __device__ void add_up_weights(const Region& g) {
         if (row.fine) {
-            add_up<false>(g, kFineHigh);
-            add_up<false>(g, kFineLow);
+            add_up<kAnyhow>(g, kFineHigh);
+            add_up<kAnyhow>(g, kFineLow);
         } else if (g.by == kOctaves) {
-            add_up<true>(g, kFast);
+            add_up<kByOctaves>(g, kFast);
+        } else if (g.by == kLinear) {
+            add_up<kByLinear>(g, kFast);
         } else {
-            add_up<false>(g, kFast);
+            add_up<kAnyhow>(g, kFast);
         }
     }
     // Sums of the bins before each: two of a lane's, by one warp.
@@ -522,7 +539,7 @@ struct Sampler {
     }
 
     // The smallest number k in [lo, hi] for which f(value of k), which is true
-    // from some value on and for hi, is true.  All lanes of each warp.
+    // from some value on and for hi, is true.  By one warp.
     template <typename F>
     __device__ unsigned first(unsigned lo, unsigned hi, F f) {
         const int lane = threadIdx.x & 31;
@@ -537,15 +554,25 @@ struct Sampler {
         }
         return hi;
     }
-    // Bins b0 to b1 of a region.
+    // Bins b0 to b1 of a region.  One warp looks for the borders: the others'
+    // instructions are better spent on other rows.
     __device__ Region part(const Region& g, int b0, int b1) {
-        const unsigned klo = L::number(g.lo), khi = L::number(g.hi);
-        auto upto = [&](int b) {
-            return first(klo, khi, [&](float x) { return x >= g.lo && bin(g, x) <= b; });
-        };
+        if (threadIdx.x < 32) {
+            const unsigned klo = L::number(g.lo), khi = L::number(g.hi);
+            auto upto = [&](int b) {
+                return first(klo, khi, [&](float x) { return x >= g.lo && bin(g, x) <= b; });
+            };
+            const float lo = L::value(upto(b1)), hi = b0 > 0 ? L::value(upto(b0 - 1) - 1) : g.hi;
+            if (threadIdx.x == 0) {
+                s.part_lo = lo;
+                s.part_hi = hi;
+            }
+        }
+        __syncthreads();
         Region r = g;
-        r.lo = L::value(upto(b1));
-        if (b0 > 0) r.hi = L::value(upto(b0 - 1) - 1);
+        r.lo = s.part_lo;
+        r.hi = s.part_hi;
+        __syncthreads();
         return r;
     }
     // How a region is cut; `level` counts the cuts before.
@@ -571,11 +598,12 @@ struct Sampler {
         if (tid == 0) mine().count = 0;
         __syncthreads();
         row.each_vector(0, row.rounds, lo, [&](const int4& v, int at) {
-            if (!(L::single(L::largest(L::kNothing, v)) >= lo)) return;
-#pragma unroll 1
-            for (int i = 0; i < L::kMany; ++i) {
+            unsigned in = 0;
+#pragma unroll
+            for (int i = 0; i < L::kMany; ++i) in |= L::at(v, i) >= lo && L::at(v, i) <= hi ? 1u << i : 0u;
+            for (; in; in &= in - 1) {
+                const int i = __ffs(in) - 1;
                 const float x = L::pick(v, i);
-                if (!(x >= lo && x <= hi)) continue;
                 const int n = atomicAdd(&mine().count, 1);
                 const unsigned b = __float_as_uint(x + 0.f), key = b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
                 if (n < kList)
@@ -605,9 +633,7 @@ struct Sampler {
             __syncthreads();
             return false;
         }
-        const int size = next_pow2(max(n, 2));
-        for (int i = n + tid; i < size; i += kThreads) s.list[i] = 0;
-        block_sort_smem_desc(s.list, size);
+        sort_list(n);
         constexpr int kPer = kList / kThreads;
         Sum own[kPer], sum = 0;
 #pragma unroll
@@ -640,6 +666,47 @@ struct Sampler {
         exact = hi == row.top;
         base = exact ? 0 : s.before[octave];
         return true;
+    }
+    // Sorts s.list[0..n), descending; no two are equal.  A warp sorts 32 of
+    // them by shuffles, and a number's place is the sum of its places in all
+    // sorted pieces: three barriers instead of one for each step of a network.
+    __device__ void sort_list(int n) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = (n + 31) / 32;
+        constexpr int kPer = kList / kThreads;
+        unsigned long long key[kPer];
+        int rank[kPer];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int piece = warp + j * kWarps, at = piece * 32 + lane;
+            unsigned long long v[1] = {at < n ? s.list[at] : 0ull};  // no number is 0
+            if (piece < pieces) {
+                warp_sort_desc(v, lane);
+                s.list[at] = v[0];
+            }
+            key[j] = v[0];
+            rank[j] = lane;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int piece = warp + j * kWarps;
+            if (piece >= pieces) continue;
+            for (int p = 0; p < pieces; ++p) {
+                if (p == piece) continue;
+                const unsigned long long* other = s.list + p * 32;
+                int above = 0;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    if (other[above + d - 1] > key[j]) above += d;
+                rank[j] += above + (other[above] > key[j]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (key[j] != 0) s.list[rank[j]] = key[j];
+        __syncthreads();
     }
     __device__ __forceinline__ float listed_value(int i) const {
         const unsigned k = (unsigned)(s.list[i] >> 32);
@@ -684,11 +751,14 @@ struct Sampler {
         return {p.value, ties, p.through, exact};
     }
 
-    // Weights lie between 2^(kBits - 1/2) and 2^(kBits + 1/2), and 2^-14 of
-    // that beside: how many of them there are at most, and at least.
-    static constexpr Sum kLightest = 1554944255987ull - (1ull << 27), kHeaviest = 3109888511976ull + (1ull << 28);
-    __device__ __forceinline__ static Sum most(Sum sum) { return sum / kLightest; }
-    __device__ __forceinline__ static Sum least(Sum sum) { return (sum + kHeaviest - 1) / kHeaviest; }
+    // Weights lie between 2^(kBits - 1/2) and 2^(kBits + 1/2): how many of them
+    // there are at most, and at least, with room for roundings.
+    __device__ __forceinline__ static int most(Sum sum) {
+        return (int)((float)sum * (1.0002f / 1554944255988.f)) + (sum > 0);
+    }
+    __device__ __forceinline__ static int least(Sum sum) {
+        return max((int)((float)sum * (0.9998f / 3109888511976.f)), sum > 0 ? 1 : 0);
+    }
 
     // Makes the list, or the run of equal elements, in which the first element
     // lies up to and with which the weights are more than t (strict) or not less.
@@ -716,7 +786,7 @@ struct Sampler {
             cut(g, level);
             int b = 0;
             if (counted) {
-                add_up<false>(g, kCount);
+                add_up<kAnyhow>(g, kCount);
                 b = pick(above);
                 room = s.bins[b];
             }
@@ -750,7 +820,7 @@ struct Sampler {
             gather(part(everything(), 0, reach).lo, row.top, 0, 0);
             return prefix_of(min(k, listed));
         }
-        add_up<false>(everything(), kCount);
+        add_up<kAnyhow>(everything(), kCount);
         if (s.above[kBins] <= (Sum)k) return all();
         const int o = bin_of(s.above, k, false);
         Sum need = k - s.above[o], room = s.bins[o];
@@ -884,8 +954,8 @@ struct Sampler {
             s.octave[2 * lane] = b0;
             s.octave[2 * lane + 1] = b1;
             write_scan(s.before, b0 >> 2 * lane, b1 >> (2 * lane + 1));
-            int upper = (int)(most(b0) + most(b1)), lower = (int)(least(b0) + least(b1));  // 2^21 and a little at most
-            const int upper1 = (int)most(b1), lower1 = (int)least(b1);
+            int upper = most(b0) + most(b1), lower = least(b0) + least(b1);  // 2^21 and a little at most
+            const int upper1 = most(b1), lower1 = least(b1);
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int yu = __shfl_up_sync(kFullMask, upper, d), yl = __shfl_up_sync(kFullMask, lower, d);
@@ -976,7 +1046,7 @@ struct Sampler {
 };
 
 template <Type kType>
-__global__ void __launch_bounds__(kThreads, SM) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
     using L = Logit<kType>;
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
@@ -1133,8 +1203,16 @@ __global__ void __launch_bounds__(kThreads, SM) sample_rows_kernel(const __grid_
 template <Type kType>
 cudaError_t launch(SampleArgs& a, int device, int sms, cudaStream_t s) {
     auto kernel = sample_rows_kernel<kType>;
+    // Blocks of a row: 8192 elements each at least, and as many as fill the
+    // SMs four times over, or once (four blocks fit an SM) where few elements
+    // are looked at again, and blocks do little but read (256 rows of 160000
+    // with top_k 50: 36 us, 73 with more; 512 of 262144 with min_p: 291 us, 470
+    // with fewer).
+    const bool light = !a.p.top_ks && a.p.top_k > 0 && a.p.top_k <= kMostFew;
     int blocks = 1;
-    while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 1024 && (long long)a.rows * blocks * 2 <= SB * sms) blocks *= 2;
+    while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 8192 &&
+           (long long)a.rows * blocks * 2 <= (long long)(light ? 1 : 4) * kBlocksPerSm * sms)
+        blocks *= 2;
     while (blocks < kMostBlocks && (long long)kMostBlocks * a.cols > (long long)blocks * kMaxCols) blocks *= 2;
     // A row has a vector more at most than its elements fill.
     const int vectors = (a.cols + Logit<kType>::kMany - 1) / Logit<kType>::kMany + 1, parts = blocks * kWarps;
