@@ -1191,7 +1191,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_rows_kernel(con
         } else {
             const double c = (double)row.c_hi + row.c_lo;
             const int octave0 = row.octave0 - __float_as_int(kMagic);
-            logp = (float)((((double)at.value - row.ref) * c - octave0 + kBits - log2f((float)kept.sum)) *
+            const int up = __clzll((long long)kept.sum);  // the logarithm of a number from 1 to 2, and the rest exactly
+            const float part = log2f((float)(kept.sum << up) * 0x1p-63f);
+            logp = (float)((((double)at.value - row.ref) * c - octave0 + kBits - (63 - up) - (double)part) *
                            0.69314718055994530942);
         }
         a.token[r] = column;
