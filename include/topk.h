@@ -511,6 +511,8 @@ int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_
  *   token    int32[rows].
  *   logp     float32[rows].
  *
+ * token and logp overlap nothing else that the call is given.
+ *
  * Device pointers (the struct is host memory); the call only enqueues, one
  * launch, and has no scratch.  Equal inputs give equal outputs, bit for bit.
  */

@@ -381,3 +381,14 @@ def test_a_decoders_steps(tk):
         token = eager[i][0][b]
         # The projection's and the attention's roundings may move a border: the token is one that is kept, or nearly.
         assert ranked[token] >= torch.sort(ranked, descending=True).values[44]
+
+
+@pytest.mark.parametrize("ties", [511, 512, 513, 1500])
+def test_limits_of_the_list(tk, ties):
+    """As many equal best entries as a list has room for, and one more or less; top_k around the same number."""
+    x = logits(4, 9000, F32, spread=1.0, seed=35)
+    x[:, torch.randperm(9000, generator=torch.Generator().manual_seed(36))[:ties]] = 6.0
+    u = torch.tensor([0.0, 0.3, 0.77, 1 - 2.0 ** -24])
+    for kw in (dict(temperature=0.0), dict(top_k=ties), dict(top_k=ties - 1), dict(top_k=ties + 1), dict(min_p=0.9),
+               dict(top_k=512), dict(top_k=513), dict(top_p=0.3), dict()):
+        check(tk, x, u, **kw)
