@@ -34,8 +34,9 @@
 // us, and there are 3 of them for top_k, 6 for top_p) and instructions, 20 an
 // element for 3 and 4; HBM only where nothing but 1 is done.  Measured: one row
 // of 131072 (bfloat16, top_k 50, top_p 0.95) 13 us; 256 of 160000 the same 36 us
-// (2.2 TB/s); 64 of 131001 float32 with top_p 0.95 93 us; 128 of 32768, nothing
-// cut off, 33 us; 512 of 262144 float32 with min_p 288 us (1.9 TB/s).
+// (2.2 TB/s); 64 of 131001 float32 with top_p 0.95 93 to 105 us (some rows need
+// the exact pass); 128 of 32768, nothing cut off, 33 to 36 us; 512 of 262144
+// float32 with min_p 288 us (1.9 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
