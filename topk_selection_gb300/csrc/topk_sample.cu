@@ -839,10 +839,14 @@ struct Sampler {
     }
     __device__ Prefix all() const { return {-INFINITY, 0, s.before[kBins], row.fine}; }
 
-    // Weights of 42 bits of what is above x, and of a prefix.
+    // Weights of 42 bits of what is above x, and of a prefix.  What an entry has
+    // below a whole unit of octave 0 is added up by itself, in 2^-32 units, and
+    // carried once: rounded away entry by entry, equal ones would all be off by
+    // the same amount (2^20 of them in octave 21 by 2^-22 of the whole row).
     __device__ void add_up_exactly(float x, Sum* above, Prefix* p) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        Sum a = 0, b = 0;
+        auto below = [](Sum m, int o) { return (m << (63 - o) << 1) >> 32; };  // of m >> o
+        Sum a = 0, a_below = 0, b = 0, b_below = 0;
         const float from = fmaxf(row.low, fminf(x, p->value));
         row.each_vector(0, row.rounds, from, [&](const int4& v, int) {
             if (!(L::single(L::largest(L::kNothing, v)) >= from)) return;
@@ -851,38 +855,52 @@ struct Sampler {
                 const float y = L::pick(v, i);
                 if (!(y >= row.low && (y > x || y > p->value))) continue;
                 const int o = row.octave(y);
-                const Sum w = (row.slow(y, s.table) + ((1ull << o) >> 1)) >> o;
-                if (y > x) a += w;
-                if (y > p->value) b += w;
+                const Sum m = row.slow(y, s.table), w = m >> o, w_below = below(m, o);
+                if (y > x) {
+                    a += w;
+                    a_below += w_below;
+                }
+                if (y > p->value) {
+                    b += w;
+                    b_below += w_below;
+                }
             }
         });
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             a += __shfl_xor_sync(kFullMask, a, d);
+            a_below += __shfl_xor_sync(kFullMask, a_below, d);
             b += __shfl_xor_sync(kFullMask, b, d);
+            b_below += __shfl_xor_sync(kFullMask, b_below, d);
         }
-        if (tid < kBins) mine().bins[tid] = 0;
-        __syncthreads();
+        static_assert(4 * kWarps <= kBins);
         if (lane == 0) {
-            mine().bins[2 * warp] = a;
-            mine().bins[2 * warp + 1] = b;
+            Sum* q = mine().bins + 4 * warp;
+            q[0] = a;
+            q[1] = a_below;
+            q[2] = b;
+            q[3] = b_below;
         }
         cluster_sync(blocks);
-        a = b = 0;
+        a = a_below = b = b_below = 0;
         for (int r = 0; r < blocks; ++r) {
             const Sum* q = theirs(r)->bins;
             for (int w = 0; w < kWarps; ++w) {
-                a += q[2 * w];
-                b += q[2 * w + 1];
+                a += q[4 * w];
+                a_below += q[4 * w + 1];
+                b += q[4 * w + 2];
+                b_below += q[4 * w + 3];
             }
         }
         turn ^= 1;
-        *above = a;
+        *above = a + (a_below >> 32);
         if (!p->exact && p->ties > 0) {
             const int o = row.octave(p->value);
-            b += (row.slow(p->value, s.table) * p->ties + ((1ull << o) >> 1)) >> o;
+            const Sum m = row.slow(p->value, s.table) * p->ties;
+            b += m >> o;
+            b_below += below(m, o);
         }
-        if (!p->exact) p->sum = b;
+        if (!p->exact) p->sum = b + (b_below >> 32);
         p->exact = true;
     }
 
