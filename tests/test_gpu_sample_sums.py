@@ -63,3 +63,51 @@ def test_as_many_as_there_can_be(tk, value):
 @pytest.mark.parametrize("cols,value", [(262144, -11.3), (2 ** 21, -13.1), (2 ** 21, -15.1)])
 def test_cut_by_top_p(tk, cols, value, top_p):
     check(tk, cols, value, F32, top_p=top_p, sure=cols // 2, seed=3)
+
+
+def octaves_with_parts_of_a_unit(g, cols, last, past, low=None):
+    """A row and a u.  The largest entry has 2^40.5 units of 2^-41 of its octave's weight 1; each of the octaves from 7 to
+    `last` below it has nearly a unit more than a whole number of them; u times all is `past` units past the largest.
+    low: the value of the other columns, not counted."""
+    values = [np.float32(-0.4999 * np.log(2))]
+    for o in range(7, min(last, 41) + 1):  # an entry each
+        while True:
+            x = np.float32((g.uniform(-0.45, 0.45) - o) * np.log(2))
+            if 0.85 < np.exp(float(x)) * 2.0 ** 41 % 1 < 0.95:
+                break
+        values.append(x)
+    for o in range(42, last + 1):  # so many that they are nearly a unit
+        values += [np.float32(-o * np.log(2))] * int(0.97 * 2 ** (o - 41))
+    w = np.exp(np.float64(values))
+    u = np.float32(w[0] / w.sum() * (1 - 2.0 ** -12 * g.uniform(1, 2)))
+    left = (w[0] + past * 2.0 ** -41) / float(u) - w.sum()  # three entries bring all to where u is
+    for share in (0.9, 1 - 2.0 ** -18, 1.0):
+        values.append(np.float32(np.log(left * share)))
+        left -= np.exp(float(values[-1]))
+    x = np.full(cols, -np.inf if low is None else low, dtype=np.float32)
+    x[g.permutation(cols)[:len(values)]] = values
+    w = np.sort(np.exp(np.float64(values)))[::-1]
+    share = (float(u) * w.sum() - w[0]) / w.sum()
+    assert 2.0 ** -36 < share < 2.0 ** -35
+    return x, u, np.argsort(-x, kind="stable")[1]
+
+
+def made(seed, rows, *args, **kw):
+    g = np.random.default_rng(seed)
+    return [np.stack(v) for v in zip(*(octaves_with_parts_of_a_unit(g, *args, **kw) for _ in range(rows)))]
+
+
+def test_sums_over_the_octaves(tk):
+    """What each octave has below a whole unit counts too: with 46 units less, u would still be in the largest entry's
+    weight, by more than 2^-36 of all."""
+    x, u, want = made(4, 64, 20000, 52, 32)
+    token, _ = tk.sample_rows(torch.from_numpy(x).cuda(), torch.from_numpy(u).cuda())
+    assert token.tolist() == want.tolist()
+
+
+def test_sums_over_the_octaves_down_to_min_p(tk):
+    """The same of what min_p keeps of a prefix that top_p cut: 2^20 entries of octave 40 are more than top_p leaves out."""
+    x, u, want = made(5, 16, 2 ** 20, 38, 25, low=np.float32(-40 * np.log(2)))
+    token, _ = tk.sample_rows(torch.from_numpy(x).cuda(), torch.from_numpy(u).cuda(), top_p=1 - 2.0 ** -22,
+                              min_p=2.0 ** -38.5)  # 2^-39 of the largest: between the two
+    assert token.tolist() == want.tolist()

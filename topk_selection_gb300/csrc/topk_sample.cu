@@ -517,19 +517,28 @@ struct Sampler {
             add_up<kAnyhow>(g, kFast);
         }
     }
-    // Sums of the bins before each: two of a lane's, by one warp.
-    static __device__ void write_scan(Sum* to, Sum b0, Sum b1) {
+    // The sum of the numbers of this lane and those before it.
+    static __device__ __forceinline__ Sum through(Sum x) {
         const int lane = threadIdx.x & 31;
-        Sum x = b0 + b1;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const Sum y = __shfl_up_sync(kFullMask, x, d);
             if (lane >= d) x += y;
         }
+        return x;
+    }
+    // Sums of the bins before each: two of a lane's, by one warp.
+    static __device__ void write_scan(Sum* to, Sum b0, Sum b1) {
+        const int lane = threadIdx.x & 31;
+        const Sum x = through(b0 + b1);
         to[2 * lane] = x - b0 - b1;
         to[2 * lane + 1] = x - b1;
         if (lane == 31) to[kBins] = x;
     }
+    // What an octave's sum, in its own unit, has below a whole unit of octave 0,
+    // in 2^-56 units: 64 of them leave room for the carries.  Without them all
+    // octaves together could be off by 2^-35 of the row.
+    static __device__ __forceinline__ Sum below(Sum b, int o) { return (b << (63 - o) << 1) >> 8; }
     // The first bin up to and with which the sums are more than t (strict) or
     // not less; the last one that has anything if t is past them all.
     static __device__ int bin_of(const Sum* sums, Sum t, bool strict) {
@@ -959,10 +968,13 @@ struct Sampler {
         Region g = everything();
         g.lo = fmaxf(from, row.low);
         add_up_weights(g);
-        Sum all = 0;
-        for (int i = 0; i < kBins; ++i) all += s.bins[i] >> i;
+        Sum all = 0, rest = 0;
+        for (int i = 0; i < kBins; ++i) {
+            all += s.bins[i] >> i;
+            rest += below(s.bins[i], i);
+        }
         __syncthreads();
-        return {q.value, 0, all, row.fine};
+        return {q.value, 0, all + (rest >> 56), row.fine};
     }
 
     // The sums of all octaves -> what is above each, and bounds on numbers.
@@ -973,6 +985,10 @@ struct Sampler {
             s.octave[2 * lane] = b0;
             s.octave[2 * lane + 1] = b1;
             write_scan(s.before, b0 >> 2 * lane, b1 >> (2 * lane + 1));
+            const Sum r0 = below(b0, 2 * lane), r1 = below(b1, 2 * lane + 1), r = through(r0 + r1);
+            s.before[2 * lane] += (r - r0 - r1) >> 56;
+            s.before[2 * lane + 1] += (r - r1) >> 56;
+            if (lane == 31) s.before[kBins] += r >> 56;
             int upper = most(b0) + most(b1), lower = least(b0) + least(b1);  // 2^21 and a little at most
             const int upper1 = most(b1), lower1 = least(b1);
 #pragma unroll
