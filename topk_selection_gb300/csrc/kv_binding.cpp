@@ -445,7 +445,7 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 k.defined() ? k.size(1) : 0, dim);
         const Stream s(a[10], device.index());
         check_written("kv_rotate", {a[8], a[9]});
-        check_followed("kv_rotate", "q, k or the norms", {a[0], a[1], a[4], a[5]}, {a[8], a[9]});
+        check_followed("kv_rotate", "q, k, freq or the norms", {a[0], a[1], a[3], a[4], a[5]}, {a[8], a[9]});
         const at::Tensor q_out = q.defined() ? rotated(a[8], "q_out", q) : at::Tensor();
         const at::Tensor k_out = k.defined() ? rotated(a[9], "k_out", k) : at::Tensor();
         topk_kv_heads h[4] = {};
@@ -463,7 +463,8 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         });
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
         written({a[8], a[9]});
-        if (followed({a[0], a[1], a[4], a[5]})) no_backward("kv_rotate", {a[0], a[1], a[4], a[5]}, {&q_out, &k_out});
+        if (followed({a[0], a[1], a[3], a[4], a[5]}))
+            no_backward("kv_rotate", {a[0], a[1], a[3], a[4], a[5]}, {&q_out, &k_out});
         return two(q_out, k_out);
     });
 }
@@ -490,11 +491,11 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 c.c.heads, c.c.dim);
         const Stream s(a[17], c);
         check_written("kv_append_rotated", {a[0], a[1], a[8], a[16]});
-        check_followed("kv_append_rotated", "q or q_norm", {a[14], a[15]}, {a[16]});
+        check_followed("kv_append_rotated", "q, freq or q_norm", {a[6], a[14], a[15]}, {a[16]});
         const at::Tensor q_out = q.defined() ? rotated(a[16], "q_out", q) : at::Tensor();
-        if (followed({a[4], a[5], a[11]}) &&
+        if (followed({a[4], a[5], a[6], a[11]}) &&
             PyErr_WarnEx(PyExc_UserWarning,
-                         "kv_append_rotated has no gradient: none will reach k_new, v_new and k_norm", 2) != 0)
+                         "kv_append_rotated has no gradient: none will reach k_new, v_new, freq and k_norm", 2) != 0)
             throw Raised();
         topk_kv_heads h[4] = {heads_of(k, "k_new"), heads_of(v, "v_new"), {}, {}};
         if (q.defined()) {
@@ -508,7 +509,7 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
         written({a[16]});
         if (tokens) written({a[0], a[1], a[8], a[9]});
-        if (followed({a[14], a[15]})) no_backward("kv_append_rotated", {a[14], a[15]}, {&q_out});
+        if (followed({a[6], a[14], a[15]})) no_backward("kv_append_rotated", {a[6], a[14], a[15]}, {&q_out});
         return wrapped(q_out);
     });
 }
@@ -534,21 +535,27 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
         };
         const float* u = static_cast<const float*>(vector(a[1], "u", at::kFloat));
         topk_sampling p = {};
-        auto parameter = [&](PyObject* o, const char* name, float* one, const float** each) {
-            if (THPVariable_Check(o)) *each = static_cast<const float*>(vector(o, name, at::kFloat));
-            else *one = (float)number(o);
+        // What it returns is the parameter's tensor, or None.
+        auto parameter = [&](PyObject* o, const char* name, float* one, const float** each) -> PyObject* {
+            if (!THPVariable_Check(o)) {
+                *one = (float)number(o);
+                return Py_None;
+            }
+            *each = static_cast<const float*>(vector(o, name, at::kFloat));
+            return o;
         };
-        parameter(a[2], "temperature", &p.temperature, &p.temperatures);
+        PyObject* const temperature = parameter(a[2], "temperature", &p.temperature, &p.temperatures);
         if (THPVariable_Check(a[3])) p.top_ks = static_cast<const int32_t*>(vector(a[3], "top_k", at::kInt));
         else p.top_k = integer(a[3]);
-        parameter(a[4], "top_p", &p.top_p, &p.top_ps);
-        parameter(a[5], "min_p", &p.min_p, &p.min_ps);
+        PyObject* const top_p = parameter(a[4], "top_p", &p.top_p, &p.top_ps);
+        PyObject* const min_p = parameter(a[5], "min_p", &p.min_p, &p.min_ps);
         if (!p.temperatures && !(p.temperature >= 0)) raise(PyExc_ValueError, "temperature must not be negative");
         const Stream s(a[8], device.index());
         if (a[6] != Py_None) vector(a[6], "token", at::kInt);
         if (a[7] != Py_None) vector(a[7], "logp", at::kFloat);
         check_written("sample_rows", {a[7]});
-        check_followed("sample_rows", "the logits", {a[0]}, {a[7]});
+        const std::initializer_list<PyObject*> read = {a[0], a[1], temperature, top_p, min_p};
+        check_followed("sample_rows", "the logits, u or parameters", read, {a[7]});
         const at::Tensor token = a[6] != Py_None ? THPVariable_Unpack(a[6])
                                                  : at::Tensor(at::detail::empty_cuda({rows}, at::kInt, device, std::nullopt));
         const at::Tensor logp = a[7] != Py_None ? THPVariable_Unpack(a[7])
@@ -561,7 +568,7 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
         });
         if (rc != TOPK_OK) return PyLong_FromLong(rc);
         written({a[6], a[7]});
-        if (followed({a[0]})) no_backward("sample_rows", {a[0]}, {&logp});
+        if (followed(read)) no_backward("sample_rows", read, {&logp});
         return two(token, logp);
     });
 }
