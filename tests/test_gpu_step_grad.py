@@ -76,3 +76,37 @@ def test_backward_through_a_sample_raises(tk, name):
         tk.sample_rows(**a, logp=torch.zeros(4, device="cuda"))
     with torch.no_grad():
         assert not tk.sample_rows(**a, logp=torch.zeros(4, device="cuda"))[1].requires_grad
+
+
+def test_tangents_are_refused(tk):
+    """In forward mode too: nothing that comes back could have a tangent."""
+    import torch.autograd.forward_ad as fwd
+
+    a = rotation()
+    x, q_out = a["x"], torch.empty(3, 2, 64, dtype=F16, device="cuda")
+    s = dict(logits=torch.randn(4, 100, device="cuda"), u=torch.full((4,), 0.5, device="cuda"),
+             temperature=torch.ones(4, device="cuda"), top_p=torch.full((4,), 0.9, device="cuda"),
+             min_p=torch.zeros(4, device="cuda"), logp=torch.zeros(4, device="cuda"))
+    with fwd.dual_level():
+        def dual(t):
+            return fwd.make_dual(t.detach().clone(), torch.ones_like(t))
+
+        for kw in (dict(q=dual(x)), dict(k=dual(x)), dict(freq=dual(a["freq"])), dict(q_norm=dual(a["norm"])),
+                   dict(k_norm=dual(a["norm"])), dict(q_out=dual(q_out))):
+            args = dict(q=x, k=x, pos=a["pos"], freq=a["freq"], q_norm=a["norm"], k_norm=a["norm"])
+            args.update(kw)
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                tk.kv_rotate(**args)
+        for kw in (dict(k_new=dual(x)), dict(v_new=dual(x)), dict(freq=dual(a["freq"])), dict(k_norm=dual(a["norm"])),
+                   dict(q=dual(x)), dict(q_norm=dual(a["norm"])), dict(q_out=dual(q_out))):
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                appending(tk, a, **kw)
+        for name in s:
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                tk.sample_rows(**{**s, name: dual(s[name])})
+        # What has no tangent runs; so does everything where forward mode is off.
+        tk.kv_rotate(x, x, a["pos"], a["freq"])
+        both = dual(s["logits"])
+        with torch.inference_mode():
+            tk.sample_rows(**{**s, "logits": both})
+        tk.sample_rows(**{**s, "logits": fwd.unpack_dual(both).primal})

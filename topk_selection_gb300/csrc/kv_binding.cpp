@@ -8,6 +8,7 @@
 // to 15 us a call), so it is done here.  The library itself stays free of
 // torch: it is loaded by ctypes, which hands over its functions' addresses.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -396,6 +397,16 @@ void check_followed(const char* name, const char* of, std::initializer_list<PyOb
                                           " require grad: outputs cannot be given then");
 }
 
+// Refuses a tangent, which would get lost as well: the operators have no
+// derivatives in forward mode either.
+void check_tangents(const char* name, std::initializer_list<PyObject*> tensors) {
+    if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+    for (PyObject* o : tensors)
+        if (o != Py_None && THPVariable_Unpack(o)._fw_grad(0).defined())
+            raise(PyExc_NotImplementedError, std::string(name) + " has no derivative in forward mode, and a tensor has a "
+                                                                 "tangent: unpack it first");
+}
+
 void no_backward(const char* name, std::initializer_list<PyObject*> read, std::initializer_list<const at::Tensor*> made) {
     torch::autograd::variable_list from;
     for (PyObject* o : read)
@@ -444,6 +455,7 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rotation rotation(a[3], a[4], a[5], a[6], a[7], type, device, q.defined() ? q.size(1) : 0,
                                 k.defined() ? k.size(1) : 0, dim);
         const Stream s(a[10], device.index());
+        check_tangents("kv_rotate", {a[0], a[1], a[3], a[4], a[5], a[8], a[9]});
         check_written("kv_rotate", {a[8], a[9]});
         check_followed("kv_rotate", "q, k, freq or the norms", {a[0], a[1], a[3], a[4], a[5]}, {a[8], a[9]});
         const at::Tensor q_out = q.defined() ? rotated(a[8], "q_out", q) : at::Tensor();
@@ -490,6 +502,8 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rotation rotation(a[6], a[15], a[11], a[12], a[13], c.type, c.device, q.defined() ? q.size(1) : 0,
                                 c.c.heads, c.c.dim);
         const Stream s(a[17], c);
+        check_tangents("kv_append_rotated",
+                       {a[0], a[1], a[4], a[5], a[6], a[8], a[11], a[14], a[15], a[16]});
         check_written("kv_append_rotated", {a[0], a[1], a[8], a[16]});
         check_followed("kv_append_rotated", "q, freq or q_norm", {a[6], a[14], a[15]}, {a[16]});
         const at::Tensor q_out = q.defined() ? rotated(a[16], "q_out", q) : at::Tensor();
@@ -553,8 +567,10 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Stream s(a[8], device.index());
         if (a[6] != Py_None) vector(a[6], "token", at::kInt);
         if (a[7] != Py_None) vector(a[7], "logp", at::kFloat);
-        check_written("sample_rows", {a[7]});
         const std::initializer_list<PyObject*> read = {a[0], a[1], temperature, top_p, min_p};
+        check_tangents("sample_rows", read);
+        check_tangents("sample_rows", {a[7]});
+        check_written("sample_rows", {a[7]});
         check_followed("sample_rows", "the logits, u or parameters", read, {a[7]});
         const at::Tensor token = a[6] != Py_None ? THPVariable_Unpack(a[6])
                                                  : at::Tensor(at::detail::empty_cuda({rows}, at::kInt, device, std::nullopt));
