@@ -440,7 +440,8 @@ struct topk_kv_heads {
  *   q, k      inputs, either may be absent; q_out, k_out: their results, of as
  *             many heads.  An output may be its own input (the same address
  *             and strides); otherwise it overlaps neither input nor the other
- *             output (all may lie in one array of rows of tokens), nor itself.
+ *             output, nor itself.  All may lie in one array, in rows of tokens
+ *             where each has columns of its own, or in rows of heads.
  *
  * Device pointers; the call only enqueues, one launch.
  */

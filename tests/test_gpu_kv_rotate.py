@@ -405,3 +405,48 @@ def test_append_refusals(tk):
     out = call(q=x.clone().requires_grad_())
     with pytest.raises(RuntimeError, match="not implemented"):
         out.float().sum().backward()
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 17])
+@pytest.mark.parametrize("heads,parts", [(5, 3), (4, 4), (1, 3)])
+def test_in_place_where_heads_lie_between_one_another(tk, tokens, heads, parts):
+    """A projection that has each head's query, key and value side by side: q, k and v share every row of tokens, and no
+    element."""
+    full = torch.randn(tokens, heads, parts, 64, generator=gen(40)).to(F16)
+    there = full.cuda()
+    q, k, v = (there[:, :, i] for i in range(3))
+    tk.kv_rotate(q, k, torch.arange(tokens, dtype=torch.int32).cuda(), freqs(32).cuda(), q_out=q, k_out=k)
+    want, tol = _rotate.rotate(full[:, :, :2].reshape(tokens, -1, 64), np.arange(tokens), freqs(32))
+    _rotate.close(there[:, :, :2].reshape(tokens, -1, 64), want, tol)
+    assert torch.equal(there[:, :, 2:].cpu(), full[:, :, 2:])
+    # On the way to the pages, the queries in place.
+    cache = _kv.Cache([9], heads, 64, 16, F16, "head", room=tokens, seed=41)
+    kp, vp, table, lens = cache.dev()
+    there = full.cuda()
+    q, k, v = (there[:, :, i] for i in range(3))
+    tk.kv_append_rotated(kp, vp, table, lens, k, v, freqs(32).cuda(),
+                         starts=torch.tensor([0, tokens], dtype=torch.int32).cuda(), q=q, q_out=q)
+    at = 9 + np.arange(tokens)
+    want, tol = _rotate.rotate(full[:, :, 0], at, freqs(32))
+    _rotate.close(there[:, :, 0], want, tol)
+    assert torch.equal(there[:, :, 1:].cpu(), full[:, :, 1:])
+    want, tol = _rotate.rotate(full[:, :, 1], at, freqs(32))
+    for i in range(tokens):
+        p, o = cache.table[0, (9 + i) // 16].item(), (9 + i) % 16
+        _rotate.close(kp[p, o], want[i], tol[i])
+        assert torch.equal(vp[p, o].cpu(), full[i, :, 2])
+
+
+def test_heads_that_meet_are_refused(tk):
+    """Rows of heads in which two tensors do share elements."""
+    full = torch.zeros(3, 4, 192 + 64, dtype=F16).cuda()
+    pos, f = torch.zeros(3, dtype=torch.int32).cuda(), freqs(32).cuda()
+    q = full[..., :64]
+    for first in (8, 32, 56, 200, 248):  # a head on from there, in these rows or into the next ones
+        k = full.view(-1)[first:].as_strided((3, 4, 64), (1024, 256, 1)) if first < 200 else \
+            full.view(-1).as_strided((2, 4, 64), (1024, 256, 1), first)
+        n = k.shape[0]
+        with pytest.raises(tk.TopKError):
+            tk.kv_rotate(q[:n], k, pos[:n], f, q_out=q[:n], k_out=k)
+    with pytest.raises(tk.TopKError):  # one token
+        tk.kv_rotate(q[:1], full[:1, :, 32:96], pos[:1], f, q_out=q[:1], k_out=full[:1, :, 32:96])

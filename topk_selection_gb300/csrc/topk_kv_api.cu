@@ -169,17 +169,22 @@ bool same(const topk_kv_heads& x, const topk_kv_heads& y) {
 }
 
 // Whether two tensors share no element: one ends before the other begins, or
-// both lie in rows of tokens of one array, in columns of their own.  Less than
-// that is not looked for.
+// both lie in rows of tokens of one array, in columns of their own, or in rows
+// of heads of one array.  Less than that is not looked for.
 bool apart(const topk_kv_heads& x, const topk_kv_heads& y, int tokens, int dim) {
     const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.data) - reinterpret_cast<uintptr_t>(x.data));
     const int64_t x_all = span(x, tokens, dim), y_all = span(y, tokens, dim);
     if (d >= 2 * x_all || -d >= 2 * y_all) return true;
     const int64_t row = x.stride[0], e = d / 2;
-    if (tokens < 2 || y.stride[0] != row || (d & 1)) return false;
-    const int64_t x_row = (x.heads - 1) * x.stride[1] + dim, y_row = (y.heads - 1) * y.stride[1] + dim;
-    const int64_t at = (e % row + row) % row;  // of y's row, behind the start of one of x's
-    return at >= x_row && at + y_row <= row;
+    if ((d & 1) || (tokens > 1 && y.stride[0] != row)) return false;
+    // In rows of n elements x has the first `has` from its start on, and y `wants` of the others.
+    auto beside = [e](int64_t n, int64_t has, int64_t wants) {
+        const int64_t at = (e % n + n) % n;
+        return at >= has && at + wants <= n;
+    };
+    if (tokens > 1 && beside(row, (x.heads - 1) * x.stride[1] + dim, (y.heads - 1) * y.stride[1] + dim)) return true;
+    const int64_t head = x.heads > 1 ? x.stride[1] : y.stride[1];
+    return (y.heads == 1 || y.stride[1] == head) && (tokens == 1 || row % head == 0) && beside(head, dim, dim);
 }
 
 // A tensor that is read; `written`: one whose heads do not lie in one another.
