@@ -392,3 +392,18 @@ def test_limits_of_the_list(tk, ties):
     for kw in (dict(temperature=0.0), dict(top_k=ties), dict(top_k=ties - 1), dict(top_k=ties + 1), dict(min_p=0.9),
                dict(top_k=512), dict(top_k=513), dict(top_p=0.3), dict()):
         check(tk, x, u, **kw)
+
+
+def test_temperatures_below_the_types_range(tk):
+    """A number that 32 bits round to 0 is above 0 all the same: equal best entries take turns, with 1e-30 as with 1e-60."""
+    x = torch.full((4, 1000), -1.0)
+    x[:, [5, 70, 900]] = 2.0
+    u = torch.tensor([0.0, 0.4, 0.9, 0.99])
+    for t in (1e-30, 1e-45, 1e-50, 1e-300):
+        token, logp = tk.sample_rows(x.cuda(), u.cuda(), temperature=t)
+        assert token.tolist() == [5, 70, 900, 900]
+        assert torch.allclose(logp.cpu(), torch.full((4,), -np.log(3.0), dtype=F32), atol=2.0 ** -18)
+    token, logp = tk.sample_rows(x.cuda(), u.cuda(), temperature=0.0)
+    assert token.tolist() == [5] * 4 and logp.tolist() == [0.0] * 4
+    with pytest.raises(ValueError):
+        tk.sample_rows(x.cuda(), u.cuda(), temperature=-1e-50)

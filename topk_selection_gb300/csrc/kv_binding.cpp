@@ -563,7 +563,12 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
         else p.top_k = integer(a[3]);
         PyObject* const top_p = parameter(a[4], "top_p", &p.top_p, &p.top_ps);
         PyObject* const min_p = parameter(a[5], "min_p", &p.min_p, &p.min_ps);
-        if (!p.temperatures && !(p.temperature >= 0)) raise(PyExc_ValueError, "temperature must not be negative");
+        if (!p.temperatures) {
+            const double given = number(a[2]);
+            if (!(given >= 0)) raise(PyExc_ValueError, "temperature must not be negative");
+            // One above 0 stays above 0 in 32 bits: 0 has another meaning, and less than 2^-60 counts as that.
+            if (given > 0) p.temperature = std::max(p.temperature, 0x1p-60f);
+        }
         const Stream s(a[8], device.index());
         if (a[6] != Py_None) vector(a[6], "token", at::kInt);
         if (a[7] != Py_None) vector(a[7], "logp", at::kFloat);
