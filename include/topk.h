@@ -396,8 +396,9 @@ int topk_kv_evict(const struct topk_kv_cache* cache, const struct topk_kv_rows* 
  * and then for each pair p of them, (a, b), at position n
  *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = n * freq[p].
  * Elements that belong to no pair stay as they are.  All in float32 (squares
- * past its range are infinite, and the head then 0), rounded once at the end; an angle is right to 2^-32 turns and 2^-22 of the turns of
- * position 2^31, whatever the position.
+ * past its range are infinite, and the head then 0; squares below it are 0),
+ * rounded once at the end.  The angle at position n is right to 2^-32 turns and
+ * |n| (1 + |freq| / 2) 2^-64 turns besides.
  *
  *   freq      float32[pairs], device memory: radians per position, of either
  *             sign, below 2^16.
@@ -504,7 +505,7 @@ int topk_kv_append_rotated(const struct topk_kv_cache* cache, const struct topk_
  *
  *   logits   row r at r * stride elements, cols of them side by side, of
  *            dtype TOPK_KV_F16, TOPK_KV_BF16 or TOPK_SAMPLE_F32, aligned to
- *            their size; cols at most 2^21.
+ *            their size; stride not below cols, cols at most 2^21.
  *   sampling one value of each parameter for all rows, or, where the pointer
  *            is not null, an array of one per row.  The values are checked
  *            here (TOPK_ERR_INVALID_ARG: a negative temperature, NaN).

@@ -522,7 +522,8 @@ def kv_append_rotated(k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch
     Arguments are kv_append's and kv_rotate's.  Token i of sequence b is at
     position next_pos[b] + i, or, without next_pos, lens[b] + i: once a cache
     has been evicted from, positions run ahead of the slots.  next_pos may come
-    without pos.  Like kv_append it has no gradient: it warns where k_new, v_new,
+    without pos.  Rows of q_out behind the last sequence's tokens are not
+    written.  Like kv_append it has no gradient: it warns where k_new, v_new,
     k_norm or freq require grad, and a backward pass that reaches q_out raises."""
     got = _kv.append_rotated(k_pages, v_pages, table, lens, k_new, v_new, freq, starts, weight, pos, next_pos, k_norm,
                              eps, pairing, q, q_norm, q_out, _kv_stream(stream))

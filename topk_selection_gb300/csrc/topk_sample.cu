@@ -34,9 +34,10 @@
 // us, and there are 3 of them for top_k, 6 for top_p) and instructions, 20 an
 // element for 3 and 4; HBM only where nothing but 1 is done.  Measured: one row
 // of 131072 (bfloat16, top_k 50, top_p 0.95) 13 us; 256 of 160000 the same 36 us
-// (2.2 TB/s); 64 of 131001 float32 with top_p 0.95 93 to 105 us (some rows need
-// the exact pass); 128 of 32768, nothing cut off, 33 to 36 us; 512 of 262144
-// float32 with min_p 288 us (1.9 TB/s).
+// (2.2 TB/s), with an array of top_k 76 us, with temperature 0 50 us, with top_k
+// 500 or 1000 alone 252 and 323 us; 64 of 131001 float32 with top_p 0.95 91 to
+// 105 us (some rows need the exact pass); 128 of 32768, nothing cut off, 33 to
+// 38 us; 512 of 262144 float32 with min_p 285 to 293 us (1.9 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,7 +57,7 @@ namespace topk {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;  // 64 registers a thread: what spills, spills between passes (64 rows with top_p: 96 us, 102 with three blocks)
+constexpr int kBlocksPerSm = 4;  // 64 registers a thread, and spills (64 rows with top_p: 96 us, 102 with three blocks)
 constexpr int kBins = 64;
 constexpr int kList = 512;          // elements that a list has room for (with 1024, 114 us instead of 93 for 64 rows with top_p)
 constexpr int kMostBlocks = 8;      // of a cluster
@@ -1241,10 +1242,12 @@ template <Type kType>
 cudaError_t launch(SampleArgs& a, int device, int sms, cudaStream_t s) {
     auto kernel = sample_rows_kernel<kType>;
     // Blocks of a row: 8192 elements each at least, and as many as fill the
-    // SMs four times over, or once (four blocks fit an SM) where few elements
-    // are looked at again, and blocks do little but read (256 rows of 160000
-    // with top_k 50: 36 us, 73 with more; 512 of 262144 with min_p: 291 us, 470
-    // with fewer).
+    // SMs four times over, or once where few elements are looked at again, and
+    // blocks do little but read (256 rows of 160000 with top_k 50: 36 us, 76
+    // with more; 512 of 262144 with min_p: 291 us, 470 with fewer).  Of an array
+    // of top_k nothing is known here.  Four blocks fit an SM as long as a row's
+    // blocks have 19 rounds at most (20.2 + 16 KB, and one for each round); 33
+    // rounds, as of 131072 float32 in one block, leave room for three.
     const bool light = !a.p.top_ks && a.p.top_k > 0 && a.p.top_k <= kMostFew;
     int blocks = 1;
     while (blocks < kMostBlocks && a.cols / (2 * blocks) >= 8192 &&
@@ -1254,7 +1257,7 @@ cudaError_t launch(SampleArgs& a, int device, int sms, cudaStream_t s) {
     // A row has a vector more at most than its elements fill.
     const int vectors = (a.cols + Logit<kType>::kMany - 1) / Logit<kType>::kMany + 1, parts = blocks * kWarps;
     a.rounds = ((vectors + parts - 1) / parts + 32 * kGroup - 1) / (32 * kGroup);
-    // 32 rounds are the most that kMaxCols take.
+    // The most that kMaxCols take: 65 rounds of float32, 33 of 16 bits.
     constexpr int kMostRounds = ((kMaxCols / Logit<kType>::kMany + 1) / (kMostBlocks * kWarps) + 32 * kGroup) / (32 * kGroup);
     const int smem = (2 * kCells + a.rounds * kThreads) * 4;
     static std::atomic<unsigned long long> allowed{0};
