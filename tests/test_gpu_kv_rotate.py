@@ -450,3 +450,20 @@ def test_heads_that_meet_are_refused(tk):
             tk.kv_rotate(q[:n], k, pos[:n], f, q_out=q[:n], k_out=k)
     with pytest.raises(tk.TopKError):  # one token
         tk.kv_rotate(q[:1], full[:1, :, 32:96], pos[:1], f, q_out=q[:1], k_out=full[:1, :, 32:96])
+
+
+def test_outputs_that_are_no_tensors_are_refused(tk):
+    """Before anything is asked of them, with gradients on and off."""
+    x = torch.zeros(2, 2, 64, dtype=F16).cuda()
+    pos, f = torch.zeros(2, dtype=torch.int32).cuda(), freqs(32).cuda()
+    cache = _kv.Cache([9, 3], 2, 64, 16, F16, "head", room=4, seed=42)
+    k, v, table, lens = cache.dev()
+    for bad in (5, "q", [x], x.cpu().numpy(), object()):
+        for mode in (torch.enable_grad(), torch.no_grad()):
+            with mode:
+                with pytest.raises(TypeError, match="q_out must be a torch.Tensor"):
+                    tk.kv_rotate(x, None, pos, f, q_out=bad)
+                with pytest.raises(TypeError, match="k_out must be a torch.Tensor"):
+                    tk.kv_rotate(x, x, pos, f, k_out=bad)
+                with pytest.raises(TypeError, match="q_out must be a torch.Tensor"):
+                    tk.kv_append_rotated(k, v, table, lens, x, x, f, q=x, q_out=bad)

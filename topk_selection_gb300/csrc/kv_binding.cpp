@@ -455,11 +455,12 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rotation rotation(a[3], a[4], a[5], a[6], a[7], type, device, q.defined() ? q.size(1) : 0,
                                 k.defined() ? k.size(1) : 0, dim);
         const Stream s(a[10], device.index());
+        // Outputs are known to be tensors before anything is asked of them.
+        const at::Tensor q_out = q.defined() ? rotated(a[8], "q_out", q) : at::Tensor();
+        const at::Tensor k_out = k.defined() ? rotated(a[9], "k_out", k) : at::Tensor();
         check_tangents("kv_rotate", {a[0], a[1], a[3], a[4], a[5], a[8], a[9]});
         check_written("kv_rotate", {a[8], a[9]});
         check_followed("kv_rotate", "q, k, freq or the norms", {a[0], a[1], a[3], a[4], a[5]}, {a[8], a[9]});
-        const at::Tensor q_out = q.defined() ? rotated(a[8], "q_out", q) : at::Tensor();
-        const at::Tensor k_out = k.defined() ? rotated(a[9], "k_out", k) : at::Tensor();
         topk_kv_heads h[4] = {};
         if (q.defined()) {
             h[0] = heads_of(q, "q");
@@ -502,11 +503,11 @@ PyObject* append_rotated(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rotation rotation(a[6], a[15], a[11], a[12], a[13], c.type, c.device, q.defined() ? q.size(1) : 0,
                                 c.c.heads, c.c.dim);
         const Stream s(a[17], c);
+        const at::Tensor q_out = q.defined() ? rotated(a[16], "q_out", q) : at::Tensor();
         check_tangents("kv_append_rotated",
                        {a[0], a[1], a[4], a[5], a[6], a[8], a[11], a[14], a[15], a[16]});
         check_written("kv_append_rotated", {a[0], a[1], a[8], a[16]});
         check_followed("kv_append_rotated", "q, freq or q_norm", {a[6], a[14], a[15]}, {a[16]});
-        const at::Tensor q_out = q.defined() ? rotated(a[16], "q_out", q) : at::Tensor();
         if (followed({a[4], a[5], a[6], a[11]}) &&
             PyErr_WarnEx(PyExc_UserWarning,
                          "kv_append_rotated has no gradient: none will reach k_new, v_new, freq and k_norm", 2) != 0)
